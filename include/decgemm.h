@@ -59,7 +59,8 @@ extern "C" {
 #define DEC_ETIMEOUT     -4  /* a bounded device-side wait gave up */
 #define DEC_ENOMEM       -5  /* the workspace could not be allocated */
 #define DEC_ENODEV       -6  /* no sm_103 device is current */
-#define DEC_EBOUNDS      -7  /* a device-side index check failed (DEC_DEBUG builds only) */
+#define DEC_EBOUNDS      -7  /* a device-side index check failed (DEC_DEBUG builds), or a paged-cache
+                                call met a length, page or sequence out of range */
 
 /* Kernel regimes reported by dec_last_choice (low 8 bits). */
 #define DEC_REGIME_NONE   0
@@ -239,7 +240,7 @@ const char* dec_strerror(int code);
  * then read and clear the device status words that kernels set when a bounded
  * wait gives up: the library's own and the one in dec_linear_noalloc's fixed
  * array. Returns DEC_OK, DEC_ETIMEOUT, or DEC_ECUDA if the synchronisation
- * itself failed. Allocates nothing: in a process that has only called
+ * itself failed (DEC_EBOUNDS as described there). Allocates nothing: in a process that has only called
  * dec_linear_noalloc it sets up no workspace, stream or event.
  */
 int dec_sync_check(void* stream);
@@ -329,6 +330,141 @@ int dec_probe_end(double* total_ms, int* launches);
  * inside a capture). Does not update dec_last_choice or dec_launch_count.
  */
 int dec_linear_noalloc(const void* x, const void* W, void* y, int M, int N, int K, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged key/value cache: what stands between a layer's q|k|v projection
+ * and its o projection, and the management of the cache's pages. These calls
+ * are the library's own; the pages describe no counterpart (the layer they
+ * describe is taken without its attention core).
+ *
+ * A cache of one layer is pages of page_size positions, each holding
+ * [2][heads][page_size][dim] bf16: the keys of every key/value head, then the
+ * values. Row s of a page table lists the pages of sequence s in order; -1
+ * marks an unused entry. A sequence's positions are 0 .. kv_len-1, and a
+ * call's new tokens are always its last ones: kv_len counts them.
+ *
+ * Lengths, page numbers and sequence numbers are device data, read by the
+ * kernels (so that a captured graph follows them from step to step). One that
+ * is out of range never makes an access out of range: what it names is left
+ * out (or read as zeros), and dec_sync_check reports DEC_EBOUNDS.
+ */
+
+/* A layer's cache and the batch of sequences that a call works on. */
+typedef struct dec_kv_view {
+  void* cache;             /* device; 16-byte aligned */
+  int64_t page_stride;     /* elements from one page to the next (a multiple of 8) */
+  int32_t pages, heads;    /* pages of the pool; key/value heads */
+  int32_t page_size, dim;  /* 16, 32, 64, 128 or 256 positions; 64 or 128 elements of a head */
+  const int32_t* table;    /* device [table_rows][table_stride] */
+  int64_t table_stride;    /* elements from one row to the next */
+  int32_t width;           /* entries of a row */
+  int32_t table_rows;      /* rows of table, and entries of kv_len */
+  const int32_t* rows;     /* device [batch]: the row (and kv_len entry) of each sequence of the
+                              batch; NULL: sequence b has row b */
+  const int32_t* cu_q;     /* device [batch+1]: sequence b's new tokens are cu_q[b] .. cu_q[b+1]-1 */
+  const int32_t* kv_len;   /* device [table_rows]: positions, the new tokens included */
+  int32_t batch;           /* 1 .. 1024 sequences; some may have no new token */
+  int32_t max_q;           /* the most new tokens of one sequence, as far as the caller knows: it
+                              chooses the kernel, not the result. 0: unknown */
+} dec_kv_view;
+
+/*
+ * kv_append -- norm and rotation of the new tokens' queries and keys, head by
+ * head, and the append of their keys and values to the cache, in one pass.
+ *
+ *   qkv  : [tokens, (q_heads + 2*heads)*dim] bf16, rows ldqkv elements apart: the
+ *          query heads, the key heads, the value heads (a fused projection's output)
+ *   wq, wk : [dim] bf16 norm weights of queries and keys; both NULL: no norm
+ *   rope : [rope_len, rot] fp32, for each position rot/2 cosines, then rot/2 sines
+ *   positions : optional [tokens] int32, the row of rope of each token; NULL: its
+ *          position in its sequence
+ *   q    : [tokens, q_heads*dim] bf16 output, rows ldq elements apart; may be qkv
+ *
+ * Per query or key head x:  y = x * rsqrt(mean(x^2) + eps) * w;  then on its
+ * first rot elements (a multiple of 16, at most dim) each pair (a, c) becomes
+ * (a cos - c sin, c cos + a sin), pairs being (i, i + rot/2), or (2i, 2i+1) with
+ * interleaved. fp32 throughout, rounded once to bf16. Values are copied. Token
+ * t of sequence b goes to position kv_len - (its new tokens) + t. Tokens past
+ * cu_q[batch] belong to no sequence and are left alone (a padded batch).
+ */
+int kv_append(const dec_kv_view* kv, const void* qkv, int64_t ldqkv, const void* wq, const void* wk,
+              float eps, const float* rope, int rope_len, int rot, int interleaved,
+              const int32_t* positions, void* q, int64_t ldq, int tokens, int q_heads, void* stream);
+
+/*
+ * kv_attention -- attention of the new tokens over the cache.
+ *
+ *   q   : [tokens, q_heads*dim] bf16, rows ldq elements apart; q_heads a multiple of
+ *         heads, at most 64 query heads per key head; query head h reads key head
+ *         h / (q_heads/heads)
+ *   out : [tokens, q_heads*dim] bf16, rows ldo elements apart
+ *   lse : optional [tokens, q_heads] fp32
+ *
+ * Per token at position i and head, over the positions j it sees (j <= i, and
+ * j > i - window if window > 0):
+ *   s_j = scale * q·k_j;  lse = log sum_j exp(s_j);  out = sum_j exp(s_j - lse) v_j
+ * Scores, maximum, sum and output are fp32; the weights enter the product with
+ * the values as bf16; out is rounded once. A token that sees nothing (its
+ * position is negative: kv_len below its chunk) gets out = 0, lse = -inf. What
+ * lies past a sequence's end in its last page is never used, whatever it is.
+ * The result is the same from run to run. Rows of tokens past cu_q[batch] are
+ * left alone. Uses the library's workspace: order such calls on one stream.
+ */
+int kv_attention(const dec_kv_view* kv, const void* q, int64_t ldq, void* out, int64_t ldo, float* lse,
+                 int tokens, int q_heads, float scale, int window, void* stream);
+
+/* kv_last_attention -- DEC_REGIME_* of this thread's last kv_attention call. */
+int kv_last_attention(void);
+
+/* The pages of all layers of a cache, and the state of its sequences. */
+typedef struct dec_kv_pool {
+  void* data;              /* device; 16-byte aligned */
+  int64_t layer_stride;    /* bytes from one layer's pages to the next's */
+  int64_t page_stride;     /* bytes from one page to the next */
+  int64_t page_bytes;      /* bytes of a page of one layer; all three multiples of 16 */
+  int32_t layers, pages;   /* pages: at most 2^19 */
+  int32_t page_size;       /* positions of a page, a power of two */
+  int32_t* refs;           /* device [pages]: table entries that hold a page; 0: free */
+  int32_t* table;          /* device [seqs][table_stride]: pages of a sequence, -1 past its last */
+  int64_t table_stride;
+  int32_t width;           /* entries of a table row */
+  int32_t* lens;           /* device [seqs]: positions of a sequence */
+  int32_t seqs;
+  int32_t* info;           /* optional device [3], written by kv_resize, kv_free, kv_fork and
+                              kv_compact: pages that were lacking (0: done), pages free after
+                              the call, pages copied */
+} dec_kv_pool;
+
+/*
+ * kv_resize -- set the lengths of n sequences (1 .. 1024, all different): pages
+ * past the new length are given back, pages up to it are taken. New pages are
+ * the lowest free ones, in the order of the requests. A sequence cut inside a
+ * page that others hold too gets a copy of that page. All or nothing: if the
+ * free pages do not suffice nothing changes and info[0] says how many are
+ * lacking. A request that the table cannot hold or that names no sequence is
+ * left out (DEC_EBOUNDS from dec_sync_check).
+ *
+ * kv_free -- kv_resize to length 0.
+ *
+ * kv_fork -- sequence dst[i] becomes a copy of src[i] (no sequence both a source
+ * and a copy; copies all different): it shares the full pages and gets a copy
+ * of the last one if that is partly filled, so that both can be appended to.
+ * Pages that dst[i] held are given back. All or nothing, as kv_resize.
+ *
+ * Pages that a call gives back are free from the next call on.
+ */
+int kv_resize(const dec_kv_pool* pool, const int32_t* seqs, const int32_t* lens, int n, void* stream);
+int kv_free(const dec_kv_pool* pool, const int32_t* seqs, int n, void* stream);
+int kv_fork(const dec_kv_pool* pool, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* kv_copy -- copy page src[i] to page dst[i] in every layer, i < n (device lists; no
+ * page both read and written, none written twice). */
+int kv_copy(const dec_kv_pool* pool, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* kv_compact -- move pages so that the n pages in use are pages 0 .. n-1: those at or
+ * past n go, in order, to the free places before n; table and refs follow. */
+int kv_compact(const dec_kv_pool* pool, void* stream);
 
 /* dec_shutdown -- free the workspace, side stream and events of the current device. */
 void dec_shutdown(void);

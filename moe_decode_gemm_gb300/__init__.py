@@ -35,6 +35,8 @@ EXPORTS = [
     "dec_strerror", "dec_sync_check", "dec_set_wait_timeout_ns", "dec_selftest_timeout",
     "dec_launch_count", "dec_probe_begin", "dec_probe_end", "dec_shutdown", "dec_version",
     "dec_linear_noalloc", "dec_debug_build", "dec_debug_check_site",
+    "kv_append", "kv_attention", "kv_last_attention", "kv_resize", "kv_free", "kv_fork", "kv_copy",
+    "kv_compact",
 ]
 
 _lib = None
@@ -74,6 +76,7 @@ def use_library(path):
 def _configure(L):
     """Declare the C signatures of every exported function on a loaded library."""
     P, I, SZ, LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+    F = ctypes.c_float
     sig = {
         "dec_linear": (I, [P, P, P, I, I, I, P]),
         "dec_linear_residual": (I, [P, P, P, P, I, I, I, P]),
@@ -99,6 +102,14 @@ def _configure(L):
         "dec_debug_build": (I, []),
         "dec_debug_check_site": (I, [ctypes.POINTER(ctypes.c_int),
                                      ctypes.POINTER(ctypes.c_longlong)]),
+        "kv_append": (I, [P, P, LL, P, P, F, P, I, I, I, P, P, LL, I, I, P]),
+        "kv_attention": (I, [P, P, LL, P, LL, P, I, I, F, I, P]),
+        "kv_last_attention": (I, []),
+        "kv_resize": (I, [P, P, P, I, P]),
+        "kv_free": (I, [P, P, I, P]),
+        "kv_fork": (I, [P, P, P, I, P]),
+        "kv_copy": (I, [P, P, P, I, P]),
+        "kv_compact": (I, [P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -416,3 +427,6 @@ def shutdown():
 
 
 PROBE_EXPERT_W13, PROBE_EXPERT_W2, PROBE_LINEAR, PROBE_ROUTER, PROBE_COMBINE = 0, 1, 2, 3, 4
+
+from .paged import (KVPool, PagedKV, kv_append, kv_attention, kv_compact, kv_copy,  # noqa: E402
+                    kv_fork, kv_free, kv_resize, last_attention)

@@ -23,8 +23,7 @@ namespace dg {
 static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 static std::once_flag g_encode_once;
 
-bool make_tmap(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
-               bool l2_promote_256, uint64_t ld) {
+static bool load_encode() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -33,7 +32,12 @@ bool make_tmap(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, 
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
-  if (!g_encode || rows == 0 || cols == 0) return false;
+  return g_encode != nullptr;
+}
+
+bool make_tmap(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
+               bool l2_promote_256, uint64_t ld) {
+  if (!load_encode() || rows == 0 || cols == 0) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {(ld ? ld : cols) * 2};  // bytes between rows
   cuuint32_t box[2] = {64, box_rows};
@@ -53,15 +57,7 @@ bool make_tmap(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, 
 // TMA instruction for what would take `kboxes` 2-D boxes.
 bool make_tmap_slab(CUtensorMap* map, const void* W, uint64_t N, uint64_t K, uint32_t rows,
                     uint32_t kboxes, uint64_t ld) {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (!g_encode || N == 0 || K == 0 || (K % 64) != 0) return false;
+  if (!load_encode() || N == 0 || K == 0 || (K % 64) != 0) return false;
   if (ld == 0) ld = K;
   if (ld < K || (ld % 8) != 0) return false;
   cuuint64_t dims[3] = {64, N, K / 64};
@@ -72,6 +68,20 @@ bool make_tmap_slab(CUtensorMap* map, const void* W, uint64_t N, uint64_t K, uin
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_kv(CUtensorMap* map, const KvView& v, int box_rows) {
+  if (!load_encode()) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)v.dim, (cuuint64_t)v.page, (cuuint64_t)v.hkv * 2,
+                        (cuuint64_t)v.pages};
+  cuuint64_t strides[3] = {(cuuint64_t)v.dim * 2, (cuuint64_t)v.dim * 2 * v.page,
+                           (cuuint64_t)v.page_stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.cache, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -90,6 +100,7 @@ struct DevState {
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
   int* status = nullptr;                  // device status word
   Buf ws_main, ctr_main, ws_side, ctr_side;
+  Buf kv, ctr_kv;                         // paged cache: partial tiles and page lists; counters
   Buf moe;                                // routing tables + intermediates
   int moe_M = 0, moe_E = 0, moe_k = 0, moe_I = 0, moe_H = 0, moe_L = 0;
   MoeBufs mb = {};
@@ -570,6 +581,28 @@ static int moe_impl(const void* x, const void* Wr, const void* W13, const void* 
   return counted(launch_combine(cx, s->mb, shared, res, out, M, H, topk));
 }
 
+int kv_context(void* stream, size_t bytes, size_t ctrs, Ctx* cx, void** ws, int** ctr) {
+  DevState* s = nullptr;
+  int rc = get_dev(&s);
+  if (rc) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (bytes && (rc = ensure(s->kv, bytes, st))) return rc;
+  if (ctrs && (rc = ensure(s->ctr_kv, ctrs * sizeof(int), st))) return rc;
+  *cx = make_ctx(s, st);
+  cx->ws_len = (long long)(s->kv.bytes / sizeof(float));
+  cx->ctr_len = (long long)(s->ctr_kv.bytes / sizeof(int));
+  if (ws) *ws = s->kv.p;
+  if (ctr) *ctr = static_cast<int*>(s->ctr_kv.p);
+  return DEC_OK;
+}
+
+int kv_sms() {
+  DevState* s = nullptr;
+  return get_dev(&s) ? 0 : s->sms;
+}
+
+void count_launches(int n) { g_launches.fetch_add(n); }
+
 }  // namespace dg
 
 using namespace dg;
@@ -658,7 +691,7 @@ const char* dec_strerror(int code) {
     case DEC_ETIMEOUT: return "a bounded device-side wait gave up";
     case DEC_ENOMEM: return "workspace allocation failed";
     case DEC_ENODEV: return "no sm_103 (GB300) device is current";
-    case DEC_EBOUNDS: return "a device-side index check failed (DEC_DEBUG build)";
+    case DEC_EBOUNDS: return "a device-side index check failed";
     default: return "unknown error code";
   }
 }
@@ -702,6 +735,7 @@ int dec_sync_check(void* stream) {
     cudaMemset(s->status, 0, sizeof(int));
     if (s->ctr_main.p) cudaMemset(s->ctr_main.p, 0, s->ctr_main.bytes);
     if (s->ctr_side.p) cudaMemset(s->ctr_side.p, 0, s->ctr_side.bytes);
+    if (s->ctr_kv.p) cudaMemset(s->ctr_kv.p, 0, s->ctr_kv.bytes);
     if (s->mb.route_ctr) cudaMemset(s->mb.route_ctr, 0, sizeof(int));
     cudaMemset(s->status, 0, sizeof(words));
     cudaDeviceSynchronize();
@@ -779,7 +813,7 @@ void dec_shutdown(void) {
   if ((int)g_dev.size() <= d || !g_dev[d].init) return;
   DevState& s = g_dev[d];
   cudaDeviceSynchronize();
-  Buf* bufs[] = {&s.ws_main, &s.ctr_main, &s.ws_side, &s.ctr_side, &s.moe};
+  Buf* bufs[] = {&s.ws_main, &s.ctr_main, &s.ws_side, &s.ctr_side, &s.kv, &s.ctr_kv, &s.moe};
   for (Buf* b : bufs) {
     if (b->p) cudaFree(b->p);
     b->p = nullptr;

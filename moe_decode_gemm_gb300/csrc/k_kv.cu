@@ -1,0 +1,603 @@
+// k_kv.cu -- what goes into a paged cache and how its pages are managed: the
+// norm and rotation of a step's queries and keys with the append of its keys
+// and values, and the calls that change, fork, copy and compact the pages of
+// a cache of several layers.
+#include "launch.h"
+#include "launch_util.cuh"
+#include "paged.cuh"
+
+namespace dg {
+
+// ------------------------------------------------------------------ append
+//   y = x * rsqrt(mean(x^2) + eps) * w    per query and key head (w: wq or wk)
+//   (a, c) -> (a cos - c sin, c cos + a sin)   on the head's first rot elements,
+//   pairs (i, i + rot/2), or (2i, 2i + 1) interleaved
+// in fp32, rounded once to bf16; values are copied. Queries go to q, keys and
+// values to the places of their positions in the cache. Each head is read and
+// written once: bound by memory at many tokens, by the latency of one chain of
+// dependent loads (sequence, page, row of angles) at few.
+//
+// D/8 lanes hold a head, 8 elements each, so that the sum of squares is a few
+// shuffles and a pair's other half is in this lane or one shuffle away. A
+// thread has `U` heads' loads in flight before it looks up where they go.
+constexpr int kAppendThreads = 256;
+
+struct AppendArgs {
+  PagedArgs p;
+  const uint16_t* qkv;
+  const uint16_t* wq;
+  const uint16_t* wk;
+  const float* rope;
+  const int32_t* positions;
+  uint16_t* q;
+  uint16_t* cache;
+  long long ldqkv, ldq, page_stride;
+  int hq, rope_len, rot, interleaved;
+  float eps;
+};
+
+template <int D, int U>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  constexpr int LG = D / 8;                      // lanes of a head
+  constexpr int kGroups = kAppendThreads / LG;   // heads at a time
+  constexpr int kUnits = kGroups * U;            // heads of this CTA
+  extern __shared__ int s_cu[];                  // [batch + 1]
+  __shared__ int s_pos[kUnits], s_rope[kUnits], s_page[kUnits];
+  const int H = a.hq + 2 * a.p.hkv;
+  const int tid = threadIdx.x, g = tid / LG, l = tid % LG;
+  const long long unit0 = (long long)blockIdx.x * kUnits;
+  const long long units = (long long)a.p.tokens * H;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  uint4 x[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const long long u = unit0 + k * kGroups + g;
+    x[k] = make_uint4(0, 0, 0, 0);
+    if (u < units) {
+      const int tok = (int)(u / H), head = (int)(u - (long long)tok * H);
+      x[k] = *reinterpret_cast<const uint4*>(a.qkv + tok * a.ldqkv + head * D + l * 8);
+    }
+  }
+  for (int b = tid; b <= a.p.batch; b += kAppendThreads) s_cu[b] = __ldg(a.p.cu_q + b);
+  __syncthreads();
+  const int tok0 = (int)(unit0 / H);
+  const long long last = unit0 + kUnits < units ? unit0 + kUnits : units;
+  const int ntok = (int)((last - 1) / H) - tok0 + 1;
+  for (int t = tid; t < ntok; t += kAppendThreads) {
+    const int tok = tok0 + t;
+    int lo = 0, hi = a.p.batch - 1;  // the last sequence that begins at or before tok
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_cu[mid] <= tok) lo = mid;
+      else hi = mid - 1;
+    }
+    int pos = -1, page = -1, rp = -1;  // rp < 0: the token belongs to no sequence
+    if (s_cu[lo] <= tok && tok < s_cu[lo + 1]) {
+      const int row = paged_row(a.p, lo);
+      pos = paged_len(a.p, row) - s_cu[lo + 1] + tok;
+      if (row >= 0 && pos >= 0) {
+        page = __ldg(a.p.table + row * a.p.table_stride + (pos >> a.p.page_shift));
+        if (page < 0 || page >= a.p.pages) page = -1;
+      }
+      rp = a.positions ? __ldg(a.positions + tok) : (pos < 0 ? 0 : pos);
+      if (rp < 0 || rp >= a.rope_len) {
+        if (a.p.status) atomicOr(a.p.status, kStatusBounds);
+        rp = rp < 0 ? 0 : a.rope_len - 1;
+      }
+      if (page < 0 && a.p.status) atomicOr(a.p.status, kStatusBounds);
+    }
+    s_pos[t] = pos;
+    s_page[t] = page;
+    s_rope[t] = rp;
+  }
+  __syncthreads();
+
+  const int half = a.rot >> 1;
+  // the lanes of this head: heads of one warp may take different branches
+  const unsigned gmask = ((1u << LG) - 1) << (tid & 31 & ~(LG - 1));
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const long long u = unit0 + k * kGroups + g;
+    const bool live = u < units;
+    const int tok = live ? (int)(u / H) : tok0, head = live ? (int)(u - (long long)tok * H) : 0;
+    const int rp = s_rope[tok - tok0];
+    uint4 out = x[k];
+    if (head < a.hq + a.p.hkv) {
+      float y[8];
+      unpack8(x[k], y);
+      if (a.wq) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+#pragma unroll
+        for (int o = LG / 2; o; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o, LG);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        float w[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(head < a.hq ? a.wq : a.wk) + l), w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
+      }
+      const float* row = a.rope + (long long)(rp < 0 ? 0 : rp) * a.rot;
+      if (a.interleaved) {
+        if (l * 8 < a.rot) {
+          const float4 cs = __ldg(reinterpret_cast<const float4*>(row + l * 4));
+          const float4 sn = __ldg(reinterpret_cast<const float4*>(row + half + l * 4));
+          const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = y[2 * j], f = y[2 * j + 1];
+            y[2 * j] = e * c[j] - f * s[j];
+            y[2 * j + 1] = f * c[j] + e * s[j];
+          }
+        }
+      } else {
+        const bool second = l * 8 >= half;
+        const int other = l * 8 < a.rot ? (second ? l - half / 8 : l + half / 8) : l;
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = __shfl_sync(gmask, y[j], other, LG);
+        if (l * 8 < a.rot) {
+          const float4* cp = reinterpret_cast<const float4*>(row + l * 8 - (second ? half : 0));
+          const float4* sp = cp + half / 4;
+          const float sign = second ? 1.f : -1.f;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float4 cs = __ldg(cp + q), sn = __ldg(sp + q);
+            const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              y[q * 4 + j] = y[q * 4 + j] * c[j] + sign * (z[q * 4 + j] * s[j]);
+          }
+        }
+      }
+      out = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                       pack_bf16(y[6], y[7]));
+    }
+    if (!live || rp < 0) continue;
+    if (head < a.hq) {
+      *reinterpret_cast<uint4*>(a.q + tok * a.ldq + head * D + l * 8) = out;
+    } else {
+      const int page = s_page[tok - tok0], pos = s_pos[tok - tok0];
+      if (page >= 0)  // head - hq: key heads, then value heads, as the cache has them
+        *reinterpret_cast<uint4*>(a.cache + page * a.page_stride +
+                                  ((long long)(head - a.hq) * a.p.page + (pos & (a.p.page - 1))) * D +
+                                  l * 8) = out;
+    }
+  }
+}
+
+template <int D>
+static cudaError_t launch_append_d(const Ctx& cx, const AppendArgs& a) {
+  constexpr int kGroups = kAppendThreads / (D / 8);
+  const long long units = (long long)a.p.tokens * (a.hq + 2 * a.p.hkv);
+  const size_t smem = (size_t)(a.p.batch + 1) * 4;
+  // few heads: one per thread group, spread over the SMs; many: four loads in
+  // flight per thread
+  if (units <= 2LL * cx.sms * kGroups)
+    return launch_k(append_kernel<D, 1>, dim3((unsigned)((units + kGroups - 1) / kGroups)),
+                    dim3(kAppendThreads), smem, cx.stream, cx.pdl, a);
+  return launch_k(append_kernel<D, 4>, dim3((unsigned)((units + 4 * kGroups - 1) / (4 * kGroups))),
+                  dim3(kAppendThreads), smem, cx.stream, cx.pdl, a);
+}
+
+cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c) {
+  AppendArgs a = {};
+  a.p = paged_args(v, c.tokens, cx.status);
+  a.qkv = static_cast<const uint16_t*>(c.qkv);
+  a.wq = static_cast<const uint16_t*>(c.wq);
+  a.wk = static_cast<const uint16_t*>(c.wk);
+  a.rope = c.rope;
+  a.positions = c.positions;
+  a.q = static_cast<uint16_t*>(c.q);
+  a.cache = static_cast<uint16_t*>(v.cache);
+  a.ldqkv = c.ldqkv;
+  a.ldq = c.ldq;
+  a.page_stride = v.page_stride;
+  a.hq = c.hq;
+  a.rope_len = c.rope_len;
+  a.rot = c.rot;
+  a.interleaved = c.interleaved;
+  a.eps = c.eps;
+  return v.dim == 64 ? launch_append_d<64>(cx, a) : launch_append_d<128>(cx, a);
+}
+
+// ------------------------------------------------------------------ page state
+// refs[page] counts the table entries that hold a page; 0 is free. A call's
+// new pages are the lowest free ones, in the order of its requests: a rank
+// over refs and a prefix sum over the requests. One thread-block cluster does
+// the whole call: each CTA ranks a slice of refs, the slices' counts are
+// exchanged through distributed shared memory, and the cluster's barriers
+// separate reading refs, giving pages back and taking new ones. The state is
+// a few hundred KB at most, so that a call is bound by latency, not by bytes.
+constexpr int kPoolCtas = 8;
+constexpr int kPoolThreads = 1024;
+constexpr int kPoolWarps = kPoolThreads / 32;
+
+struct PoolArgs {
+  KvPool p;
+  const int32_t* seqs;  // resize: the sequences; fork: the copies (dst)
+  const int32_t* src;   // fork
+  const int32_t* len;   // resize: new lengths, null for 0
+  int n;
+  int32_t* pairs;       // [2 n] pages to copy: from (-1: none), to
+  int* status;
+};
+
+// Exclusive prefix of v over the CTA's threads; total in all threads.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int w = s_warp[lane];  // kPoolWarps == 32
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(~0u, w, o);
+    if (lane >= o) w += t;
+  }
+  total = __shfl_sync(~0u, w, 31);
+  const int before = __shfl_sync(~0u, w, warp ? warp - 1 : 0);
+  __syncthreads();
+  return inc - v + (warp ? before : 0);
+}
+
+// This thread's run of pages [first, first + per) and, in bits, which of them
+// are free (per <= 64).
+struct PageRun {
+  int first, count;
+  unsigned long long bits;
+  __device__ PageRun(const KvPool& p, uint32_t rank, bool want_free) {
+    const int per = (p.pages + kPoolCtas * kPoolThreads - 1) / (kPoolCtas * kPoolThreads);
+    const long long f = ((long long)rank * kPoolThreads + threadIdx.x) * per;
+    first = f < p.pages ? (int)f : p.pages;
+    count = p.pages - first < per ? p.pages - first : per;
+    bits = 0;
+    for (int k = 0; k < count; ++k)
+      if ((__ldcg(p.refs + first + k) <= 0) == want_free) bits |= 1ull << k;
+  }
+};
+
+template <bool FORK>
+__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
+    kv_change_kernel(const PoolArgs a) {
+  __shared__ int s_start[kMaxBatch + 1];  // new pages before each request
+  __shared__ int s_col[kMaxBatch];        // first table column that gets a new page
+  __shared__ int s_cow[kMaxBatch];        // page to copy into it, or -1
+  __shared__ int s_row[kMaxBatch];        // the sequence, or -1 (a request that is left out)
+  __shared__ int s_src[FORK ? kMaxBatch : 1];
+  __shared__ int s_old[kMaxBatch], s_new[kMaxBatch];  // columns held before, after
+  __shared__ int s_warp[32], s_cnt[kPoolCtas], s_rel[kPoolCtas], s_mine;
+  const KvPool& p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int mask = (1 << p.page_shift) - 1;
+  if (tid == 0) s_mine = 0;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  auto blocks = [&](int n) { return (int)(((long long)n + mask) >> p.page_shift); };
+  auto bad = [&] {
+    if (a.status) atomicOr(a.status, kStatusBounds);
+  };
+  auto length = [&](int s) -> int {  // a sequence's length, within its table row
+    const int n = __ldcg(p.lens + s);
+    const long long cap = (long long)p.width << p.page_shift;
+    return n < 0 ? 0 : (n > cap ? (int)cap : n);
+  };
+  auto entry = [&](int s, int col) -> int {
+    return __ldcg(p.table + (long long)s * p.table_stride + col);
+  };
+  auto is_page = [&](int pg) { return pg >= 0 && pg < p.pages; };
+
+  // request tid
+  int need = 0, cow = 0, newlen = 0;
+  if (tid < a.n) {
+    int row = __ldg(a.seqs + tid), from = -1, col = 0, nold = 0, nnew = 0;
+    if (row < 0 || row >= p.seqs) row = -1;
+    if (FORK) {
+      const int s = __ldg(a.src + tid);
+      if (s < 0 || s >= p.seqs || s == row) row = -1;
+      s_src[tid] = s;
+      if (row >= 0) {
+        newlen = length(s);
+        nold = blocks(length(row));
+        col = newlen >> p.page_shift;  // full pages are shared
+        nnew = blocks(newlen);
+        need = nnew - col;
+        if (need) from = entry(s, col);
+      }
+    } else {
+      newlen = a.len ? __ldg(a.len + tid) : 0;
+      if (newlen < 0 || newlen > ((long long)p.width << p.page_shift)) row = -1;
+      if (row >= 0) {
+        const int was = length(row);
+        nold = blocks(was);
+        nnew = blocks(newlen);
+        col = nold;
+        if (nnew > nold) need = nnew - nold;
+        if (newlen < was && (newlen & mask)) {
+          // the last page stays in part: if others hold it too, a page of its
+          // own, for what will be written after its end
+          const int pg = entry(row, nnew - 1);
+          if (is_page(pg) && __ldcg(p.refs + pg) > 1) {
+            from = pg;
+            col = nnew - 1;
+            need = 1;
+          }
+        }
+      }
+    }
+    if (row < 0) bad();
+    if (from >= 0 && !is_page(from)) {
+      bad();
+      from = -1;
+    }
+    cow = from >= 0;
+    s_row[tid] = row;
+    s_cow[tid] = from;
+    s_col[tid] = col;
+    s_old[tid] = nold;
+    s_new[tid] = nnew;
+  }
+  const PageRun run(p, rank, true);
+  int total, mine, copies;
+  const int start = block_scan(need, s_warp, total);
+  if (tid < a.n) s_start[tid] = start;
+  block_scan(cow, s_warp, copies);
+  const int before = block_scan(__popcll(run.bits), s_warp, mine);
+  if (tid < kPoolCtas) st_dsmem_s32(&s_cnt[rank], tid, mine);
+  cluster_sync_all();  // every CTA has read refs, lengths and the entries above
+
+  int offset = before, free_pages = 0;
+  for (int r = 0; r < kPoolCtas; ++r) {
+    if (r < (int)rank) offset += s_cnt[r];
+    free_pages += s_cnt[r];
+  }
+  const int lacking = total > free_pages ? total - free_pages : 0;
+  if (rank == 0 && tid < a.n && a.pairs && (!cow || lacking)) a.pairs[2 * tid] = -1;
+  const int wid = (int)rank * kPoolWarps + warp;
+  if (!lacking) {
+    if (FORK) {
+      for (int i = wid; i < a.n; i += kPoolCtas * kPoolWarps)
+        if (s_row[i] >= 0)
+          for (int c = lane; c < s_col[i]; c += 32) {
+            const int pg = entry(s_src[i], c);
+            if (is_page(pg)) atomicAdd(p.refs + pg, 1);
+            else bad();
+          }
+    }
+  }
+  if (FORK) cluster_sync_all();  // a page is added to before it is taken from
+  if (!lacking) {
+    int freed = 0;
+    auto release = [&](int pg) {
+      if (!is_page(pg)) bad();
+      else if (atomicSub(p.refs + pg, 1) == 1) ++freed;
+    };
+    for (int i = wid; i < a.n; i += kPoolCtas * kPoolWarps) {
+      const int row = s_row[i];
+      if (row < 0) continue;
+      int32_t* t = p.table + (long long)row * p.table_stride;
+      if (FORK) {
+        const int end = s_old[i] > s_new[i] ? s_old[i] : s_new[i];
+        for (int c = lane; c < end; c += 32) {
+          if (c < s_old[i]) release(__ldcg(t + c));
+          t[c] = c < s_col[i] ? entry(s_src[i], c) : -1;
+        }
+      } else {
+        for (int c = s_new[i] + lane; c < s_old[i]; c += 32) {
+          release(__ldcg(t + c));
+          t[c] = -1;
+        }
+        if (lane == 0 && s_cow[i] >= 0) release(s_cow[i]);
+      }
+    }
+    freed = __reduce_add_sync(~0u, freed);
+    if (lane == 0 && freed) atomicAdd(&s_mine, freed);
+  }
+  __syncthreads();
+  if (tid == 0) st_dsmem_s32(&s_rel[rank], 0, s_mine);
+  cluster_sync_all();
+  if (!lacking) {
+    if (rank == 0 && tid < a.n && s_row[tid] >= 0) p.lens[s_row[tid]] = newlen;
+    int r = offset;
+    for (unsigned long long m = run.bits; m && r < total; m &= m - 1, ++r) {
+      const int pg = run.first + __ffsll(m) - 1;
+      int lo = 0, hi = a.n - 1;  // the last request that starts at or before r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_start[mid] <= r) lo = mid;
+        else hi = mid - 1;
+      }
+      p.refs[pg] = 1;
+      p.table[(long long)s_row[lo] * p.table_stride + s_col[lo] + (r - s_start[lo])] = pg;
+      if (s_cow[lo] >= 0 && a.pairs) {
+        a.pairs[2 * lo] = s_cow[lo];
+        a.pairs[2 * lo + 1] = pg;
+      }
+    }
+  }
+  if (rank == 0 && tid == 0 && p.info) {
+    int freed = 0;
+    for (int r = 0; r < kPoolCtas; ++r) freed += s_rel[r];
+    p.info[0] = lacking;
+    p.info[1] = lacking ? free_pages : free_pages - total + freed;
+    p.info[2] = lacking ? 0 : copies;
+  }
+}
+
+// ------------------------------------------------------------------ page copies
+// Pages move in chunks of 16 KB: a chunk of one page of one layer for each
+// pass of a CTA, 64 bytes in flight per thread.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyChunk = kCopyThreads * 64;
+
+template <typename Pair>
+__device__ __forceinline__ void copy_pages(const KvPool& p, int n, const Pair& pair) {
+  const int chunks = (int)((p.page_bytes + kCopyChunk - 1) / kCopyChunk);
+  const long long total = (long long)n * p.layers * chunks;
+  for (long long x = blockIdx.x; x < total; x += gridDim.x) {
+    const int i = (int)(x / ((long long)p.layers * chunks));
+    const int rest = (int)(x - (long long)i * p.layers * chunks);
+    const int layer = rest / chunks;
+    const long long at = (long long)(rest - layer * chunks) * kCopyChunk;
+    int src, dst;
+    if (!pair(i, src, dst)) continue;
+    const uint8_t* s = p.data + layer * p.layer_stride + src * p.page_stride + at;
+    uint8_t* d = p.data + layer * p.layer_stride + dst * p.page_stride + at;
+    const long long left = p.page_bytes - at;
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int o = (k * kCopyThreads + threadIdx.x) * 16;
+      if (o < left) v[k] = __ldcs(reinterpret_cast<const uint4*>(s + o));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int o = (k * kCopyThreads + threadIdx.x) * 16;
+      if (o < left) __stcs(reinterpret_cast<uint4*>(d + o), v[k]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    kv_copy_kernel(const KvPool p, const int32_t* src, const int32_t* dst, int step, int n, int* status) {
+  griddep_launch_dependents();
+  griddep_wait();
+  copy_pages(p, n, [&](int i, int& s, int& d) {
+    s = __ldcg(src + (long long)i * step);
+    if (s == -1) return false;
+    d = __ldcg(dst + (long long)i * step);
+    if (s >= 0 && s < p.pages && d >= 0 && d < p.pages) return s != d;
+    if (status) atomicOr(status, kStatusBounds);
+    return false;
+  });
+}
+
+// ------------------------------------------------------------------ compact
+// The live pages at or past n = (number of live pages) move, in order, to the
+// free pages before n. ws: [0] live pages before page n, [1] moves, then
+// holes[pages], movers[pages] (indexed by the live pages before them) and
+// rank[pages] (live pages before a page).
+__global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
+    kv_rank_kernel(const KvPool p, int* ws) {
+  __shared__ int s_warp[32], s_cnt[kPoolCtas];
+  const uint32_t rank = cluster_rank();
+  griddep_launch_dependents();
+  griddep_wait();
+  int* holes = ws + 2;
+  int* movers = holes + p.pages;
+  int* ranks = movers + p.pages;
+  const PageRun run(p, rank, false);
+  int mine;
+  int before = block_scan(__popcll(run.bits), s_warp, mine);
+  if (threadIdx.x < kPoolCtas) st_dsmem_s32(&s_cnt[rank], threadIdx.x, mine);
+  cluster_sync_all();
+  int n = 0;
+  for (int r = 0; r < kPoolCtas; ++r) {
+    if (r < (int)rank) before += s_cnt[r];
+    n += s_cnt[r];
+  }
+  auto write_head = [&](int live_before) {
+    ws[0] = live_before;
+    ws[1] = n - live_before;
+    if (p.info) {
+      p.info[0] = 0;
+      p.info[1] = p.pages - n;
+      p.info[2] = n - live_before;
+    }
+  };
+  for (int k = 0; k < run.count; ++k) {
+    const int pg = run.first + k;
+    const bool live = (run.bits >> k) & 1;
+    if (pg == n) write_head(before);
+    if (pg < n) {
+      if (!live) holes[pg - before] = pg;
+    } else {
+      ranks[pg] = before;
+      if (live) movers[before] = pg;
+    }
+    before += live;
+  }
+  if (n == p.pages && rank == 0 && threadIdx.x == 0) write_head(n);
+}
+
+__global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(const KvPool p, const int* ws) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int l0 = __ldcg(ws), moves = __ldcg(ws + 1), n = l0 + moves;
+  const int* holes = ws + 2;
+  const int* movers = holes + p.pages;
+  const int* ranks = movers + p.pages;
+  const long long tid = (long long)blockIdx.x * kCopyThreads + threadIdx.x;
+  const long long threads = (long long)gridDim.x * kCopyThreads;
+  for (long long i = tid; i < moves; i += threads) {
+    const int from = __ldcg(movers + l0 + i), to = __ldcg(holes + i);
+    p.refs[to] = p.refs[from];
+    p.refs[from] = 0;
+  }
+  const long long entries = (long long)p.seqs * p.width;
+  for (long long i = tid; i < entries; i += threads) {
+    const long long s = i / p.width;
+    int32_t* t = p.table + s * p.table_stride + (i - s * p.width);
+    const int pg = *t;
+    if (pg < n || pg >= p.pages) continue;
+    // live pages at or past n only: an entry of a page that refs calls free
+    // would be a mistake of the caller's; its rank is still within the lists
+    const int m = __ldcg(ranks + pg) - l0;
+    if (m < moves) *t = __ldcg(holes + m);
+  }
+  copy_pages(p, moves, [&](int i, int& s, int& d) {
+    s = __ldcg(movers + l0 + i);
+    d = __ldcg(holes + i);
+    return true;
+  });
+}
+
+// ------------------------------------------------------------------ launches
+static int copy_grid(const Ctx& cx, const KvPool& p, long long n) {
+  const long long chunks = n * p.layers * ((p.page_bytes + kCopyChunk - 1) / kCopyChunk);
+  const long long most = 8LL * cx.sms;
+  return (int)(chunks < 1 ? 1 : (chunks < most ? chunks : most));
+}
+
+cudaError_t launch_kv_copy(const Ctx& cx, const KvPool& p, const int32_t* src, const int32_t* dst,
+                           int step, int n) {
+  return launch_k(kv_copy_kernel, dim3(copy_grid(cx, p, n)), dim3(kCopyThreads), 0, cx.stream, cx.pdl,
+                  p, src, dst, step, n, cx.status);
+}
+
+cudaError_t launch_kv_resize(const Ctx& cx, const KvPool& p, const int32_t* seqs,
+                             const int32_t* len, int n, int* pairs) {
+  PoolArgs a = {p, seqs, nullptr, len, n, pairs, cx.status};
+  cudaError_t e = launch_k(kv_change_kernel<false>, dim3(kPoolCtas), dim3(kPoolThreads), 0, cx.stream,
+                           cx.pdl, a);
+  if (e != cudaSuccess || !len) return e;  // all lengths 0: nothing to copy
+  return launch_kv_copy(cx, p, pairs, pairs + 1, 2, n);
+}
+
+cudaError_t launch_kv_fork(const Ctx& cx, const KvPool& p, const int32_t* src, const int32_t* dst,
+                           int n, int* pairs) {
+  PoolArgs a = {p, dst, src, nullptr, n, pairs, cx.status};
+  cudaError_t e = launch_k(kv_change_kernel<true>, dim3(kPoolCtas), dim3(kPoolThreads), 0, cx.stream,
+                           cx.pdl, a);
+  if (e != cudaSuccess) return e;
+  return launch_kv_copy(cx, p, pairs, pairs + 1, 2, n);
+}
+
+cudaError_t launch_kv_compact(const Ctx& cx, const KvPool& p, int* ws) {
+  cudaError_t e = launch_k(kv_rank_kernel, dim3(kPoolCtas), dim3(kPoolThreads), 0, cx.stream, cx.pdl,
+                           p, ws);
+  if (e != cudaSuccess) return e;
+  return launch_k(kv_move_kernel, dim3(copy_grid(cx, p, p.pages / 2 + 1)), dim3(kCopyThreads), 0,
+                  cx.stream, cx.pdl, p, ws);
+}
+
+}  // namespace dg

@@ -156,6 +156,88 @@ cudaError_t launch_add(const Ctx& cx, const void* a, const void* b, void* out, s
 cudaError_t launch_prefetch(const Ctx& cx, const void* ptr, size_t bytes);
 cudaError_t launch_selftest_timeout(const Ctx& cx, long long ns);
 
+// ------------------------------------------------------------------ paged cache
+// A cache and the batch of sequences that a call works on (dec_kv_view).
+struct KvView {
+  void* cache;
+  long long page_stride;  // elements
+  int pages, hkv, page, dim;
+  const int32_t* table;
+  long long table_stride;
+  int width, table_rows;
+  const int32_t* rows;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int batch;
+};
+
+// Tensor map of a cache, 4-D: (dim, position in page, keys' heads then values'
+// heads, page), read in boxes of 64 columns x box_rows positions with 128-byte
+// swizzle; pages that do not exist read as zeros. Returns false on failure.
+bool make_tmap_kv(CUtensorMap* map, const KvView& v, int box_rows);
+
+struct AttnCall {
+  const void* q;
+  void* out;
+  float* lse;
+  long long ldq, ldo;
+  int tokens, hq, window;
+  float scale;
+};
+
+// Attention for row tiles of 16 * rt rows (rt 1, 2 or 4) on mma.sync; ws of
+// attn_mma_ws bytes, ctr of one zero int per SM.
+size_t attn_mma_ws(int dim, int rt, int sms);
+cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCall& c, float* ws,
+                            int* ctr);
+
+struct AppendCall {
+  const void* qkv;
+  const void* wq;
+  const void* wk;
+  const float* rope;
+  const int32_t* positions;
+  void* q;
+  long long ldqkv, ldq;
+  int tokens, hq, rope_len, rot;
+  bool interleaved;
+  float eps;
+};
+cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c);
+
+// The pages of a cache of several layers and the state of its sequences
+// (dec_kv_pool); strides and page_bytes in bytes.
+struct KvPool {
+  uint8_t* data;
+  long long layer_stride, page_stride, page_bytes;
+  int layers, pages, page_shift;
+  int32_t* refs;
+  int32_t* table;
+  long long table_stride;
+  int width;
+  int32_t* lens;
+  int seqs;
+  int32_t* info;
+};
+// Change the lengths of n sequences (len null: to 0), or make sequences dst
+// copies of src. pairs: 2 n ints of workspace for the pages to copy.
+cudaError_t launch_kv_resize(const Ctx& cx, const KvPool& p, const int32_t* seqs,
+                             const int32_t* len, int n, int* pairs);
+cudaError_t launch_kv_fork(const Ctx& cx, const KvPool& p, const int32_t* src, const int32_t* dst,
+                           int n, int* pairs);
+// Copy pages: pair i is (src[i * step], dst[i * step]), none where src < 0.
+cudaError_t launch_kv_copy(const Ctx& cx, const KvPool& p, const int32_t* src, const int32_t* dst,
+                           int step, int n);
+// ws: 3 * pages + 2 ints.
+cudaError_t launch_kv_compact(const Ctx& cx, const KvPool& p, int* ws);
+
+// What the library keeps for the current device: its context and, for the
+// paged-cache calls, `bytes` of workspace and `ctrs` ints that are zero at
+// rest. DEC_* codes.
+int kv_sms();                  // SMs of the current device; 0 if it is not usable
+void count_launches(int n);    // for dec_launch_count
+int kv_context(void* stream, size_t bytes, size_t ctrs, Ctx* cx, void** ws, int** ctr);
+
 // Status bits of the allocation-free projection's fixed array on the current
 // device, read and cleared (0 if none or never used; -1 if the read failed).
 int noalloc_take_status();

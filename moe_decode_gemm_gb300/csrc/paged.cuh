@@ -1,0 +1,299 @@
+// paged.cuh -- what the paged-cache kernels share: the view of a cache and a
+// batch of sequences, and the split of an attention call's work over CTAs.
+//
+// A cache holds pages of `page` positions, [pages][2][heads][page][dim] bf16
+// (keys, then values). Sequence b of a batch owns row rows[b] (or b) of the
+// page table; its qn new tokens cu_q[b] .. cu_q[b+1] - 1 are the last of its
+// kv_len positions. Lengths and page numbers are device data: they are clamped
+// to what the caller's arrays hold, so wrong ones give wrong results and a
+// status, never an access out of range.
+//
+// Work is counted in units: one key tile (BN positions) read for one row tile
+// (tq tokens x the query heads that share a key head) of one sequence and key
+// head. The units of a call, in the order sequence, key head, row tile, key
+// tile, are cut into equal contiguous ranges, one per CTA; a row tile that
+// spans several ranges is finished by the last of its CTAs to arrive, which
+// joins the partial softmax states in CTA order.
+#pragma once
+
+#include "dg_common.cuh"
+#include "launch.h"
+
+namespace dg {
+
+constexpr int kMaxBatch = 1024;   // sequences of one call
+
+struct PagedArgs {
+  const int32_t* table;
+  const int32_t* rows;      // optional
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  long long table_stride;
+  int width, table_rows;    // entries of a table row, rows of the table (and of kv_len)
+  int pages, hkv, page;     // page: a power of two
+  int page_shift;
+  int batch, tokens;
+  int* status;
+};
+
+inline PagedArgs paged_args(const KvView& v, int tokens, int* status) {
+  PagedArgs p = {};
+  p.table = v.table;
+  p.rows = v.rows;
+  p.cu_q = v.cu_q;
+  p.kv_len = v.kv_len;
+  p.table_stride = v.table_stride;
+  p.width = v.width;
+  p.table_rows = v.table_rows;
+  p.pages = v.pages;
+  p.hkv = v.hkv;
+  p.page = v.page;
+  while ((1 << p.page_shift) < v.page) ++p.page_shift;
+  p.batch = v.batch;
+  p.tokens = tokens;
+  p.status = status;
+  return p;
+}
+
+// Row of the table (and of kv_len) of sequence b, or -1 if there is none.
+__device__ __forceinline__ int paged_row(const PagedArgs& p, int b) {
+  const int r = p.rows ? __ldg(p.rows + b) : b;
+  if (r >= 0 && r < p.table_rows) return r;
+  if (p.status) atomicOr(p.status, kStatusBounds);
+  return -1;
+}
+
+// Positions of a sequence: kv_len clamped to what its table row can hold.
+__device__ __forceinline__ int paged_len(const PagedArgs& p, int row) {
+  if (row < 0) return 0;
+  const int n = __ldg(p.kv_len + row);
+  const long long cap = (long long)p.width << p.page_shift;
+  if (n >= 0 && n <= cap) return n;
+  if (p.status) atomicOr(p.status, kStatusBounds);
+  return n < 0 ? 0 : (int)cap;
+}
+
+// First token and token count of sequence b, within [0, tokens].
+__device__ __forceinline__ void paged_tokens(const PagedArgs& p, int b, int& q0, int& qn) {
+  const int a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
+  q0 = a < 0 ? 0 : (a > p.tokens ? p.tokens : a);
+  const int q1 = e < q0 ? q0 : (e > p.tokens ? p.tokens : e);
+  qn = q1 - q0;
+  if ((a != q0 || e != q1) && p.status) atomicOr(p.status, kStatusBounds);
+}
+
+// ------------------------------------------------------------------ the split
+struct SplitShape {
+  int tq;        // tokens of a row tile
+  int bn_shift;  // log2 of the key tile
+  int window;    // 0: none
+  int hkv;
+};
+
+// Key tiles [j0, j0 + n) of row tile i of a sequence with qn new tokens and kv
+// positions; n >= 1 (a tile whose rows see nothing still writes its zeros).
+// klo, khi: positions that some row of the tile sees, [klo, khi).
+struct TileRange {
+  int j0, n, klo, khi;
+};
+__device__ __forceinline__ TileRange tile_range(const SplitShape& s, int qn, int kv, int i) {
+  TileRange r;
+  const int t0 = i * s.tq;
+  const int t1 = t0 + s.tq < qn ? t0 + s.tq : qn;
+  r.khi = kv - qn + t1;
+  if (r.khi < 0) r.khi = 0;
+  r.klo = 0;
+  if (s.window > 0) {
+    const int lo = kv - qn + t0 - s.window + 1;
+    if (lo > 0) r.klo = lo;
+  }
+  r.j0 = r.klo >> s.bn_shift;
+  r.n = ((r.khi + (1 << s.bn_shift) - 1) >> s.bn_shift) - r.j0;
+  if (r.n < 1) r.n = 1;
+  return r;
+}
+
+// Shared-memory tables of a call's sequences (sized for the batch).
+struct SplitTables {
+  long long* base;   // [batch + 1] first unit of each sequence
+  long long* wsum;   // [32] scan scratch
+  int* q0;           // [batch]
+  int* qn;
+  int* kv;
+  int* row;
+  int* loc;          // [4] this CTA's first sequence, head, row tile, key tile in it
+  static __host__ __device__ constexpr int bytes(int batch) {
+    return 8 * (batch + 1) + 8 * 32 + 16 * batch + 16;
+  }
+  __device__ explicit SplitTables(void* smem, int batch) {
+    base = reinterpret_cast<long long*>(smem);
+    wsum = base + batch + 1;
+    q0 = reinterpret_cast<int*>(wsum + 32);
+    qn = q0 + batch;
+    kv = qn + batch;
+    row = kv + batch;
+    loc = row + batch;
+  }
+};
+
+// Fill the tables and find this CTA's range [u0, u1) of the W units and where
+// it begins. Called by all NT threads of the CTA; ends with a barrier.
+// G: CTAs that take part (W / min_units at most).
+template <int NT>
+__device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape& s,
+                                            const SplitTables& t, int min_units, long long& W,
+                                            long long& G, long long& u0, long long& u1) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kFew = 4;  // row tiles of a sequence that one thread counts by itself
+  // units of each sequence and head, into base[b + 1]
+  for (int b = tid; b < p.batch; b += NT) {
+    int q0, qn;
+    paged_tokens(p, b, q0, qn);
+    const int row = paged_row(p, b);
+    const int kv = paged_len(p, row);
+    t.q0[b] = q0;
+    t.qn[b] = qn;
+    t.kv[b] = kv;
+    t.row[b] = row;
+    const int tiles = (qn + s.tq - 1) / s.tq;
+    long long u = 0;
+    if (tiles <= kFew)
+      for (int i = 0; i < tiles; ++i) u += tile_range(s, qn, kv, i).n;
+    t.base[b + 1] = u;
+  }
+  __syncthreads();
+  for (int b = warp; b < p.batch; b += NT / 32) {
+    const int qn = t.qn[b], tiles = (qn + s.tq - 1) / s.tq;
+    if (tiles <= kFew) continue;
+    long long u = 0;
+    for (int i = lane; i < tiles; i += 32) u += tile_range(s, qn, t.kv[b], i).n;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(~0u, u, o);
+    if (lane == 0) t.base[b + 1] = u;
+  }
+  __syncthreads();
+  // inclusive scan of base[1 .. batch] (units of all heads)
+  const int per = (p.batch + NT - 1) / NT;
+  long long mine = 0;
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    if (b < p.batch) mine += t.base[b + 1] * s.hkv;
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) t.wsum[warp] = inc;
+  __syncthreads();
+  long long at = inc - mine;
+  for (int w = 0; w < warp; ++w) at += t.wsum[w];
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    if (b < p.batch) {
+      at += t.base[b + 1] * s.hkv;
+      t.base[b + 1] = at;
+    }
+  }
+  if (tid == 0) t.base[0] = 0;
+  __syncthreads();
+  W = t.base[p.batch];
+  G = W / min_units;
+  if (G < 1) G = 1;
+  if (G > (long long)gridDim.x) G = gridDim.x;
+  const long long c = blockIdx.x;
+  u0 = c < G ? cta_start(c, W, G) : 0;
+  u1 = c < G ? cta_start(c + 1, W, G) : 0;
+  if (warp == 0 && u0 < u1) {
+    int lo = 0, hi = p.batch - 1;  // last sequence with base <= u0 (and units)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.base[mid] <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    const int b = lo;
+    const long long U = (t.base[b + 1] - t.base[b]) / s.hkv;
+    const long long r = u0 - t.base[b];
+    const int h = (int)(r / U);
+    long long off = r - h * U;
+    int i = 0;
+    const int qn = t.qn[b], kv = t.kv[b];
+    for (;; i += 32) {
+      // past the last row tile the ranges are not used: off ends before them
+      const int n = tile_range(s, qn, kv, i + lane).n;
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const unsigned past = __ballot_sync(~0u, (long long)sum > off);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        off -= __shfl_sync(~0u, sum - n, l);
+        i += l;
+        break;
+      }
+      off -= __shfl_sync(~0u, sum, 31);
+    }
+    if (lane == 0) {
+      t.loc[0] = b;
+      t.loc[1] = h;
+      t.loc[2] = i;
+      t.loc[3] = (int)off;
+    }
+  }
+  __syncthreads();
+}
+
+// Walks this CTA's range segment by segment: a segment is the part of one row
+// tile's key tiles that the CTA has. Every warp role walks the same sequence.
+struct SplitWalk {
+  const SplitShape& s;
+  const SplitTables& t;
+  long long u, u1;
+  int b, h, i, off;
+  // the current segment
+  TileRange tr;
+  int j, n;             // key tiles [j, j + n)
+  bool whole;           // covers its row tile
+  __device__ SplitWalk(const SplitShape& s_, const SplitTables& t_, long long u0, long long u1_)
+      : s(s_), t(t_), u(u0), u1(u1_), b(0), h(0), i(0), off(0) {
+    if (u < u1) {
+      b = t.loc[0];
+      h = t.loc[1];
+      i = t.loc[2];
+      off = t.loc[3];
+      load();
+    }
+  }
+  __device__ bool more() const { return u < u1; }
+  __device__ void load() {
+    tr = tile_range(s, t.qn[b], t.kv[b], i);
+    j = tr.j0 + off;
+    const long long left = u1 - u;
+    n = tr.n - off;
+    if (left < n) n = (int)left;
+    whole = n == tr.n;
+  }
+  // first unit of the current row tile
+  __device__ long long tile_unit() const { return u - off; }
+  __device__ void next() {
+    u += n;
+    if (u >= u1) return;
+    // the CTA's range goes on, so the row tile has ended
+    off = 0;
+    if (++i * s.tq >= t.qn[b]) {
+      i = 0;
+      if (++h == s.hkv) {
+        h = 0;
+        do ++b;
+        while (t.qn[b] == 0);
+      }
+    }
+    load();
+  }
+};
+
+}  // namespace dg

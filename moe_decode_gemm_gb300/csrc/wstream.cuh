@@ -153,15 +153,6 @@ __device__ __forceinline__ UnitPos unit_pos(long long u, int KB, int TILES) {
   return UnitPos{(int)(u - gt * KB), (int)(gt % TILES), (int)(gt / TILES)};
 }
 
-__device__ __forceinline__ long long cta_start(long long c, long long T, long long G) {
-  return (c * T) / G;
-}
-
-// CTA whose unit range contains unit v: largest c with start(c) <= v.
-__device__ __forceinline__ long long cta_of(long long v, long long T, long long G) {
-  return ((v + 1) * G + T - 1) / T - 1;
-}
-
 // ------------------------------------------------------------------ epilogue
 template <int EPI, bool GROUPED>
 __device__ __forceinline__ void store_out(const StreamArgs& a, const GroupInfo& gi, int t, int n,
