@@ -52,15 +52,28 @@ static int attention(const dec_kv_view* kv, const AttnCall& c, void* stream) {
   if (!al(c.q, 16) || !al(c.out, 16) || !al(c.lse, 4)) return DEC_EINVAL;
   const int group = c.hq / v.hkv;
   if (group > 64) return DEC_EUNSUPPORTED;
-  // The smallest row tile that holds the longest chunk's rows (token, query
-  // head), at most 64 rows: longer chunks take several tiles.
-  const int64_t rows = (int64_t)(kv->max_q > 0 ? kv->max_q : c.tokens) * group;
-  const int rt = rows <= 16 && group <= 16 ? 1 : (rows <= 32 && group <= 32 ? 2 : 4);
   const int sms = kv_sms();
   if (!sms) return DEC_ENODEV;
   Ctx cx;
   void* ws;
   int* ctr;
+  // Rows (token, query head) of the longest chunk. tcgen05 above 64: a key tile
+  // then serves several mma.sync row tiles and the products bound the call. A
+  // scale of 0 or below (whose maximum is not the scaled maximum) stays on
+  // mma.sync, which scales before it compares.
+  const int64_t rows = (int64_t)(kv->max_q > 0 ? kv->max_q : c.tokens) * group;
+  bool tc = rows > 64;
+  const char* force = std::getenv("DEC_FORCE");
+  if (force && !std::strcmp(force, "mma")) tc = false;
+  if (force && !std::strcmp(force, "tc")) tc = true;
+  if (tc && c.scale > 0.f) {
+    if ((rc = kv_context(stream, attn_tc_ws(v.dim, sms), 0, &cx, &ws, nullptr))) return rc;
+    t_last_attention = DEC_REGIME_TC;
+    return result(launch_attn_tc(cx, v, c, ws), 2);
+  }
+  // the smallest row tile that holds them, at most 64 rows: longer chunks take
+  // several
+  const int rt = rows <= 16 && group <= 16 ? 1 : (rows <= 32 && group <= 32 ? 2 : 4);
   if ((rc = kv_context(stream, attn_mma_ws(v.dim, rt, sms), sms, &cx, &ws, &ctr))) return rc;
   t_last_attention = DEC_REGIME_MMA;
   return result(launch_attn_mma(cx, v, rt, c, static_cast<float*>(ws), ctr), 1);

@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
   float* sc_ml = scratch + kWarps * 16 * Sh::kLd;  // [warp][16][m, l]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * Sh::kStage + Sh::kScratch);
   uint64_t* empty = full + kStages;
-  volatile int* s_flag = reinterpret_cast<volatile int*>(empty + kStages);  // [0] abort [1] last
+  // [0] abort [1] last [2], [3] segment number + 1 with a non-finite edge value
+  volatile int* s_flag = reinterpret_cast<volatile int*>(empty + kStages);
   const SplitTables tab(reinterpret_cast<uint8_t*>(empty + kStages) + 64, a.p.batch);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       mbar_init(&empty[i], kWarps);
     }
     s_flag[0] = 0;
+    s_flag[2] = s_flag[3] = 0;
     fence_mbar_init();
     prefetch_tmap(&kvmap);
   }
@@ -149,8 +151,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
   // ------------------------------------------------------------------ consumers
   const int rt = warp / kKS, ks = warp % kKS;   // row tile of 16, share of the positions
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;
-  int it = 0;
-  for (; w.more(); w.next()) {
+  int it = 0, seg = 0;
+  for (; w.more(); w.next(), ++seg) {
     const int qn = tab.qn[w.b], kv = tab.kv[w.b];
     const int t0 = w.i * a.s.tq;
     const int nt = qn - t0 < a.s.tq ? qn - t0 : a.s.tq;
@@ -174,9 +176,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
         qf[kk][e + 2] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + c0)) : 0u;
       }
     }
-    // positions that every row sees: [all_lo, all_hi)
-    const int all_hi = pos0 + 1;
-    const int all_lo = a.s.window > 0 ? pos0 + nt - 1 - a.s.window + 1 : 0;
+    const EdgeRange er = edge_range(a.s, w.tr, pos0, nt);
+    bool found = false;  // a non-finite value that only some rows see
     float o[D / 8][4];
 #pragma unroll
     for (int d = 0; d < D / 8; ++d)
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       if (!s_flag[0] && !mbar_wait(&full[st], (it / kStages) & 1, a.timeout_ns, a.p.status))
         s_flag[0] = 1;
       const uint32_t kb = smem_u32(smem + st * Sh::kStage), vb = kb + Sh::kKBytes;
-      const bool edge = key0 + kAttnKeys > all_hi || key0 < all_lo;
+      const bool edge = er.in(key0, kAttnKeys);
 #pragma unroll
       for (int blk = 0; blk < kAttnKeys / 16 / kKS; ++blk) {
         const int kr = (blk * kKS + ks) * 16;  // first position of this block in the tile
@@ -258,14 +259,19 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
             pf[t * 2 + e] = pack_bf16(p0, p1);
           }
         }
-        uint32_t vm0 = ~0u, vm1 = ~0u;
         if (edge) {
-          // values that no row sees may be anything (an unused place of a
-          // page): 0 in their place, as 0 * NaN is not 0
-          auto keep = [&](int key) -> bool { return key >= w.tr.klo && key < w.tr.khi; };
-          const int key = key0 + kr + c0;
-          vm0 = (keep(key) ? 0xFFFFu : 0u) | (keep(key + 1) ? 0xFFFF0000u : 0u);
-          vm1 = (keep(key + 8) ? 0xFFFFu : 0u) | (keep(key + 9) ? 0xFFFF0000u : 0u);
+          // values that no row sees (the unused end of a page may hold
+          // anything), and non-finite ones that only some rows see, become 0.
+          // Warps of other row tiles may do the same to the same values.
+          for (int x = lane; x < 16 * (D / 8); x += 32) {
+            const int key = kr + x / (D / 8), ch = x % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(smem + st * Sh::kStage + Sh::kKBytes +
+                                                 (ch >> 3) * Sh::kHalf + key * 128 +
+                                                 (((ch & 7) ^ (key & 7)) << 4));
+            found |= clean_edge_value(at, er, key0 + key);
+          }
+          fence_async_shared();
+          __syncwarp();
         }
         {
           // matrices: positions 0-7 / 8-15 (lane bit 3), column chunks 0 / 1 (bit 4)
@@ -276,12 +282,6 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
             const int chunk = (d & 3) * 2 + ch;
             ldmatrix_x4_trans(b0, b1, b2, b3,
                               vb + (d >> 2) * Sh::kHalf + key * 128 + ((chunk ^ (key & 7)) << 4));
-            if (edge) {
-              b0 &= vm0;
-              b1 &= vm1;
-              b2 &= vm0;
-              b3 &= vm1;
-            }
             mma_bf16_16816(o[2 * d], pf, b0, b1);
             mma_bf16_16816(o[2 * d + 1], pf, b2, b3);
           }
@@ -305,8 +305,10 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
         *reinterpret_cast<float2*>(scratch + (warp * 16 + r0 + e * 8) * Sh::kLd + d * 8 + c0) =
             make_float2(o[d][2 * e], o[d][2 * e + 1]);
     }
+    if (found) s_flag[2 + (seg & 1)] = seg + 1;
     named_bar_sync(1, kCons);
     const bool aborted = s_flag[0] != 0;
+    const bool poison = s_flag[2 + (seg & 1)] == seg + 1;
     const int ct = threadIdx.x;
     const long long c = blockIdx.x;
     const long long ut = w.tile_unit();
@@ -342,6 +344,18 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
         v.y += f * q4.y;
         v.z += f * q4.z;
         v.w += f * q4.w;
+      }
+      if (poison) {
+        const int t = r / a.group, p = pos0 + t;
+        edge_values<D>(a.p, tab.row[w.b], w.h, er, a.s.window > 0 ? p - a.s.window + 1 : 0, p,
+                       w.j * kAttnKeys, (w.j + w.n) * kAttnKeys, d, [&](const uint16_t* e) {
+                         const uint2 pk = __ldg(reinterpret_cast<const uint2*>(e));
+                         const float f[4] = {bf16lo(pk.x), bf16hi(pk.x), bf16lo(pk.y), bf16hi(pk.y)};
+                         if (!isfinite(f[0])) v.x += f[0];
+                         if (!isfinite(f[1])) v.y += f[1];
+                         if (!isfinite(f[2])) v.z += f[2];
+                         if (!isfinite(f[3])) v.w += f[3];
+                       });
       }
       if (w.whole) {
         if (!aborted) store(r, d, v, M, L);

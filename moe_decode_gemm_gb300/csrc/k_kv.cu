@@ -31,7 +31,7 @@ struct AppendArgs {
   const int32_t* positions;
   uint16_t* q;
   uint16_t* cache;
-  long long ldqkv, ldq, page_stride;
+  long long ldqkv, ldq;
   int hq, rope_len, rot, interleaved;
   float eps;
 };
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     } else {
       const int page = s_page[tok - tok0], pos = s_pos[tok - tok0];
       if (page >= 0)  // head - hq: key heads, then value heads, as the cache has them
-        *reinterpret_cast<uint4*>(a.cache + page * a.page_stride +
+        *reinterpret_cast<uint4*>(a.cache + page * a.p.page_stride +
                                   ((long long)(head - a.hq) * a.p.page + (pos & (a.p.page - 1))) * D +
                                   l * 8) = out;
     }
@@ -194,7 +194,6 @@ cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c) {
   a.cache = static_cast<uint16_t*>(v.cache);
   a.ldqkv = c.ldqkv;
   a.ldq = c.ldq;
-  a.page_stride = v.page_stride;
   a.hq = c.hq;
   a.rope_len = c.rope_len;
   a.rot = c.rot;

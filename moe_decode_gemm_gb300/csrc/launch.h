@@ -191,6 +191,17 @@ size_t attn_mma_ws(int dim, int rt, int sms);
 cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCall& c, float* ws,
                             int* ctr);
 
+// Tensor map of activations [tokens, heads, dim] (rows ld elements apart) read
+// in boxes of 64 columns x box_heads x box_tokens, 128-byte swizzle; tokens past
+// the end read as zeros.
+bool make_tmap_heads(CUtensorMap* map, const void* q, int tokens, int heads, int dim, long long ld,
+                     int box_heads, int box_tokens);
+
+// Attention for longer chunks on tcgen05 (scale > 0); two kernels; ws of
+// attn_tc_ws bytes.
+size_t attn_tc_ws(int dim, int sms);
+cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, void* ws);
+
 struct AppendCall {
   const void* qkv;
   const void* wq;

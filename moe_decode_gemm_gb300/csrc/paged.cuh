@@ -30,6 +30,8 @@ struct PagedArgs {
   const int32_t* kv_len;
   long long table_stride;
   int width, table_rows;    // entries of a table row, rows of the table (and of kv_len)
+  const uint16_t* cache;
+  long long page_stride;    // elements
   int pages, hkv, page;     // page: a power of two
   int page_shift;
   int batch, tokens;
@@ -45,6 +47,8 @@ inline PagedArgs paged_args(const KvView& v, int tokens, int* status) {
   p.table_stride = v.table_stride;
   p.width = v.width;
   p.table_rows = v.table_rows;
+  p.cache = static_cast<const uint16_t*>(v.cache);
+  p.page_stride = v.page_stride;
   p.pages = v.pages;
   p.hkv = v.hkv;
   p.page = v.page;
@@ -113,6 +117,68 @@ __device__ __forceinline__ TileRange tile_range(const SplitShape& s, int qn, int
   return r;
 }
 
+// What the rows of a row tile see of the positions.
+struct EdgeRange {
+  int klo, khi;          // seen by some row: [klo, khi)
+  int all_lo, all_hi;    // seen by every row: [all_lo, all_hi)
+  // positions [key0, key0 + n) are not all seen by every row
+  __device__ bool in(int key0, int n) const { return key0 + n > all_hi || key0 < all_lo; }
+};
+// pos0: position of the tile's first of nt tokens
+__device__ __forceinline__ EdgeRange edge_range(const SplitShape& s, const TileRange& r, int pos0,
+                                                int nt) {
+  return EdgeRange{r.klo, r.khi, s.window > 0 ? pos0 + nt - s.window : 0, pos0 + 1};
+}
+
+// A value of a key tile at the edge must not reach the sums of rows that do
+// not see it: as 0 * NaN and 0 * inf are NaN, the kernels make 0 of what no
+// row sees (the unused end of a page may hold anything), and of a non-finite
+// value that only some rows see, which those rows get added at the end.
+//
+// Cleans 8 values of position pos in shared memory; true if one of them is
+// such a non-finite value.
+__device__ __forceinline__ bool clean_edge_value(uint4* at, const EdgeRange& er, int pos) {
+  if (pos < er.klo || pos >= er.khi) {
+    *at = make_uint4(0, 0, 0, 0);
+    return false;
+  }
+  if (pos >= er.all_lo && pos < er.all_hi) return false;
+  uint4 v = *at;
+  bool any = false;
+  auto finite = [&](uint32_t& e) {
+    if ((e & 0x7F80u) == 0x7F80u) e &= 0xFFFF0000u, any = true;
+    if ((e & 0x7F800000u) == 0x7F800000u) e &= 0xFFFFu, any = true;
+  };
+  finite(v.x);
+  finite(v.y);
+  finite(v.z);
+  finite(v.w);
+  if (any) *at = v;
+  return any;
+}
+
+// Calls f(pointer to column d) for each position in [kbeg, kend) that a row
+// seeing [lo, hi] sees and some other row of its tile does not.
+template <int D, typename F>
+__device__ __forceinline__ void edge_values(const PagedArgs& p, int row, int h, const EdgeRange& er,
+                                            int lo, int hi, int kbeg, int kend, int d, const F& f) {
+  if (row < 0) return;
+  for (int side = 0; side < 2; ++side) {
+    int from = side ? (er.all_hi > er.all_lo ? er.all_hi : er.all_lo) : er.klo;
+    int to = side ? er.khi : er.all_lo;
+    if (from < lo) from = lo;
+    if (from < kbeg) from = kbeg;
+    if (to > hi + 1) to = hi + 1;
+    if (to > kend) to = kend;
+    for (int key = from; key < to; ++key) {
+      const int pg = __ldg(p.table + row * p.table_stride + (key >> p.page_shift));
+      if (pg < 0 || pg >= p.pages) continue;
+      f(p.cache + pg * p.page_stride +
+        ((long long)(p.hkv + h) * p.page + (key & (p.page - 1))) * D + d);
+    }
+  }
+}
+
 // Shared-memory tables of a call's sequences (sized for the batch).
 struct SplitTables {
   long long* base;   // [batch + 1] first unit of each sequence
@@ -138,7 +204,7 @@ struct SplitTables {
 
 // Fill the tables and find this CTA's range [u0, u1) of the W units and where
 // it begins. Called by all NT threads of the CTA; ends with a barrier.
-// G: CTAs that take part (W / min_units at most).
+// G: CTAs that take part (W / min_units at most, and the grid).
 template <int NT>
 __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape& s,
                                             const SplitTables& t, int min_units, long long& W,

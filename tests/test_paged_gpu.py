@@ -402,3 +402,56 @@ def test_a_pools_layer_is_attended():
     past[0] = [None, None]
     dg.kv_compact(pool)
     step([3, 1, 2, 0], [1, 20, 1, 40])
+
+
+# ------------------------------------------------------------------ non-finite values
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("new,total,window,max_q", [
+    ([6], [200], 0, 6), ([6], [130], 40, 6), ([40], [300], 0, 40), ([40], [40], 0, 40),
+    ([90], [400], 64, 90), ([200], [1000], 0, 200), ([1, 3], [66, 67], 0, 3)])
+def test_non_finite_values_reach_only_the_rows_that_see_them(bad, new, total, window, max_q):
+    bt = pg.Batch(new, total, 14, 1, 128, 16, seed=50)
+    g = pg.gen(51)
+    for b, (n, m) in enumerate(zip(new, total)):
+        k, v = bt.k[b], bt.v[b]
+        for _ in range(4):  # among the new tokens, and where windows end
+            j = m - 1 - int(torch.randint(0, min(m, n + window), (1,), generator=g))
+            v[0, j, int(torch.randint(0, 128, (1,), generator=g))] = bad
+        v[0, m - 1, 5] = bad
+        bt.put(b, k, v)
+    out, lse = run(bt, window=window, max_q=max_q)
+    ref, rl, ab = pg.attention(bt, window)
+    o = out.double().cpu()
+    fine = ref.isfinite()
+    assert torch.equal(o.isfinite(), fine)
+    assert torch.equal(o.isnan(), ref.isnan())
+    assert torch.equal(o[~fine & ~ref.isnan()], ref[~fine & ~ref.isnan()])
+    err = (o - ref)[fine].abs()
+    assert bool((err <= (pg.U * ref.abs() + (pg.U + 2.0 ** -12) * ab)[fine]).all())
+    assert bool(((lse.double().cpu() - rl).abs() <= 2.0 ** -16 * (1 + rl.abs())).all())
+
+
+@pytest.mark.parametrize("max_q", [5, 100])
+def test_non_finite_keys_reach_only_the_rows_that_see_them(max_q):
+    bt = pg.Batch([5, 100], [90, 333], 14, 1, 128, 16, seed=52)
+    for b, j in ((0, 87), (1, 300)):
+        bt.k[b][0, j, 3] = float("nan")
+        bt.put(b, bt.k[b], bt.v[b])
+    out, lse = run(bt, max_q=max_q)
+    ref, rl, ab = pg.attention(bt)
+    o = out.double().cpu()
+    assert torch.equal(o.isnan(), ref.isnan()) and torch.equal(lse.cpu().isnan(), rl.isnan())
+    fine = ref.isfinite()
+    assert bool(((o - ref)[fine].abs()
+                 <= (pg.U * ref.abs() + (pg.U + 2.0 ** -12) * ab)[fine]).all())
+
+
+def test_regimes_and_forced_regimes(monkeypatch):
+    bt = pg.Batch([3, 70], [100, 300], 14, 1, 128, 64, seed=53)
+    res = {}
+    for force in ("", "mma", "tc"):
+        monkeypatch.setenv("DEC_FORCE", force)
+        for max_q in (1, 70):
+            res[force, max_q] = run(bt, max_q=max_q)
+            pg.check_attention(bt, *res[force, max_q], what="%s %d" % (force, max_q))
+            assert dg.last_attention() == (force or ("mma" if max_q == 1 else "tc"))
