@@ -352,6 +352,38 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// The larger of three; a NaN is passed over, as by fmaxf.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two fp32 operations in one instruction: a * b + c and a + b, elementwise.
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 y;
+  asm("{\n\t.reg .b64 u, v, w;\n\t"
+      "mov.b64 u, {%2, %3};\n\t"
+      "mov.b64 v, {%4, %4};\n\t"
+      "mov.b64 w, {%5, %5};\n\t"
+      "fma.rn.f32x2 u, u, v, w;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 u, v;\n\t"
+      "mov.b64 u, {%2, %3};\n\t"
+      "mov.b64 v, {%4, %5};\n\t"
+      "add.rn.f32x2 u, u, v;\n\t"
+      "mov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
+}
+
 // 2^x (approximate to about 2 ulp; 0 at -inf, subnormal results flushed).
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
     int it = 0;
     bool ok = true;
     for (; w.more() && ok; w.next()) {
-      const int row = tab.row[w.b];
+      const int row = paged_row(a.p, w.b);
       const int32_t* trow = a.p.table + (long long)(row < 0 ? 0 : row) * a.p.table_stride;
       auto page_at = [&](int j) -> int {
         const int pos = j * kAttnKeys + piece * rows;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
   int it = 0, seg = 0;
   for (; w.more(); w.next(), ++seg) {
     const int qn = tab.qn[w.b], kv = tab.kv[w.b];
-    const int t0 = w.i * a.s.tq;
+    const int q0 = paged_first(a.p, w.b), t0 = w.i * a.s.tq;
     const int nt = qn - t0 < a.s.tq ? qn - t0 : a.s.tq;
     const int rows = nt * a.group;
     const int pos0 = kv - qn + t0;               // position of the tile's first token
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       const int r = rt * 16 + r0 + e * 8;
       const bool live = r < rows;
       const int t = live ? r / a.group : 0;
-      const uint16_t* src = a.q + (long long)(tab.q0[w.b] + t0 + t) * a.ldq +
+      const uint16_t* src = a.q + (long long)(q0 + t0 + t) * a.ldq +
                             (long long)(w.h * a.group + (live ? r - t * a.group : 0)) * D;
       hi[e] = live ? pos0 + t : -1;
       lo[e] = live && a.s.window > 0 ? pos0 + t - a.s.window + 1 : 0;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
     float* mine = a.ws + slot * Sh::kSlot;
     auto store = [&](int r, int d, float4 v, float mm, float ll) {
       const int t = r / a.group, g = r - t * a.group;
-      const long long tok = tab.q0[w.b] + t0 + t;
+      const long long tok = q0 + t0 + t;
       const int head = w.h * a.group + g;
       const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // NaN stays NaN
       uint2 pk = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       }
       if (poison) {
         const int t = r / a.group, p = pos0 + t;
-        edge_values<D>(a.p, tab.row[w.b], w.h, er, a.s.window > 0 ? p - a.s.window + 1 : 0, p,
+        edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, a.s.window > 0 ? p - a.s.window + 1 : 0, p,
                        w.j * kAttnKeys, (w.j + w.n) * kAttnKeys, d, [&](const uint16_t* e) {
                          const uint2 pk = __ldg(reinterpret_cast<const uint2*>(e));
                          const float f[4] = {bf16lo(pk.x), bf16hi(pk.x), bf16lo(pk.y), bf16hi(pk.y)};

@@ -29,6 +29,8 @@
 // The work is split into equal ranges of (row tile pair, key tile) units, see
 // paged.cuh. A pair that spans several CTAs leaves its unnormalised O, m and
 // sum in the workspace, and a second small kernel joins them.
+#include <type_traits>
+
 #include "launch.h"
 #include "launch_util.cuh"
 #include "paged.cuh"
@@ -39,7 +41,7 @@ namespace dg {
 constexpr int kTcKeys = 128;         // positions of a key tile
 constexpr int kTcKeysShift = 7;
 constexpr int kTcRowsA = 128;        // rows of a row tile
-constexpr int kTcAttnThreads = 352;
+constexpr int kTcAttnThreads = 384;
 constexpr float kTcLazy = 8.f;       // growth of the maximum (log2) that is left in P
 
 struct TcAttnArgs {
@@ -57,55 +59,150 @@ struct TcAttnArgs {
   long long timeout_ns;
 };
 
+// Shared memory: Q of A and B, and a ring of pairs: slot i holds the values of
+// the CTA's key tile i - 1 and the keys of its tile i, which are needed and
+// given back together.
 template <int D>
 struct TcAttnShape {
   static constexpr int kHalf = kTcKeys * 128;            // 64 columns of a 128-row tile
   static constexpr int kTile = kTcKeys * D * 2;          // a tile of Q, K or V
-  static constexpr int kStages = 128 * 1024 / kTile;
-  static constexpr int kSlot = 2 * kTcRowsA * (D + 2);   // floats of a split pair's partial
+  static constexpr int kSlots = 64 * 1024 / kTile;       // of 2 tiles
+  static constexpr int kStage = 16 * 1024;               // output rows on their way: 2 KB a warp
+  static constexpr int kPart = 2 * kTcRowsA * (D + 2);   // floats of a split pair's partial
   static int smem(int batch) {
-    return 1024 + 2 * kTile + kStages * kTile + 8 * (3 * kStages + 16) + 128 +
+    return 1024 + 2 * kTile + kSlots * 2 * kTile + kStage + 8 * (3 * kSlots + 16) + 64 +
            SplitTables::bytes(batch) + 16;
   }
 };
+
+// The 16-position steps [k0, k1) of an edge tile that some row sees (at least
+// one, so that O is written).
+__device__ __forceinline__ void edge_steps(const EdgeRange& er, int key0, int& k0, int& k1) {
+  k0 = er.klo > key0 ? (er.klo - key0) >> 4 : 0;
+  k1 = er.khi - key0 < kTcKeys ? (er.khi - key0 + 15) >> 4 : kTcKeys / 16;
+  if (k0 > kTcKeys / 16 - 1) k0 = kTcKeys / 16 - 1;
+  if (k1 <= k0) k1 = k0 + 1;
+}
+
+// Puts -inf in the columns of a row of S (128 fp32 in TMEM, this thread's lane)
+// outside [l0, h0]. A pass of its own over the few tiles at the edge of what
+// the rows see, in few instructions: code that runs once in a while costs its
+// instruction fetches.
+__device__ __forceinline__ void row_mask(uint32_t ts, int l0, int h0) {
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q, ts += 32, l0 -= 32, h0 -= 32) {
+    const uint32_t above = l0 <= 0 ? ~0u : (l0 > 31 ? 0u : ~0u << l0);
+    const uint32_t below = h0 < 0 ? 0u : (h0 >= 31 ? ~0u : ~(~0u << (h0 + 1)));
+    const uint32_t seen = above & below;
+    if (__all_sync(~0u, seen == ~0u)) continue;
+    uint32_t v[32];
+    tmem_ld32(ts, v);
+    tmem_ld_wait();
+    tmem_settle<32>(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(seen & (1u << e))) v[e] = 0xFF800000u;  // -inf
+    tmem_st32(ts, v);
+  }
+  tmem_st_wait();
+}
+
+// The maximum of c s over the first 32 columns of a row of S.
+__device__ __forceinline__ float row_start(uint32_t ts, float c) {
+  uint32_t v[32];
+  tmem_ld32(ts, v);
+  tmem_ld_wait();
+  tmem_settle<32>(v);
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    mx0 = max3(mx0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    mx1 = max3(mx1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+  }
+  return fmaxf(mx0, mx1) * c;
+}
+
+// One row of S: top = max c s, the weights 2^(c s - m) as bf16 pairs in pk, and
+// their fp32 sum. The next 32 columns load while the current ones are worked
+// on.
+__device__ __forceinline__ void row_pass(uint32_t ts, float c, float m, uint32_t* pk, float& top,
+                                         float& sum) {
+  alignas(8) uint32_t s[2][32];
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+  float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+  tmem_ld32(ts, s[0]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t* v = s[q & 1];
+    tmem_ld_wait();
+    tmem_settle<32>(v);
+    if (q < 3) tmem_ld32(ts + (q + 1) * 32, s[(q + 1) & 1]);
+    float2* f = reinterpret_cast<float2*>(v);
+    // in the order of a pipeline four pairs deep: a pair's scaling ahead of its
+    // exponentials, its sum and packing behind them
+#pragma unroll
+    for (int e = 0; e < 16 + 8; ++e) {
+      if (e < 16) {
+        if (e & 1) mx1 = max3(mx1, f[e].x, f[e].y);
+        else mx0 = max3(mx0, f[e].x, f[e].y);
+        f[e] = fma2(f[e], c, -m);
+      }
+      if (e >= 4 && e < 20) {
+        f[e - 4].x = exp2_approx(f[e - 4].x);
+        f[e - 4].y = exp2_approx(f[e - 4].y);
+      }
+      if (e >= 8) {
+        const float2 p = f[e - 8];
+        if (e & 1) acc1 = add2(acc1, p);
+        else acc0 = add2(acc0, p);
+        pk[q * 16 + e - 8] = pack_bf16(p.x, p.y);  // weights as bf16: see k_attn.cu
+      }
+    }
+  }
+  top = fmaxf(mx0, mx1) * c;
+  sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kTcAttnThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                    const TcAttnArgs a) {
   using Sh = TcAttnShape<D>;
-  constexpr int kStages = Sh::kStages;
+  constexpr int kSlots = Sh::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sq = smem;                       // Q of A and B
-  uint8_t* ring = smem + 2 * Sh::kTile;     // K, V, K, V, ...
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Sh::kTile);
-  uint64_t* empty = full + kStages;
-  uint64_t* s_full = empty + kStages;   // [2] S ready, and everything issued before it done
+  uint8_t* ring = smem + 2 * Sh::kTile;     // [slot] V, K
+  uint8_t* stage = ring + kSlots * 2 * Sh::kTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage + Sh::kStage);
+  uint64_t* empty = full + kSlots;
+  uint64_t* v_clean = empty + kSlots;   // [slot] edge values looked over (edge tiles only)
+  uint64_t* s_full = v_clean + kSlots;  // [2] S ready, and the P·V before it done
   uint64_t* p_full = s_full + 2;        // [2] P written
-  uint64_t* q_full = p_full + 2;
+  uint64_t* o_full = p_full + 2;        // [2] a segment's last P·V done
+  uint64_t* q_full = o_full + 2;
   uint64_t* q_empty = q_full + 1;
   uint64_t* mma_done = q_empty + 1;
-  uint64_t* v_clean = mma_done + 1;     // [kStages / 2] value stage looked over
-  volatile int* s_flag = reinterpret_cast<volatile int*>(full + 3 * kStages + 16);  // [0] abort
+  volatile int* s_flag = reinterpret_cast<volatile int*>(full + 3 * kSlots + 16);  // [0] abort
   volatile int* s_poison = s_flag + 4;  // [4] segment number + 1 with a non-finite edge value
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(const_cast<int*>(s_flag) + 8);
-  const SplitTables tab(reinterpret_cast<uint8_t*>(const_cast<int*>(s_flag)) + 128, a.p.batch);
+  const SplitTables tab(reinterpret_cast<uint8_t*>(const_cast<int*>(s_flag)) + 64, a.p.batch);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&v_clean[i], 1);
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 4);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_full[x], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int i = 0; i < kStages / 2; ++i) mbar_init(&v_clean[i], 1);
     mbar_init(mma_done, 1);
     s_flag[0] = 0;
     for (int i = 0; i < 4; ++i) s_poison[i] = 0;
@@ -134,11 +231,14 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   };
   // B has rows
   auto has_b = [&] { return tab.qn[w.b] - w.i * a.s.tq > a.tq; };
+  // The same result in all lanes: false once any wait of the CTA has run out.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (s_flag[0]) return false;
-    if (mbar_wait(bar, parity & 1, a.timeout_ns, a.p.status)) return true;
-    s_flag[0] = 1;
-    return false;
+    bool ok = true;
+    if (!mbar_try_wait(bar, parity & 1)) {
+      ok = !s_flag[0] && mbar_wait(bar, parity & 1, a.timeout_ns, a.p.status);
+      if (!ok) s_flag[0] = 1;
+    }
+    return __all_sync(~0u, ok);
   };
 
   if (warp == 9) {
@@ -146,22 +246,34 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     const uint64_t pol = policy_evict_last();
     const int rows = a.p.page < kTcKeys ? a.p.page : kTcKeys;
     const int pieces = kTcKeys / rows, page_mask = a.p.page - 1;
-    const int half = lane % (D / 64), piece = lane / (D / 64);
-    int it = 0, seg = 0;
+    const int half = lane % (D / 64), piece = (lane & 15) / (D / 64);
+    const bool vlane = lane >= 16;  // lanes 0-15 load keys, 16-31 the values of the tile before
+    int i = 0, seg = 0;
+    int pg_prev = -1, c1_prev = 0, h_prev = 0;   // the tile before: page, place in it, head
     bool ok = true;
-    for (; w.more() && ok; w.next(), ++seg) {
-      const bool two = has_b();
-      if (!__all_sync(~0u, seg == 0 || wait(q_empty, seg - 1))) break;
-      if (lane == 0) {
-        const uint32_t bytes = a.group * a.tq * 128;
-        mbar_arrive_expect_tx(q_full, bytes * (D / 64) * (two ? 2 : 1));
-        for (int x = 0; x < (two ? 2 : 1); ++x)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sq + x * Sh::kTile + h * Sh::kHalf, &qmap, h * 64, w.h * a.group,
-                        tab.q0[w.b] + w.i * a.s.tq + x * a.tq, q_full, pol);
-      }
+    // slot i: values of the tile before, keys of this one (pg < 0: none)
+    auto put = [&](int pg, int c1, int h) {
+      const int st = i % kSlots;
+      if (i >= kSlots && !wait(&empty[st], i / kSlots + 1)) return false;
+      const int vpg = __shfl_sync(~0u, pg_prev, lane & 15);
+      const int my = vlane ? vpg : pg;
+      const int n = __popc(__ballot_sync(~0u, my >= 0));
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], n * rows * 128);
       __syncwarp();
-      const int row = tab.row[w.b];
+      if (my >= 0)
+        tma_load_4d(ring + (st * 2 + (vlane ? 0 : 1)) * Sh::kTile + half * Sh::kHalf +
+                        piece * rows * 128,
+                    &kvmap, half * 64, vlane ? c1_prev : c1, vlane ? a.p.hkv + h_prev : h, my,
+                    &full[st], pol);
+      ++i;
+      pg_prev = pg;
+      c1_prev = c1;
+      h_prev = h;
+      return true;
+    };
+    for (; w.more() && ok; w.next()) {
+      const bool two = has_b();
+      const int row = paged_row(a.p, w.b);
       const int32_t* trow = a.p.table + (long long)(row < 0 ? 0 : row) * a.p.table_stride;
       auto page_at = [&](int j) -> int {
         const int pos = j * kTcKeys + piece * rows;
@@ -171,131 +283,165 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         if ((pg < 0 || pg >= a.p.pages) && a.p.status) atomicOr(a.p.status, kStatusBounds);
         return pg < 0 || pg >= a.p.pages ? a.p.pages : pg;
       };
-      int pg_next = page_at(w.j);
-      for (int k = 0; k < w.n && ok; ++k) {
-        const int j = w.j + k, pg = pg_next;
-        if (k + 1 < w.n) pg_next = page_at(j + 1);
-        const int n = __popc(__ballot_sync(~0u, pg >= 0));
-        for (int v = 0; v < 2; ++v, ++it) {
-          const int st = it % kStages;
-          if (it >= kStages && !wait(&empty[st], it / kStages + 1)) ok = false;
-          ok = __all_sync(~0u, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], n * rows * 128);
-          __syncwarp();
-          if (pg >= 0)
-            tma_load_4d(ring + st * Sh::kTile + half * Sh::kHalf + piece * rows * 128, &kvmap,
-                        half * 64, (j * kTcKeys + piece * rows) & page_mask, v * a.p.hkv + w.h, pg,
-                        &full[st], pol);
-        }
+      auto place = [&](int j) { return (j * kTcKeys + piece * rows) & page_mask; };
+      const int pg0 = page_at(w.j);
+      int pg_next = w.n > 1 ? page_at(w.j + 1) : -1;
+      // the first slot also brings the values that the segment before ends with
+      ok = put(pg0, place(w.j), w.h) && (seg == 0 || wait(q_empty, seg - 1));
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t bytes = a.group * a.tq * 128;
+        const int tok = paged_first(a.p, w.b) + w.i * a.s.tq;
+        mbar_arrive_expect_tx(q_full, bytes * (D / 64) * (two ? 2 : 1));
+        for (int x = 0; x < (two ? 2 : 1); ++x)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(sq + x * Sh::kTile + h * Sh::kHalf, &qmap, h * 64, w.h * a.group,
+                        tok + x * a.tq, q_full, pol);
+      }
+      ++seg;
+      __syncwarp();
+      for (int k = 1; k < w.n && ok; ++k) {
+        const int pg = pg_next;
+        if (k + 1 < w.n) pg_next = page_at(w.j + k + 1);
+        ok = put(pg, place(w.j + k), w.h);
       }
     }
+    if (ok && i > 0) put(-1, 0, 0);
     // the copies in flight land before the CTA's shared memory is given back
     if (lane == 0) {
       if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, drain_ns(a.timeout_ns), nullptr);
-      for (int st = 0; st < kStages && st < it; ++st)
-        mbar_wait(&full[st], ((it - st + kStages - 1) / kStages - 1) & 1, drain_ns(a.timeout_ns),
+      for (int st = 0; st < kSlots && st < i; ++st)
+        mbar_wait(&full[st], ((i - st + kSlots - 1) / kSlots - 1) & 1, drain_ns(a.timeout_ns),
                   nullptr);
     }
+    __syncwarp();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t qk_desc = umma_idesc_bf16(128, 128);
-      constexpr uint32_t pv_desc = umma_idesc_bf16(128, D) | kUmmaBMnMajor;
-      const uint32_t qa = smem_u32(sq), ra = smem_u32(ring);
-      auto qk = [&](int x, uint32_t kb) {
+    // One warp issues the MMAs of A and B in turn: from two warps they would
+    // interleave in the tensor cores' queue, A and B would finish together and
+    // the tensor cores idle while both do their softmax.
+    constexpr uint32_t qk_desc = umma_idesc_bf16(128, 128);
+    constexpr uint32_t pv_desc = umma_idesc_bf16(128, D) | kUmmaBMnMajor;
+    // descriptors: the low word holds the address (in 16-byte units)
+    const uint64_t kd = umma_desc_sw128(0), vd = umma_desc_sw128_mn(0, Sh::kHalf);
+    const uint32_t k_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32);
+    const uint32_t leader = elect_one();
+    const uint32_t tm = __shfl_sync(~0u, taddr, 0);
+    const uint32_t qa = __shfl_sync(~0u, (uint32_t)kd + (smem_u32(sq) >> 4), 0);
+    const uint32_t va = __shfl_sync(~0u, (uint32_t)vd + (smem_u32(ring) >> 4), 0);
+    const uint32_t ka = __shfl_sync(~0u, (uint32_t)kd + (smem_u32(ring + Sh::kTile) >> 4), 0);
+    auto qk = [&](auto x, int st) {
+      const uint32_t k = ka + st * (2 * Sh::kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * Sh::kHalf + (kk & 3) * 32;
-          umma_bf16(taddr + x * 128, umma_desc_sw128(qa + x * Sh::kTile + off),
-                    umma_desc_sw128(kb + off), qk_desc, kk > 0);
-        }
-      };
-      auto pv = [&](int x, uint32_t vb, bool first) {
-#pragma unroll
-        for (int kk = 0; kk < kTcKeys / 16; ++kk)
-          umma_bf16_ta(taddr + 256 + x * D, taddr + x * 128 + kk * 8,
-                       umma_desc_sw128_mn(vb + kk * 2048, Sh::kHalf), pv_desc, !first || kk > 0);
-      };
-      int it = 0, seg = 0;
-      uint32_t pn[2] = {0, 0};
-      bool ok = true;
-      for (; w.more() && ok; w.next(), ++seg) {
-        const int nx = has_b() ? 2 : 1;
-        ok = wait(q_full, seg) && wait(&full[it % kStages], it / kStages);
-        if (!ok) break;
-        tc_fence_after();
-        for (int x = 0; x < nx; ++x) {
-          qk(x, ra + (it % kStages) * Sh::kTile);
-          umma_commit(&s_full[x]);
-        }
-        umma_commit(&empty[it % kStages]);
-        if (w.n == 1) umma_commit(q_empty);
-        for (int k = 0; k < w.n && ok; ++k, it += 2) {
-          const int vs = it + 1, ks = it + 2;  // stages of V and of the next K
-          const bool more = k + 1 < w.n;
-          ok = wait(&full[vs % kStages], vs / kStages);
-          ok = ok && wait(&v_clean[vs % kStages / 2], vs / kStages);
-          for (int x = 0; x < nx && ok; ++x) {
-            ok = wait(&p_full[x], pn[x]++);
-            if (!ok) break;
-            tc_fence_after();
-            pv(x, ra + (vs % kStages) * Sh::kTile, k == 0);
-            if (more) {
-              if (x == 0) {
-                ok = wait(&full[ks % kStages], ks / kStages);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              qk(x, ra + (ks % kStages) * Sh::kTile);
-            }
-            umma_commit(&s_full[x]);
-          }
-          umma_commit(&empty[vs % kStages]);
-          if (more) umma_commit(&empty[ks % kStages]);
-          if (k + 2 == w.n) umma_commit(q_empty);  // the segment's last Q·Kᵀ
-        }
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * Sh::kHalf + (kk & 3) * 32) >> 4;
+        umma_bf16_elect(leader, tm + x * 128, qa + x * (Sh::kTile >> 4) + off, k_hi, k + off, k_hi,
+                        qk_desc, kk > 0);
       }
-      umma_commit(mma_done);
-      mbar_wait(mma_done, 0, drain_ns(a.timeout_ns), nullptr);
+    };
+    auto commit = [&](uint64_t* bar) { umma_commit_elect(leader, bar); };
+    const std::integral_constant<int, 0> A;
+    const std::integral_constant<int, 1> B;
+    int i = 0, seg = 0;
+    uint32_t pa = 0, pb = 0, clean = 0;  // phases: P of A and B; edge tiles of each slot
+    bool ok = w.more() && wait(&full[0], 0);
+#pragma unroll 1
+    for (; ok; w.next(), ++seg) {
+      // the segment's first Q·Kᵀ, while the output of the one before is read
+      ok = w.more() && wait(q_full, seg);
+      if (!ok) break;
+      tc_fence_after();
+      const bool two = has_b();
+      const EdgeRange er = edges();
+      qk(A, i % kSlots);
+      commit(&s_full[0]);
+      if (two) {
+        qk(B, i % kSlots);
+        commit(&s_full[1]);
+      }
+      commit(&empty[i % kSlots]);
+      if (w.n == 1) commit(q_empty);
+#pragma unroll 1
+      for (int k = 0; k < w.n; ++k) {
+        ++i;  // the slot with this tile's values and the next tile's keys
+        const int st = i % kSlots, key0 = (w.j + k) * kTcKeys;
+        const bool more = k + 1 < w.n, edge = er.in(key0, kTcKeys);
+        const uint32_t v = va + st * (2 * Sh::kTile >> 4), first = k == 0 ? 0u : 1u;
+        auto step = [&](auto x) {
+          tc_fence_after();
+          const uint32_t ts = tm + x * 128, to = tm + 256 + x * D;
+          if (!edge) {
+#pragma unroll
+            for (int kk = 0; kk < kTcKeys / 16; ++kk)
+              umma_bf16_ta_elect(leader, to, ts + kk * 8, v + kk * (2048 >> 4), v_hi, pv_desc,
+                                 kk > 0 ? 1u : first);
+          } else {
+            int k0, k1;
+            edge_steps(er, key0, k0, k1);
+#pragma unroll 1
+            for (int kk = k0; kk < k1; ++kk)
+              umma_bf16_ta_elect(leader, to, ts + kk * 8, v + kk * (2048 >> 4), v_hi, pv_desc,
+                                 kk > k0 ? 1u : first);
+          }
+          if (more) qk(x, st);
+          commit(more ? &s_full[x] : &o_full[x]);
+        };
+        ok = wait(&full[st], i / kSlots);
+        if (edge) {
+          ok = ok && wait(&v_clean[st], clean >> st);
+          clean ^= 1u << st;
+        }
+        if (!ok || !(ok = wait(&p_full[0], pa++))) break;
+        step(A);
+        if (two) {
+          if (!(ok = wait(&p_full[1], pb++))) break;
+          step(B);
+        }
+        if (more) commit(&empty[st]);
+        if (k + 2 == w.n) commit(q_empty);  // the segment's last Q·Kᵀ
+      }
     }
+    commit(mma_done);
+    mbar_wait(mma_done, 0, drain_ns(a.timeout_ns), nullptr);
     __syncwarp();
   } else if (warp == 10) {
     // ---------------------------------------------------------------- edge values
-    int it = 0, seg = 0;
+    int i = 0, seg = 0;
     bool ok = true;
     for (; w.more() && ok; w.next(), ++seg) {
       const EdgeRange er = edges();
-      for (int k = 0; k < w.n && ok; ++k, it += 2) {
-        const int key0 = (w.j + k) * kTcKeys, vs = it + 1;
+      for (int k = 0; k < w.n && ok; ++k) {
+        ++i;
+        const int key0 = (w.j + k) * kTcKeys, st = i % kSlots;
         // every tile is waited for, edge or not: a phase cannot be told from
         // the one two later
-        ok = __all_sync(~0u, wait(&full[vs % kStages], vs / kStages));
-        if (!ok) break;
-        uint64_t* done = &v_clean[vs % kStages / 2];
-        if (!er.in(key0, kTcKeys)) {
-          if (lane == 0) mbar_arrive(done);
-          continue;
-        }
-        uint8_t* v = ring + (vs % kStages) * Sh::kTile;
+        ok = wait(&full[st], i / kSlots);
+        if (!ok || !er.in(key0, kTcKeys)) continue;
+        uint8_t* v = ring + st * 2 * Sh::kTile;
+        int k0, k1;
+        edge_steps(er, key0, k0, k1);
         bool found = false;
-        auto clean = [&](int from, int to) {  // keys of the tile
+        auto clean = [&](int from, int to) {  // positions of the tile
+#pragma unroll 4
           for (int x = from * (D / 8) + lane; x < to * (D / 8); x += 32) {
-            const int key = x / (D / 8), ch = x % (D / 8), pos = key0 + key;
-            uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * Sh::kHalf + key * 128 +
-                                                 (((ch & 7) ^ (key & 7)) << 4));
-            found |= clean_edge_value(at, er, pos);
+            const int key = x / (D / 8), ch = x % (D / 8);
+            found |= clean_edge_value(
+                reinterpret_cast<uint4*>(v + (ch >> 3) * Sh::kHalf + key * 128 +
+                                         (((ch & 7) ^ (key & 7)) << 4)),
+                er, key0 + key);
           }
         };
-        const int lo_end = er.all_lo - key0 < 0 ? 0 : (er.all_lo - key0 < kTcKeys ? er.all_lo - key0 : kTcKeys);
-        int hi_from = er.all_hi - key0 < 0 ? 0 : (er.all_hi - key0 < kTcKeys ? er.all_hi - key0 : kTcKeys);
-        if (hi_from < lo_end) hi_from = lo_end;
-        clean(0, lo_end);
-        clean(hi_from, kTcKeys);
+        auto within = [&](int pos) {
+          const int n = pos - key0;
+          return n < k0 * 16 ? k0 * 16 : (n > k1 * 16 ? k1 * 16 : n);
+        };
+        const int lo_end = within(er.all_lo);
+        clean(k0 * 16, lo_end);
+        clean(within(er.all_hi > er.all_lo ? er.all_hi : er.all_lo), k1 * 16);
         if (__any_sync(~0u, found) && lane == 0) s_poison[seg & 3] = seg + 1;
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(done);
+        if (lane == 0) mbar_arrive(&v_clean[st]);
       }
     }
   } else if (warp < 8) {
@@ -303,7 +449,9 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     const int x = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = taddr + lanes + x * 128, to = taddr + lanes + 256 + x * D;
-    uint32_t sn = 0;
+    const int t = r / a.group, g = r - t * a.group;
+    uint8_t* mine = stage + warp * 2048;
+    uint32_t sn = 0, on = 0;
     int seg = 0;
     bool ok = true;
     for (; w.more() && ok; w.next(), ++seg) {
@@ -312,7 +460,6 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       const int qn = tab.qn[w.b];
       const int t0 = w.i * a.s.tq + x * a.tq;
       const int nt = qn - t0 < a.tq ? qn - t0 : a.tq;
-      const int t = r / a.group, g = r - t * a.group;
       const bool live = t < nt;
       const int pos = tab.kv[w.b] - qn + t0 + t;
       const int hi = live ? pos : -1;
@@ -320,83 +467,74 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < w.n; ++k) {
         const int key0 = (w.j + k) * kTcKeys;
-        ok = __all_sync(~0u, wait(&s_full[x], sn++));
+        ok = wait(&s_full[x], sn++);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s + q * 32);
-        tmem_ld_wait();
-        tmem_settle<128>(s);
-        if (er.in(key0, kTcKeys)) {
-          const int h0 = hi - key0, l0 = lo - key0;
-#pragma unroll
-          for (int q = 0; q < 128; ++q)
-            if (q > h0 || q < l0) s[q] = 0xFF800000u;  // -inf
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int q = 0; q < 128; ++q) mx[q & 3] = fmaxf(mx[q & 3], __uint_as_float(s[q]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
-        if (__any_sync(~0u, top > m + kTcLazy)) {
+        // One pass over the row with the maximum of the tiles before: weights,
+        // their sum and the row's own maximum. If that has outgrown m the pass
+        // is made again with the new one: S stays in TMEM until the weights
+        // replace it. A segment's first tile starts from the maximum of its
+        // first 32 columns.
+        if (er.in(key0, kTcKeys)) row_mask(ts, lo - key0, hi - key0);
+        uint32_t pk[64];
+        float top, sum;
+        if (k == 0) m = row_start(ts, a.c);
+#pragma unroll 1
+        for (;;) {
+          row_pass(ts, a.c, m == -INFINITY ? 0.f : m, pk, top, sum);
+          if (!__any_sync(~0u, top > m + kTcLazy)) break;
           // m was -inf before the first visible position: O and l are 0 then
           const float mn = fmaxf(m, top);
           const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
           m = mn;
           l *= f;
-          if (k > 0) {
+          if (k == 0) continue;
+#pragma unroll 1
+          for (int q = 0; q < D; q += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + q, o);
+            tmem_ld_wait();
+            tmem_settle<32>(o);
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(to + q * 32, o);
-              tmem_ld_wait();
-              tmem_settle<32>(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(to + q * 32, o);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(to + q, o);
           }
         }
-        const float mb = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 128; q += 2) {
-          const float p0 = exp2_approx(fmaf(__uint_as_float(s[q]), a.c, -mb));
-          const float p1 = exp2_approx(fmaf(__uint_as_float(s[q + 1]), a.c, -mb));
-          sum[(q >> 1) & 1] += p0;
-          sum[2 + ((q >> 1) & 1)] += p1;
-          // weights as bf16: see k_attn.cu
-          s[q >> 1] = pack_bf16(p0, p1);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st32(ts, s);
-        tmem_st32(ts + 32, s + 32);
+        l += sum;
+        tmem_st32(ts, pk);
+        tmem_st32(ts + 32, pk + 32);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
-      ok = __all_sync(~0u, wait(&s_full[x], sn++));
+      ok = wait(&o_full[x], on++);
       if (!ok) break;
       tc_fence_after();
       // rows that see a non-finite edge value get it here
       const bool poison = s_poison[seg & 3] == seg + 1;
-      const int row = tab.row[w.b];
-      const long long tok = tab.q0[w.b] + t0 + t;
-      const int head = w.h * a.group + g;
       const long long slot = (long long)blockIdx.x * 2 + (w.tile_unit() >= u0 ? 1 : 0);
-      float* part = a.ws + slot * Sh::kSlot + x * kTcRowsA * (D + 2);
+      float* part = a.ws + slot * Sh::kPart + x * kTcRowsA * (D + 2);
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+      // rows that this lane writes, four lanes to a row: 64 bytes of it at a time
+      uint16_t* dst[4];
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
+      for (int e = 0; e < 4; ++e) {
+        const int row = (warp & 3) * 32 + e * 8 + (lane >> 2), tt = row / a.group;
+        dst[e] = tt >= nt ? nullptr
+                          : a.out + (paged_first(a.p, w.b) + t0 + tt) * a.ldo +
+                                (long long)(w.h * a.group + row - tt * a.group) * D + (lane & 3) * 8;
+      }
+#pragma unroll 1
+      for (int q = 0; q < D; q += 32) {
         uint32_t o[32];
-        tmem_ld32(to + q * 32, o);
+        tmem_ld32(to + q, o);
         tmem_ld_wait();
         tmem_settle<32>(o);
-        if (poison && live && row >= 0) {
-          edge_values<D>(a.p, row, w.h, er, lo, hi, w.j * kTcKeys, (w.j + w.n) * kTcKeys, q * 32,
-                         [&](const uint16_t* v) {
+        if (poison && live) {
+          edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, lo, hi, w.j * kTcKeys,
+                         (w.j + w.n) * kTcKeys, q, [&](const uint16_t* v) {
 #pragma unroll
                            for (int e = 0; e < 32; ++e) {
                              const float f = bf_bits2f(__ldg(v + e));
@@ -405,25 +543,33 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
                          });
         }
         if (w.whole) {
-          if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + tok * a.ldo + (long long)head * D + q * 32);
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t* v = o + e * 8;
-              auto at = [&](int i) { return __uint_as_float(v[i]) * inv; };
-              dst[e] = make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
-                                  pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
-            }
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t* v = o + e * 8;
+            auto at = [&](int n) { return __uint_as_float(v[n]) * inv; };
+            *reinterpret_cast<uint4*>(mine + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) =
+                make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
+                           pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int rr = e * 8 + (lane >> 2);
+            if (dst[e])
+              *reinterpret_cast<uint4*>(dst[e] + q) = *reinterpret_cast<const uint4*>(
+                  mine + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
           }
         } else {
+          float* col = DG_AT(a.p.status, part, q * kTcRowsA + r, Sh::kPart - 31 * kTcRowsA);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            __stcg(DG_AT(a.p.status, part, (q * 32 + e) * kTcRowsA + r, Sh::kSlot), __uint_as_float(o[e]));
+          for (int e = 0; e < 32; ++e) __stcg(col + e * kTcRowsA, __uint_as_float(o[e]));
         }
       }
       if (w.whole) {
         if (live && a.lse)
-          a.lse[tok * a.hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          a.lse[(paged_first(a.p, w.b) + t0 + t) * (long long)a.hq + w.h * a.group + g] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       } else {
         __stcg(part + D * kTcRowsA + r, m);
         __stcg(part + (D + 1) * kTcRowsA + r, l);
@@ -441,7 +587,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       if (!f.whole && f.tile_unit() >= u0) {
         const int qn = tab.qn[f.b], t0 = f.i * a.s.tq;
         n = (int)(cta_of(f.tile_unit() + f.tr.n - 1, W, G) - blockIdx.x + 1);
-        q0 = tab.q0[f.b] + t0;
+        q0 = paged_first(a.p, f.b) + t0;
         rows = (qn - t0 < a.s.tq ? qn - t0 : a.s.tq);
         h = f.h;
       }
@@ -472,7 +618,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const TcAttnArgs a) {
   const int t = r / a.group, g = r - t * a.group, tt = x * a.tq + t;
   if (n == 0 || t >= a.tq || tt >= s.z) return;
   auto part = [&](int k) -> const float* {
-    return a.ws + ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kSlot + x * kTcRowsA * (D + 2) + r;
+    return a.ws + ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kPart + x * kTcRowsA * (D + 2) + r;
   };
   float M = -INFINITY;
 #pragma unroll 8

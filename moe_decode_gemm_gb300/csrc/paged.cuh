@@ -86,6 +86,12 @@ __device__ __forceinline__ void paged_tokens(const PagedArgs& p, int b, int& q0,
   if ((a != q0 || e != q1) && p.status) atomicOr(p.status, kStatusBounds);
 }
 
+// First token of sequence b.
+__device__ __forceinline__ int paged_first(const PagedArgs& p, int b) {
+  const int a = __ldg(p.cu_q + b);
+  return a < 0 ? 0 : (a > p.tokens ? p.tokens : a);
+}
+
 // ------------------------------------------------------------------ the split
 struct SplitShape {
   int tq;        // tokens of a row tile
@@ -183,22 +189,18 @@ __device__ __forceinline__ void edge_values(const PagedArgs& p, int row, int h, 
 struct SplitTables {
   long long* base;   // [batch + 1] first unit of each sequence
   long long* wsum;   // [32] scan scratch
-  int* q0;           // [batch]
-  int* qn;
-  int* kv;
-  int* row;
+  int* qn;           // [batch] new tokens
+  int* kv;           // positions
   int* loc;          // [4] this CTA's first sequence, head, row tile, key tile in it
   static __host__ __device__ constexpr int bytes(int batch) {
-    return 8 * (batch + 1) + 8 * 32 + 16 * batch + 16;
+    return 8 * (batch + 1) + 8 * 32 + 8 * batch + 16;
   }
   __device__ explicit SplitTables(void* smem, int batch) {
     base = reinterpret_cast<long long*>(smem);
     wsum = base + batch + 1;
-    q0 = reinterpret_cast<int*>(wsum + 32);
-    qn = q0 + batch;
+    qn = reinterpret_cast<int*>(wsum + 32);
     kv = qn + batch;
-    row = kv + batch;
-    loc = row + batch;
+    loc = kv + batch;
   }
 };
 
@@ -217,10 +219,8 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     paged_tokens(p, b, q0, qn);
     const int row = paged_row(p, b);
     const int kv = paged_len(p, row);
-    t.q0[b] = q0;
     t.qn[b] = qn;
     t.kv[b] = kv;
-    t.row[b] = row;
     const int tiles = (qn + s.tq - 1) / s.tq;
     long long u = 0;
     if (tiles <= kFew)
