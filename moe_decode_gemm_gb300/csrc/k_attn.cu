@@ -445,7 +445,8 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
   a.ctr = ctr;
   a.ws_len = cx.ws_len;
   a.ctr_len = (int)cx.ctr_len;
-  a.min_units = 4;
+  a.s.start = 3;
+  a.min_units = 7;
   a.timeout_ns = cx.timeout_ns;
   const bool d64 = v.dim == 64;
   if (rt == 1) return d64 ? launch_rt<64, 1>(cx, map, a, cx.sms) : launch_rt<128, 1>(cx, map, a, cx.sms);

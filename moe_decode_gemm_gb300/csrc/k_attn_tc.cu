@@ -509,70 +509,93 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
+      // while the last P·V runs: where the rows go and their sums. Four lanes
+      // write a row, 64 bytes of it at a time.
+      const long long tok0 = paged_first(a.p, w.b) + t0;
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+      const long long slot = (long long)blockIdx.x * 2 + (w.tile_unit() >= u0 ? 1 : 0);
+      float* part = a.ws + slot * Sh::kPart + x * kTcRowsA * (D + 2) + r;
+      uint16_t* dst[4];
+      if (w.whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = (warp & 3) * 32 + e * 8 + (lane >> 2), tt = row / a.group;
+          dst[e] = tt >= nt ? nullptr
+                            : a.out + (tok0 + tt) * a.ldo +
+                                  (long long)(w.h * a.group + row - tt * a.group) * D + (lane & 3) * 8;
+        }
+        if (live && a.lse)
+          a.lse[(tok0 + t) * a.hq + w.h * a.group + g] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      } else {
+        __stcg(part + D * kTcRowsA, m);
+        __stcg(part + (D + 1) * kTcRowsA, l);
+      }
       ok = wait(&o_full[x], on++);
       if (!ok) break;
       tc_fence_after();
-      // rows that see a non-finite edge value get it here
-      const bool poison = s_poison[seg & 3] == seg + 1;
-      const long long slot = (long long)blockIdx.x * 2 + (w.tile_unit() >= u0 ? 1 : 0);
-      float* part = a.ws + slot * Sh::kPart + x * kTcRowsA * (D + 2);
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
-      // rows that this lane writes, four lanes to a row: 64 bytes of it at a time
-      uint16_t* dst[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = (warp & 3) * 32 + e * 8 + (lane >> 2), tt = row / a.group;
-        dst[e] = tt >= nt ? nullptr
-                          : a.out + (paged_first(a.p, w.b) + t0 + tt) * a.ldo +
-                                (long long)(w.h * a.group + row - tt * a.group) * D + (lane & 3) * 8;
-      }
+      if (s_poison[seg & 3] == seg + 1) {
+        // rows that see a non-finite edge value get it here
 #pragma unroll 1
-      for (int q = 0; q < D; q += 32) {
-        uint32_t o[32];
-        tmem_ld32(to + q, o);
-        tmem_ld_wait();
-        tmem_settle<32>(o);
-        if (poison && live) {
-          edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, lo, hi, w.j * kTcKeys,
-                         (w.j + w.n) * kTcKeys, q, [&](const uint16_t* v) {
+        for (int q = 0; q < D; q += 16) {
+          uint32_t o[16];
+          tmem_ld16(to + q, o);
+          tmem_ld_wait();
+          tmem_settle<16>(o);
+          if (live)
+            edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, lo, hi, w.j * kTcKeys,
+                           (w.j + w.n) * kTcKeys, q, [&](const uint16_t* v) {
 #pragma unroll
-                           for (int e = 0; e < 32; ++e) {
-                             const float f = bf_bits2f(__ldg(v + e));
-                             if (!isfinite(f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
-                           }
-                         });
+                             for (int e = 0; e < 16; ++e) {
+                               const float f = bf_bits2f(__ldg(v + e));
+                               if (!isfinite(f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
+                             }
+                           });
+          __syncwarp();
+          tmem_st16(to + q, o);
         }
-        if (w.whole) {
-          __syncwarp();
+        tmem_st_wait();
+      }
+      if (w.whole) {
+#pragma unroll 1
+        for (int q = 0; q < D; q += 64) {
+          uint32_t o[64];
+          tmem_ld32(to + q, o);
+          tmem_ld32(to + q + 32, o + 32);
+          tmem_ld_wait();
+          tmem_settle<64>(o);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t* v = o + e * 8;
-            auto at = [&](int n) { return __uint_as_float(v[n]) * inv; };
-            *reinterpret_cast<uint4*>(mine + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) =
-                make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
-                           pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
-          }
-          __syncwarp();
+          for (int hh = 0; hh < 2; ++hh) {
+            __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int rr = e * 8 + (lane >> 2);
-            if (dst[e])
-              *reinterpret_cast<uint4*>(dst[e] + q) = *reinterpret_cast<const uint4*>(
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* v = o + hh * 32 + e * 8;
+              auto at = [&](int n) { return __uint_as_float(v[n]) * inv; };
+              *reinterpret_cast<uint4*>(mine + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) =
+                  make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
+                             pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int rr = e * 8 + (lane >> 2);
+              const uint4 v = *reinterpret_cast<const uint4*>(
                   mine + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
+              if (dst[e]) *reinterpret_cast<uint4*>(dst[e] + q + hh * 32) = v;
+            }
           }
-        } else {
-          float* col = DG_AT(a.p.status, part, q * kTcRowsA + r, Sh::kPart - 31 * kTcRowsA);
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < D; q += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + q, o);
+          tmem_ld_wait();
+          tmem_settle<32>(o);
+          float* col = DG_AT(a.p.status, part, q * kTcRowsA, Sh::kPart - 31 * kTcRowsA);
 #pragma unroll
           for (int e = 0; e < 32; ++e) __stcg(col + e * kTcRowsA, __uint_as_float(o[e]));
         }
-      }
-      if (w.whole) {
-        if (live && a.lse)
-          a.lse[(paged_first(a.p, w.b) + t0 + t) * (long long)a.hq + w.h * a.group + g] =
-              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      } else {
-        __stcg(part + D * kTcRowsA + r, m);
-        __stcg(part + (D + 1) * kTcRowsA + r, l);
       }
       // O is read: P of the next segment may be followed by its first P·V
       tc_fence_before();
@@ -681,7 +704,8 @@ cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, vo
   a.c = c.scale * 1.4426950408889634f;
   a.split = static_cast<int*>(ws);
   a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + (size_t)cx.sms * 16);
-  a.min_units = 2;
+  a.s.start = 2;
+  a.min_units = 4;
   a.timeout_ns = cx.timeout_ns;
   // few pairs, each split over many CTAs: spread each join over more blocks
   const long long pairs = ((long long)c.tokens / a.s.tq + v.batch) * v.hkv;

@@ -10,10 +10,11 @@
 //
 // Work is counted in units: one key tile (BN positions) read for one row tile
 // (tq tokens x the query heads that share a key head) of one sequence and key
-// head. The units of a call, in the order sequence, key head, row tile, key
-// tile, are cut into equal contiguous ranges, one per CTA; a row tile that
-// spans several ranges is finished by the last of its CTAs to arrive, which
-// joins the partial softmax states in CTA order.
+// head, and `start` more at the beginning of each row tile for what it costs
+// whatever its length (queries in, output out). The units of a call, in the
+// order sequence, key head, row tile, key tile, are cut into equal contiguous
+// ranges, one per CTA; the partial softmax states of a row tile that spans
+// several ranges are joined in CTA order.
 #pragma once
 
 #include "dg_common.cuh"
@@ -98,6 +99,7 @@ struct SplitShape {
   int bn_shift;  // log2 of the key tile
   int window;    // 0: none
   int hkv;
+  int start;     // units of a row tile before its first key tile
 };
 
 // Key tiles [j0, j0 + n) of row tile i of a sequence with qn new tokens and kv
@@ -191,9 +193,9 @@ struct SplitTables {
   long long* wsum;   // [32] scan scratch
   int* qn;           // [batch] new tokens
   int* kv;           // positions
-  int* loc;          // [4] this CTA's first sequence, head, row tile, key tile in it
+  int* loc;          // [4] this CTA's first sequence, head, row tile, unit in it; row tiles
   static __host__ __device__ constexpr int bytes(int batch) {
-    return 8 * (batch + 1) + 8 * 32 + 8 * batch + 16;
+    return 8 * (batch + 1) + 8 * 32 + 8 * batch + 24;
   }
   __device__ explicit SplitTables(void* smem, int batch) {
     base = reinterpret_cast<long long*>(smem);
@@ -212,6 +214,8 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
                                             const SplitTables& t, int min_units, long long& W,
                                             long long& G, long long& u0, long long& u1) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) t.loc[4] = 0;
+  __syncthreads();
   constexpr int kFew = 4;  // row tiles of a sequence that one thread counts by itself
   // units of each sequence and head, into base[b + 1]
   for (int b = tid; b < p.batch; b += NT) {
@@ -224,15 +228,16 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     const int tiles = (qn + s.tq - 1) / s.tq;
     long long u = 0;
     if (tiles <= kFew)
-      for (int i = 0; i < tiles; ++i) u += tile_range(s, qn, kv, i).n;
+      for (int i = 0; i < tiles; ++i) u += tile_range(s, qn, kv, i).n + s.start;
     t.base[b + 1] = u;
+    if (tiles) atomicAdd(&t.loc[4], tiles);
   }
   __syncthreads();
   for (int b = warp; b < p.batch; b += NT / 32) {
     const int qn = t.qn[b], tiles = (qn + s.tq - 1) / s.tq;
     if (tiles <= kFew) continue;
     long long u = 0;
-    for (int i = lane; i < tiles; i += 32) u += tile_range(s, qn, t.kv[b], i).n;
+    for (int i = lane; i < tiles; i += 32) u += tile_range(s, qn, t.kv[b], i).n + s.start;
 #pragma unroll
     for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(~0u, u, o);
     if (lane == 0) t.base[b + 1] = u;
@@ -265,7 +270,9 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
   if (tid == 0) t.base[0] = 0;
   __syncthreads();
   W = t.base[p.batch];
+  // no more CTAs than give each min_units, but one for each row tile
   G = W / min_units;
+  if (G < (long long)t.loc[4] * s.hkv) G = (long long)t.loc[4] * s.hkv;
   if (G < 1) G = 1;
   if (G > (long long)gridDim.x) G = gridDim.x;
   const long long c = blockIdx.x;
@@ -287,7 +294,7 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     const int qn = t.qn[b], kv = t.kv[b];
     for (;; i += 32) {
       // past the last row tile the ranges are not used: off ends before them
-      const int n = tile_range(s, qn, kv, i + lane).n;
+      const int n = tile_range(s, qn, kv, i + lane).n + s.start;
       int sum = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -319,10 +326,11 @@ struct SplitWalk {
   const SplitShape& s;
   const SplitTables& t;
   long long u, u1;
-  int b, h, i, off;
+  int b, h, i, off;     // position: sequence, head, row tile, unit in it
   // the current segment
   TileRange tr;
-  int j, n;             // key tiles [j, j + n)
+  int step;             // units of it
+  int j, n;             // key tiles [j, j + n), n >= 1
   bool whole;           // covers its row tile
   __device__ SplitWalk(const SplitShape& s_, const SplitTables& t_, long long u0, long long u1_)
       : s(s_), t(t_), u(u0), u1(u1_), b(0), h(0), i(0), off(0) {
@@ -337,16 +345,19 @@ struct SplitWalk {
   __device__ bool more() const { return u < u1; }
   __device__ void load() {
     tr = tile_range(s, t.qn[b], t.kv[b], i);
-    j = tr.j0 + off;
     const long long left = u1 - u;
-    n = tr.n - off;
-    if (left < n) n = (int)left;
+    step = tr.n + s.start - off;
+    if (left < step) step = (int)left;
+    const int first = off > s.start ? off - s.start : 0;
+    j = tr.j0 + first;
+    n = off + step - s.start - first;
     whole = n == tr.n;
+    if (n <= 0) u = u1;  // the range ends before this row tile's first key tile
   }
-  // first unit of the current row tile
-  __device__ long long tile_unit() const { return u - off; }
+  // the unit of the current row tile's first key tile
+  __device__ long long tile_unit() const { return u - off + s.start; }
   __device__ void next() {
-    u += n;
+    u += step;
     if (u >= u1) return;
     // the CTA's range goes on, so the row tile has ended
     off = 0;
