@@ -57,23 +57,22 @@ static int attention(const dec_kv_view* kv, const AttnCall& c, void* stream) {
   Ctx cx;
   void* ws;
   int* ctr;
-  // Rows (token, query head) of the longest chunk. tcgen05 above 64: a key tile
-  // then serves several mma.sync row tiles and the products bound the call. A
-  // scale of 0 or below (whose maximum is not the scaled maximum) stays on
-  // mma.sync, which scales before it compares.
+  // Rows (token, query head) of the longest chunk: up to 32 on mma.sync, in
+  // row tiles of 16 or 32; above that tcgen05. 8 sequences of 4 tokens (56 rows)
+  // over 512 / 2048 / 8192 positions: 30 / 39 / 73 us in mma.sync row tiles of 64,
+  // 18 / 21 / 43 on tcgen05; of 2 tokens (28 rows) over 64 / 2048: 9.4 / 24
+  // against 13 / 21.
   const int64_t rows = (int64_t)(kv->max_q > 0 ? kv->max_q : c.tokens) * group;
-  bool tc = rows > 64;
+  bool tc = rows > 32;
   const char* force = std::getenv("DEC_FORCE");
-  if (force && !std::strcmp(force, "mma")) tc = false;
+  if (force && !std::strcmp(force, "mma") && group <= 32) tc = false;
   if (force && !std::strcmp(force, "tc")) tc = true;
-  if (tc && c.scale > 0.f) {
+  if (tc) {
     if ((rc = kv_context(stream, attn_tc_ws(v.dim, sms), 0, &cx, &ws, nullptr))) return rc;
     t_last_attention = DEC_REGIME_TC;
     return result(launch_attn_tc(cx, v, c, ws), 2);
   }
-  // the smallest row tile that holds them, at most 64 rows: longer chunks take
-  // several
-  const int rt = rows <= 16 && group <= 16 ? 1 : (rows <= 32 && group <= 32 ? 2 : 4);
+  const int rt = rows <= 16 && group <= 16 ? 1 : 2;
   if ((rc = kv_context(stream, attn_mma_ws(v.dim, rt, sms), sms, &cx, &ws, &ctr))) return rc;
   t_last_attention = DEC_REGIME_MMA;
   return result(launch_attn_mma(cx, v, rt, c, static_cast<float*>(ws), ctr), 1);

@@ -1,5 +1,5 @@
 // k_attn.cu -- attention of a batch's new tokens over a paged cache for row
-// tiles of up to 64 rows (decode, draft tokens, short chunks), on mma.sync.
+// tiles of up to 32 rows (decode, a few draft tokens), on mma.sync.
 //
 //   s_j = scale * q·k_j,  p_j = exp(s_j - m),  o = sum_j p_j v_j / sum_j p_j,
 //   lse = m + log sum_j p_j      over the positions j that a token sees:
@@ -12,8 +12,8 @@
 // memory, and the matrix instructions only have to keep up with it.
 //
 // One producer warp brings key tiles of 64 positions (keys and values) into a
-// ring of shared-memory stages by TMA, page by page. The 4*RT (2*RT at RT = 4)
-// consumer warps split each tile's positions among them; every one keeps the
+// ring of shared-memory stages by TMA, page by page. The four consumer warps
+// split the row tile (16 rows a warp) and each tile's positions; every one keeps the
 // running maximum, sum and output of its own positions in registers, so that
 // the main loop has no barrier between warps, and they are joined once at the
 // end of a segment. Work over all sequences is cut into equal ranges (see
@@ -24,8 +24,8 @@
 
 namespace dg {
 
-constexpr int kAttnKeys = 64;  // positions of a key tile
-constexpr int kAttnKeysShift = 6;
+constexpr int attn_keys_shift(int dim) { return dim == 64 ? 7 : 6; }
+constexpr int kClusterTiles = 16;   // row tiles up to which clusters are used
 
 struct AttnArgs {
   PagedArgs p;
@@ -44,40 +44,86 @@ struct AttnArgs {
   long long timeout_ns;
 };
 
-template <int D, int RT>
+template <int D, int RT, int CL>
 struct AttnShape {
-  static constexpr int kKS = RT == 4 ? 2 : 4;          // warps that share a row tile's positions
+  static constexpr int kKeys = 1 << attn_keys_shift(D);  // positions of a key tile: 16 KB of keys
+  // warps that share a row tile's positions: 8 warps of 32 positions for two row
+  // tiles of 64 columns; of 128 columns the registers allow 4 warps
+  static constexpr int kKS = RT == 2 && D == 128 ? 2 : 4;
+  static constexpr int kBlk = kKeys / kKS;             // positions of a warp at a time: 16 or 32
   static constexpr int kWarps = RT * kKS;
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kRows = 16 * RT;
-  static constexpr int kHalf = kAttnKeys * 128;        // 64 columns of a tile's keys or values
-  static constexpr int kKBytes = kAttnKeys * D * 2;
+  static constexpr int kHalf = kKeys * 128;        // 64 columns of a tile's keys or values
+  static constexpr int kKBytes = kKeys * D * 2;
   static constexpr int kStage = 2 * kKBytes;
-  static constexpr int kStages = 128 * 1024 / kStage;
+  static constexpr int kStages = (CL > 1 ? 96 : 128) * 1024 / kStage;
   static constexpr int kLd = D + 8;                    // floats between rows of the join scratch
   static constexpr int kScratch = kWarps * 16 * kLd * 4 + kWarps * 16 * 8;
-  static constexpr int kSlot = kRows * (D + 2);        // floats of a partial tile
+  static constexpr int kItems = kRows * (D / 4);       // four columns of a row each
+  static constexpr int kSlot = kItems * 6;             // floats of a partial tile: o, then m and l
+  static constexpr int kMerged = CL > 1 ? kRows * (D + 2) * 4 : 0;  // a CTA's part of a cluster's tile
   static int smem(int batch) {
-    return 1024 + kStages * kStage + kScratch + 2 * kStages * 8 + 64 + SplitTables::bytes(batch) + 16;
+    return 1024 + kStages * kStage + kScratch + 2 * kMerged + (2 * kStages + 1) * 8 + 64 +
+           SplitTables::bytes(batch) + 16;
   }
 };
 
-template <int D, int RT>
-__global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
+// Joins two partial softmax states (v, m, l): exact but for the rounding of the
+// factors; a state that has seen nothing (m = -inf) changes nothing.
+struct State {
+  float4 v;
+  float m, l;
+  __device__ void add(float4 v2, float m2, float l2) {
+    const float M = fmaxf(m, m2);
+    const float f = M == -INFINITY ? 1.f : exp2_approx(m - M);
+    const float g = M == -INFINITY ? 1.f : exp2_approx(m2 - M);
+    v.x = v.x * f + v2.x * g;
+    v.y = v.y * f + v2.y * g;
+    v.z = v.z * f + v2.z * g;
+    v.w = v.w * f + v2.w * g;
+    l = l * f + l2 * g;
+    m = M;
+  }
+};
+
+// Non-finite values at the edge that the row at position p sees, in columns d ..
+// d + 3 of the key tile at key0 (out of line: it hardly ever runs).
+template <int D>
+__device__ __noinline__ void add_edge_values(const PagedArgs& p, int window, int b, int h,
+                                             const EdgeRange& er, int pos, int key0, int d, State& s) {
+  edge_values<D>(p, paged_row(p, b), h, er, window > 0 ? pos - window + 1 : 0, pos, key0,
+                 key0 + (1 << attn_keys_shift(D)), d, [&](const uint16_t* e) {
+                   const uint2 pk = __ldg(reinterpret_cast<const uint2*>(e));
+                   const float f[4] = {bf16lo(pk.x), bf16hi(pk.x), bf16lo(pk.y), bf16hi(pk.y)};
+                   if (!isfinite(f[0])) s.v.x += f[0];
+                   if (!isfinite(f[1])) s.v.y += f[1];
+                   if (!isfinite(f[2])) s.v.z += f[2];
+                   if (!isfinite(f[3])) s.v.w += f[3];
+                 });
+}
+
+template <int D, int RT, int CL>
+__global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
     attn_mma_kernel(const __grid_constant__ CUtensorMap kvmap, const AttnArgs a) {
-  using Sh = AttnShape<D, RT>;
+  using Sh = AttnShape<D, RT, CL>;
   constexpr int kKS = Sh::kKS, kStages = Sh::kStages, kWarps = Sh::kWarps;
   constexpr int kCons = kWarps * 32;
+  constexpr int kKeys = Sh::kKeys, kBlk = Sh::kBlk;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   float* scratch = reinterpret_cast<float*>(smem + kStages * Sh::kStage);
   float* sc_ml = scratch + kWarps * 16 * Sh::kLd;  // [warp][16][m, l]
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * Sh::kStage + Sh::kScratch);
+  // [2] this CTA's part of a tile for its cluster: o [row][D], then m and l [row]
+  float* merged = reinterpret_cast<float*>(smem + kStages * Sh::kStage + Sh::kScratch);
+  uint64_t* full =
+      reinterpret_cast<uint64_t*>(smem + kStages * Sh::kStage + Sh::kScratch + 2 * Sh::kMerged);
   uint64_t* empty = full + kStages;
+  uint64_t* peers = empty + kStages;   // every CTA of the cluster has written its part
   // [0] abort [1] last [2], [3] segment number + 1 with a non-finite edge value
-  volatile int* s_flag = reinterpret_cast<volatile int*>(empty + kStages);
-  const SplitTables tab(reinterpret_cast<uint8_t*>(empty + kStages) + 64, a.p.batch);
+  volatile int* s_flag = reinterpret_cast<volatile int*>(peers + 1);
+  const SplitTables tab(reinterpret_cast<uint8_t*>(peers + 1) + 64, a.p.batch);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -85,6 +131,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kWarps);
     }
+    mbar_init(peers, CL);
     s_flag[0] = 0;
     s_flag[2] = s_flag[3] = 0;
     fence_mbar_init();
@@ -93,7 +140,10 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   long long W, G, u0, u1;
-  split_setup<Sh::kThreads>(a.p, a.s, tab, a.min_units, W, G, u0, u1);
+  const long long worker = blockIdx.x / CL;
+  const int rank = CL > 1 ? (int)cluster_rank() : 0;
+  if (CL > 1) cluster_sync_all();  // the barriers of all its CTAs are set up
+  split_setup<Sh::kThreads>(a.p, a.s, tab, a.min_units, worker, gridDim.x / CL, W, G, u0, u1);
   SplitWalk w(a.s, tab, u0, u1);
   const int page_mask = a.p.page - 1;
 
@@ -102,8 +152,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
     const uint64_t pol = policy_evict_first();
     // a tile is `pieces` boxes of `rows` positions, times keys/values, times
     // column halves: one lane each
-    const int rows = a.p.page < kAttnKeys ? a.p.page : kAttnKeys;
-    const int pieces = kAttnKeys / rows;
+    const int rows = a.p.page < kKeys ? a.p.page : kKeys;
+    const int pieces = kKeys / rows;
     const int half = lane % (D / 64), kvsel = (lane / (D / 64)) & 1, piece = lane / (D / 64 * 2);
     int it = 0;
     bool ok = true;
@@ -111,17 +161,17 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       const int row = paged_row(a.p, w.b);
       const int32_t* trow = a.p.table + (long long)(row < 0 ? 0 : row) * a.p.table_stride;
       auto page_at = [&](int j) -> int {
-        const int pos = j * kAttnKeys + piece * rows;
+        const int pos = j * kKeys + piece * rows;
         if (piece >= pieces || pos >= w.tr.khi) return -1;
         const int pg = __ldg(trow + (pos >> a.p.page_shift));
         // a page that does not exist reads as zeros
         if ((pg < 0 || pg >= a.p.pages) && a.p.status) atomicOr(a.p.status, kStatusBounds);
         return pg < 0 || pg >= a.p.pages ? a.p.pages : pg;
       };
-      int pg_next = page_at(w.j);
-      for (int k = 0; k < w.n; ++k, ++it) {
+      int pg_next = rank < w.n ? page_at(w.j + rank) : -1;
+      for (int k = rank; k < w.n; k += CL, ++it) {
         const int j = w.j + k, pg = pg_next;
-        if (k + 1 < w.n) pg_next = page_at(j + 1);
+        if (k + CL < w.n) pg_next = page_at(j + CL);
         const int st = it % kStages;
         if (it >= kStages && !mbar_wait(&empty[st], ((it / kStages) + 1) & 1, a.timeout_ns, a.p.status))
           s_flag[0] = 1;
@@ -136,7 +186,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
         if (pg >= 0)
           tma_load_4d(smem + st * Sh::kStage + kvsel * Sh::kKBytes + half * Sh::kHalf +
                           piece * rows * 128,
-                      &kvmap, half * 64, (j * kAttnKeys + piece * rows) & page_mask,
+                      &kvmap, half * 64, (j * kKeys + piece * rows) & page_mask,
                       kvsel * a.p.hkv + w.h, pg, &full[st], pol);
       }
     }
@@ -145,9 +195,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       for (int st = 0; st < kStages && st < it; ++st)
         mbar_wait(&full[st], ((it - st + kStages - 1) / kStages - 1) & 1, drain_ns(a.timeout_ns),
                   nullptr);
-    return;
-  }
-
+    __syncwarp();
+  } else {
   // ------------------------------------------------------------------ consumers
   const int rt = warp / kKS, ks = warp % kKS;   // row tile of 16, share of the positions
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;
@@ -185,85 +234,41 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
       for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    for (int k = 0; k < w.n; ++k, ++it) {
-      const int st = it % kStages, key0 = (w.j + k) * kAttnKeys;
+    for (int k = rank; k < w.n; k += CL, ++it) {
+      const int st = it % kStages, key0 = (w.j + k) * kKeys;
       if (!s_flag[0] && !mbar_wait(&full[st], (it / kStages) & 1, a.timeout_ns, a.p.status))
         s_flag[0] = 1;
       const uint32_t kb = smem_u32(smem + st * Sh::kStage), vb = kb + Sh::kKBytes;
-      const bool edge = er.in(key0, kAttnKeys);
+      const bool edge = er.in(key0, kKeys);
+      const int kr = ks * kBlk;  // first position of this warp in the tile
+      if (key0 + kr < w.tr.khi && key0 + kr + kBlk > w.tr.klo) {
+        float s[kBlk / 8][4];
 #pragma unroll
-      for (int blk = 0; blk < kAttnKeys / 16 / kKS; ++blk) {
-        const int kr = (blk * kKS + ks) * 16;  // first position of this block in the tile
-        if (key0 + kr >= w.tr.khi || key0 + kr + 16 <= w.tr.klo) continue;
-        float s[2][4];
+        for (int t = 0; t < kBlk / 8; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
         {
           // matrices: positions 0-7 / 8-15 (lane bit 4), column chunks 0 / 1 (bit 3)
           const int key = kr + (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t b0, b1, b2, b3;
             const int chunk = (kk & 3) * 2 + ch;
-            ldmatrix_x4(b0, b1, b2, b3,
-                        kb + (kk >> 2) * Sh::kHalf + key * 128 + ((chunk ^ (key & 7)) << 4));
-            mma_bf16_16816(s[0], qf[kk], b0, b1);
-            mma_bf16_16816(s[1], qf[kk], b2, b3);
-          }
-        }
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[t][e] *= a.c;  // before the mask: c may be 0 or negative
-            const int key = key0 + kr + t * 8 + c0 + (e & 1);
-            if (edge && (key > hi[e >> 1] || key < lo[e >> 1])) s[t][e] = -INFINITY;
-          }
-        float base[2];
-        bool grew = false;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-          const float mn = fmaxf(m[e], mx);
-          grew |= mn > m[e];
-          base[e] = mn;
-        }
-        if (__any_sync(~0u, grew)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // a row that has seen nothing yet has o = l = 0 whatever the factor
-            const float f = m[e] == -INFINITY ? 0.f : exp2_approx(m[e] - base[e]);
-            m[e] = base[e];
-            l[e] *= f;
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-              o[d][2 * e] *= f;
-              o[d][2 * e + 1] *= f;
+            for (int t = 0; t < kBlk / 16; ++t) {
+              uint32_t b0, b1, b2, b3;
+              ldmatrix_x4(b0, b1, b2, b3, kb + (kk >> 2) * Sh::kHalf + (key + t * 16) * 128 +
+                                              ((chunk ^ (key & 7)) << 4));
+              mma_bf16_16816(s[2 * t], qf[kk], b0, b1);
+              mma_bf16_16816(s[2 * t + 1], qf[kk], b2, b3);
             }
-          }
-        }
-        uint32_t pf[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mb = m[e] == -INFINITY ? 0.f : m[e];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float p0 = exp2_approx(s[t][2 * e] - mb);
-            const float p1 = exp2_approx(s[t][2 * e + 1] - mb);
-            l[e] += p0 + p1;
-            // weights enter the product with the values as bf16: a relative
-            // error of at most 2^-8 each, of the size of the output's own
-            // rounding; the sum l takes them unrounded
-            pf[t * 2 + e] = pack_bf16(p0, p1);
           }
         }
         if (edge) {
           // values that no row sees (the unused end of a page may hold
           // anything), and non-finite ones that only some rows see, become 0.
           // Warps of other row tiles may do the same to the same values.
-          for (int x = lane; x < 16 * (D / 8); x += 32) {
+#pragma unroll 1
+          for (int x = lane; x < kBlk * (D / 8); x += 32) {
             const int key = kr + x / (D / 8), ch = x % (D / 8);
             uint4* at = reinterpret_cast<uint4*>(smem + st * Sh::kStage + Sh::kKBytes +
                                                  (ch >> 3) * Sh::kHalf + key * 128 +
@@ -273,18 +278,67 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
           fence_async_shared();
           __syncwarp();
         }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < kBlk / 8; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[t][e] *= a.c;  // before the mask: c may be 0 or negative
+            const int key = key0 + kr + t * 8 + c0 + (e & 1);
+            if (edge && (key > hi[e >> 1] || key < lo[e >> 1])) s[t][e] = -INFINITY;
+            mx[e >> 1] = fmaxf(mx[e >> 1], s[t][e]);
+          }
+        bool grew = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 1));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(~0u, mx[e], 2));
+          grew |= mx[e] > m[e];
+        }
+        if (__any_sync(~0u, grew)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // a row that has seen nothing yet has o = l = 0 whatever the factor
+            const float mn = fmaxf(m[e], mx[e]);
+            const float f = m[e] == -INFINITY ? 0.f : exp2_approx(m[e] - mn);
+            m[e] = mn;
+            l[e] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+              o[d][2 * e] *= f;
+              o[d][2 * e + 1] *= f;
+            }
+          }
+        }
+        uint32_t pf[kBlk / 16][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mb = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+          for (int t = 0; t < kBlk / 8; ++t) {
+            const float p0 = exp2_approx(s[t][2 * e] - mb);
+            const float p1 = exp2_approx(s[t][2 * e + 1] - mb);
+            l[e] += p0 + p1;
+            // weights enter the product with the values as bf16: a relative
+            // error of at most 2^-8 each, of the size of the output's own
+            // rounding; the sum l takes them unrounded
+            pf[t / 2][(t & 1) * 2 + e] = pack_bf16(p0, p1);
+          }
+        }
         {
           // matrices: positions 0-7 / 8-15 (lane bit 3), column chunks 0 / 1 (bit 4)
           const int key = kr + (lane & 15), ch = lane >> 4;
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            uint32_t b0, b1, b2, b3;
-            const int chunk = (d & 3) * 2 + ch;
-            ldmatrix_x4_trans(b0, b1, b2, b3,
-                              vb + (d >> 2) * Sh::kHalf + key * 128 + ((chunk ^ (key & 7)) << 4));
-            mma_bf16_16816(o[2 * d], pf, b0, b1);
-            mma_bf16_16816(o[2 * d + 1], pf, b2, b3);
-          }
+          for (int t = 0; t < kBlk / 16; ++t)
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              uint32_t b0, b1, b2, b3;
+              const int chunk = (d & 3) * 2 + ch;
+              ldmatrix_x4_trans(b0, b1, b2, b3, vb + (d >> 2) * Sh::kHalf + (key + t * 16) * 128 +
+                                                    ((chunk ^ (key & 7)) << 4));
+              mma_bf16_16816(o[2 * d], pf[t], b0, b1);
+              mma_bf16_16816(o[2 * d + 1], pf[t], b2, b3);
+            }
         }
       }
       __syncwarp();
@@ -310,129 +364,200 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1)
     const bool aborted = s_flag[0] != 0;
     const bool poison = s_flag[2 + (seg & 1)] == seg + 1;
     const int ct = threadIdx.x;
-    const long long c = blockIdx.x;
     const long long ut = w.tile_unit();
-    // the tile's first CTA ends its range with it, the others begin with it
-    const long long slot = c * 2 + (ut >= u0 ? 1 : 0);
-    float* mine = a.ws + slot * Sh::kSlot;
-    auto store = [&](int r, int d, float4 v, float mm, float ll) {
+    auto store = [&](int r, int d, const State& s) {
       const int t = r / a.group, g = r - t * a.group;
       const long long tok = q0 + t0 + t;
       const int head = w.h * a.group + g;
-      const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);  // NaN stays NaN
-      uint2 pk = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-      *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (long long)head * D + d) = pk;
+      const float inv = s.l > 0.f ? 1.f / s.l : (s.l == 0.f ? 0.f : s.l);  // NaN stays NaN
+      *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (long long)head * D + d) = make_uint2(
+          pack_bf16(s.v.x * inv, s.v.y * inv), pack_bf16(s.v.z * inv, s.v.w * inv));
       if (a.lse && d == 0)
-        a.lse[tok * a.hq + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+        a.lse[tok * a.hq + head] =
+            s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * 0.6931471805599453f;
     };
-    for (int x = ct; x < rows * (D / 4); x += kCons) {
-      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+    // the state of four columns of a row over the warps that share the row tile
+    auto own = [&](int r, int d) -> State {
       const int wr = (r >> 4) * kKS, rr = r & 15;
-      float M = -INFINITY;
+      State s = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
 #pragma unroll
-      for (int k = 0; k < kKS; ++k) M = fmaxf(M, sc_ml[((wr + k) * 16 + rr) * 2]);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      float L = 0.f;
+      for (int k = 0; k < kKS; ++k) s.m = fmaxf(s.m, sc_ml[((wr + k) * 16 + rr) * 2]);
 #pragma unroll
       for (int k = 0; k < kKS; ++k) {
         const float mk = sc_ml[((wr + k) * 16 + rr) * 2];
-        const float f = M == -INFINITY ? 1.f : exp2_approx(mk - M);
+        const float f = s.m == -INFINITY ? 1.f : exp2_approx(mk - s.m);
         const float4 q4 =
             *reinterpret_cast<const float4*>(scratch + ((wr + k) * 16 + rr) * Sh::kLd + d);
-        L += f * sc_ml[((wr + k) * 16 + rr) * 2 + 1];
-        v.x += f * q4.x;
-        v.y += f * q4.y;
-        v.z += f * q4.z;
-        v.w += f * q4.w;
+        s.l += f * sc_ml[((wr + k) * 16 + rr) * 2 + 1];
+        s.v.x += f * q4.x;
+        s.v.y += f * q4.y;
+        s.v.z += f * q4.z;
+        s.v.w += f * q4.w;
       }
-      if (poison) {
-        const int t = r / a.group, p = pos0 + t;
-        edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, a.s.window > 0 ? p - a.s.window + 1 : 0, p,
-                       w.j * kAttnKeys, (w.j + w.n) * kAttnKeys, d, [&](const uint16_t* e) {
-                         const uint2 pk = __ldg(reinterpret_cast<const uint2*>(e));
-                         const float f[4] = {bf16lo(pk.x), bf16hi(pk.x), bf16lo(pk.y), bf16hi(pk.y)};
-                         if (!isfinite(f[0])) v.x += f[0];
-                         if (!isfinite(f[1])) v.y += f[1];
-                         if (!isfinite(f[2])) v.z += f[2];
-                         if (!isfinite(f[3])) v.w += f[3];
-                       });
+      if (poison)
+        for (int k = rank; k < w.n; k += CL)  // the positions of this CTA
+          add_edge_values<D>(a.p, a.s.window, w.b, w.h, er, pos0 + r / a.group,
+                             (w.j + k) * kKeys, d, s);
+      return s;
+    };
+    const int items = rows * (D / 4);
+    if (CL > 1) {
+      // in a cluster: this CTA's part to shared memory; then each CTA joins
+      // every CL-th run of columns from all of them. Two buffers: whoever
+      // writes one again has seen every CTA arrive for the other, after
+      // reading this one.
+      float* buf = merged + (seg & 1) * (Sh::kMerged / 4);
+#pragma unroll 1
+      for (int x = ct; x < items; x += kCons) {
+        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        const State s = own(r, d);
+        *reinterpret_cast<float4*>(buf + r * D + d) = s.v;
+        if (d == 0) *reinterpret_cast<float2*>(buf + Sh::kRows * D + r * 2) = make_float2(s.m, s.l);
       }
+      named_bar_sync(1, kCons);
+      if (ct < CL) mbar_arrive_remote(peers, ct);
+      if (!mbar_wait_cluster(peers, seg & 1, a.timeout_ns, a.p.status)) s_flag[0] = 1;
+    }
+    // the item's state over the whole segment
+    auto part = [&](int r, int d) -> State {
+      if (CL == 1) return own(r, d);
+      const float* buf = merged + (seg & 1) * (Sh::kMerged / 4);
+      float4 v[CL];
+      float2 ml[CL];
+#pragma unroll
+      for (int k = 0; k < CL; ++k) {
+        v[k] = ld_dsmem_f32x4(buf + r * D + d, k);
+        ml[k] = ld_dsmem_f32x2(buf + Sh::kRows * D + r * 2, k);
+      }
+      State s = {v[0], ml[0].x, ml[0].y};
+#pragma unroll
+      for (int k = 1; k < CL; ++k) s.add(v[k], ml[k].x, ml[k].y);
+      return s;
+    };
+    const int x0 = rank * kCons + ct;
+    // A tile shared with other workers: its first one ends its range with it
+    // (slot 1), the others begin with it (slot 0). The CTAs of rank r of each
+    // see to the same columns, so that the last of them joins these.
+    auto slot_of = [&](long long c, bool first) { return a.ws + (c * 2 + (first ? 1 : 0)) * Sh::kSlot; };
+    float* mine = slot_of(worker, ut >= u0);
+#pragma unroll 1
+    for (int x = x0; x < items; x += CL * kCons) {
+      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+      const State s = part(r, d);
       if (w.whole) {
-        if (!aborted) store(r, d, v, M, L);
+        if (!aborted) store(r, d, s);
       } else {
-        __stcg(reinterpret_cast<float4*>(DG_AT(a.p.status, mine, r * D + d, Sh::kSlot - 3)), v);
-        if (d == 0)
-          __stcg(reinterpret_cast<float2*>(mine + Sh::kRows * D + r * 2), make_float2(M, L));
+        __stcg(reinterpret_cast<float4*>(DG_AT(a.p.status, mine, x * 4, Sh::kSlot - 3)), s.v);
+        __stcg(reinterpret_cast<float2*>(mine + Sh::kItems * 4 + x * 2), make_float2(s.m, s.l));
+      }
+    }
+    if (w.whole) {
+      named_bar_sync(1, kCons);
+      continue;
+    }
+    named_bar_sync(1, kCons);
+    const long long cf = cta_of(ut, W, G);
+    const int nc = (int)(cta_of(ut + w.tr.n - 1, W, G) - cf + 1);
+    if (ct == 0) {
+      // the tile's counters are its first worker's (which is first for no other)
+      int* cp = DG_AT(a.p.status, a.ctr, cf * CL + rank, a.ctr_len);
+      const int old = atomic_add_acq_rel_gpu(cp, 1);
+      const int last = old == nc - 1 ? 1 : 0;
+      if (last) *cp = 0;
+      s_flag[1] = last;
+    }
+    named_bar_sync(1, kCons);
+    if (s_flag[1] && !aborted) {
+      constexpr int kAhead = 4;  // parts in flight
+#pragma unroll 1
+      for (int x = x0; x < items; x += CL * kCons) {
+        State s = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+#pragma unroll 1
+        for (int k0 = 0; k0 < nc; k0 += kAhead) {
+          float4 v[kAhead];
+          float2 ml[kAhead];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+            if (k0 + k < nc) {
+              const float* p = slot_of(cf + k0 + k, k0 + k == 0);
+              v[k] = __ldcg(reinterpret_cast<const float4*>(p + x * 4));
+              ml[k] = __ldcg(reinterpret_cast<const float2*>(p + Sh::kItems * 4 + x * 2));
+            }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+            if (k0 + k < nc) s.add(v[k], ml[k].x, ml[k].y);
+        }
+        const int r = x / (D / 4);
+        store(r, (x % (D / 4)) * 4, s);
       }
     }
     named_bar_sync(1, kCons);
-    if (!w.whole) {
-      const long long cf = cta_of(ut, W, G), cl = cta_of(ut + w.tr.n - 1, W, G);
-      const int nc = (int)(cl - cf + 1);
-      if (ct == 0) {
-        // the tile's counter is its first CTA's (which is first for no other)
-        int* cp = DG_AT(a.p.status, a.ctr, cf, a.ctr_len);
-        const int old = atomic_add_acq_rel_gpu(cp, 1);
-        const int last = old == nc - 1 ? 1 : 0;
-        if (last) *cp = 0;
-        s_flag[1] = last;
-      }
-      named_bar_sync(1, kCons);
-      if (s_flag[1] && !aborted) {
-        auto slot_of = [&](int k) -> const float* {
-          return a.ws + ((cf + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kSlot;
-        };
-        for (int x = ct; x < rows * (D / 4); x += kCons) {
-          const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-          float M = -INFINITY;
-          for (int k = 0; k < nc; ++k) M = fmaxf(M, __ldcg(slot_of(k) + Sh::kRows * D + r * 2));
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          float L = 0.f;
-#pragma unroll 4
-          for (int k = 0; k < nc; ++k) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot_of(k) + Sh::kRows * D + r * 2));
-            const float4 q4 = __ldcg(reinterpret_cast<const float4*>(slot_of(k) + r * D + d));
-            const float f = M == -INFINITY ? 1.f : exp2_approx(ml.x - M);
-            L += f * ml.y;
-            v.x += f * q4.x;
-            v.y += f * q4.y;
-            v.z += f * q4.z;
-            v.w += f * q4.w;
-          }
-          store(r, d, v, M, L);
-        }
-      }
-      named_bar_sync(1, kCons);
-    }
   }
+  }
+  if (CL > 1) cluster_sync_all();  // no CTA ends while another may read its part
 }
 
 // ------------------------------------------------------------------ launch
-template <int D, int RT>
-static cudaError_t launch_rt(const Ctx& cx, const CUtensorMap& map, const AttnArgs& a, int grid) {
-  using Sh = AttnShape<D, RT>;
+// Clusters of the kernel that fit on the device at once (0: none).
+template <int D, int RT, int CL>
+static int clusters_at_once(int smem) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL);
+  cfg.blockDim = dim3(AttnShape<D, RT, CL>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {CL, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, attn_mma_kernel<D, RT, CL>, &cfg) == cudaSuccess ? n : 0;
+}
+
+template <int D, int RT, int CL>
+static cudaError_t launch_rt(const Ctx& cx, const CUtensorMap& map, const AttnArgs& a) {
+  using Sh = AttnShape<D, RT, CL>;
   static DevOnce once;
-  cudaError_t e = setup_smem(once, attn_mma_kernel<D, RT>, kMaxDynSmem);
+  cudaError_t e = setup_smem(once, attn_mma_kernel<D, RT, CL>, kMaxDynSmem);
   if (e != cudaSuccess) return e;
-  return launch_k(attn_mma_kernel<D, RT>, dim3(grid), dim3(Sh::kThreads), Sh::smem(a.p.batch),
-                  cx.stream, cx.pdl, map, a);
+  if (CL == 1)
+    return launch_k(attn_mma_kernel<D, RT, CL>, dim3(cx.sms), dim3(Sh::kThreads),
+                    Sh::smem(a.p.batch), cx.stream, cx.pdl, map, a);
+  static DevOnce asked;
+  static int at_once[64];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  int n = 0;
+  if (dev < 64) {
+    e = asked.run([&]() -> cudaError_t {
+      at_once[dev] = clusters_at_once<D, RT, CL>(Sh::smem(kMaxBatch));
+      return cudaSuccess;
+    });
+    if (e != cudaSuccess) return e;
+    n = at_once[dev];
+  }
+  if (n < 1) n = 1;
+  if (n > cx.sms / CL) n = cx.sms / CL;
+  return launch_kc(attn_mma_kernel<D, RT, CL>, dim3(n * CL), dim3(Sh::kThreads),
+                   Sh::smem(a.p.batch), cx.stream, cx.pdl, CL, map, a);
 }
 
 size_t attn_mma_ws(int dim, int rt, int sms) {
-  return (size_t)sms * 2 * 16 * rt * (dim + 2) * sizeof(float);
+  return (size_t)sms * 2 * 16 * rt * (dim / 4) * 6 * sizeof(float);
 }
 
 cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCall& c, float* ws,
                             int* ctr) {
   CUtensorMap map;
-  if (!make_tmap_kv(&map, v, v.page < kAttnKeys ? v.page : kAttnKeys))
+  const int keys = 1 << attn_keys_shift(v.dim);
+  if (!make_tmap_kv(&map, v, v.page < keys ? v.page : keys))
     return cudaErrorInvalidValue;
   AttnArgs a = {};
   a.p = paged_args(v, c.tokens, cx.status);
   a.group = c.hq / v.hkv;
   a.hq = c.hq;
   a.s.tq = 16 * rt / a.group;
-  a.s.bn_shift = kAttnKeysShift;
+  a.s.bn_shift = attn_keys_shift(v.dim);
   a.s.window = c.window;
   a.s.hkv = v.hkv;
   a.q = static_cast<const uint16_t*>(c.q);
@@ -449,9 +574,16 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
   a.min_units = 7;
   a.timeout_ns = cx.timeout_ns;
   const bool d64 = v.dim == 64;
-  if (rt == 1) return d64 ? launch_rt<64, 1>(cx, map, a, cx.sms) : launch_rt<128, 1>(cx, map, a, cx.sms);
-  if (rt == 2) return d64 ? launch_rt<64, 2>(cx, map, a, cx.sms) : launch_rt<128, 2>(cx, map, a, cx.sms);
-  return d64 ? launch_rt<64, 4>(cx, map, a, cx.sms) : launch_rt<128, 4>(cx, map, a, cx.sms);
+  // Few row tiles: a cluster of 8 CTAs for each part of one, so that the parts
+  // are joined through distributed shared memory and only a few partial tiles
+  // go through the workspace.
+  const long long tiles = ((long long)c.tokens / a.s.tq + v.batch) * v.hkv;
+  if (rt == 1 && tiles <= kClusterTiles)
+    return d64 ? launch_rt<64, 1, 8>(cx, map, a) : launch_rt<128, 1, 8>(cx, map, a);
+  if (tiles <= kClusterTiles)
+    return d64 ? launch_rt<64, 2, 8>(cx, map, a) : launch_rt<128, 2, 8>(cx, map, a);
+  if (rt == 1) return d64 ? launch_rt<64, 1, 1>(cx, map, a) : launch_rt<128, 1, 1>(cx, map, a);
+  return d64 ? launch_rt<64, 2, 1>(cx, map, a) : launch_rt<128, 2, 1>(cx, map, a);
 }
 
 }  // namespace dg

@@ -84,11 +84,11 @@ __device__ __forceinline__ void edge_steps(const EdgeRange& er, int key0, int& k
   if (k1 <= k0) k1 = k0 + 1;
 }
 
-// Puts -inf in the columns of a row of S (128 fp32 in TMEM, this thread's lane)
-// outside [l0, h0]. A pass of its own over the few tiles at the edge of what
+// Puts `none` (which c makes -inf) in the columns of a row of S (128 fp32 in
+// TMEM, this thread's lane) outside [l0, h0]. A pass of its own over the few tiles at the edge of what
 // the rows see, in few instructions: code that runs once in a while costs its
 // instruction fetches.
-__device__ __forceinline__ void row_mask(uint32_t ts, int l0, int h0) {
+__device__ __forceinline__ void row_mask(uint32_t ts, int l0, int h0, uint32_t none) {
 #pragma unroll 1
   for (int q = 0; q < 4; ++q, ts += 32, l0 -= 32, h0 -= 32) {
     const uint32_t above = l0 <= 0 ? ~0u : (l0 > 31 ? 0u : ~0u << l0);
@@ -101,7 +101,7 @@ __device__ __forceinline__ void row_mask(uint32_t ts, int l0, int h0) {
     tmem_settle<32>(v);
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-      if (!(seen & (1u << e))) v[e] = 0xFF800000u;  // -inf
+      if (!(seen & (1u << e))) v[e] = none;
     tmem_st32(ts, v);
   }
   tmem_st_wait();
@@ -116,10 +116,10 @@ __device__ __forceinline__ float row_start(uint32_t ts, float c) {
   float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
-    mx0 = max3(mx0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-    mx1 = max3(mx1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+    mx0 = max3(mx0, __uint_as_float(v[e]) * c, __uint_as_float(v[e + 1]) * c);
+    mx1 = max3(mx1, __uint_as_float(v[e + 2]) * c, __uint_as_float(v[e + 3]) * c);
   }
-  return fmaxf(mx0, mx1) * c;
+  return fmaxf(mx0, mx1);
 }
 
 // One row of S: top = max c s, the weights 2^(c s - m) as bf16 pairs in pk, and
@@ -142,12 +142,10 @@ __device__ __forceinline__ void row_pass(uint32_t ts, float c, float m, uint32_t
     // exponentials, its sum and packing behind them
 #pragma unroll
     for (int e = 0; e < 16 + 8; ++e) {
-      if (e < 16) {
-        if (e & 1) mx1 = max3(mx1, f[e].x, f[e].y);
-        else mx0 = max3(mx0, f[e].x, f[e].y);
-        f[e] = fma2(f[e], c, -m);
-      }
+      if (e < 16) f[e] = fma2(f[e], c, -m);
       if (e >= 4 && e < 20) {
+        if (e & 1) mx1 = max3(mx1, f[e - 4].x, f[e - 4].y);
+        else mx0 = max3(mx0, f[e - 4].x, f[e - 4].y);
         f[e - 4].x = exp2_approx(f[e - 4].x);
         f[e - 4].y = exp2_approx(f[e - 4].y);
       }
@@ -159,7 +157,7 @@ __device__ __forceinline__ void row_pass(uint32_t ts, float c, float m, uint32_t
       }
     }
   }
-  top = fmaxf(mx0, mx1) * c;
+  top = fmaxf(mx0, mx1) + m;
   sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
 }
 
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   long long W, G, u0, u1;
-  split_setup<kTcAttnThreads>(a.p, a.s, tab, a.min_units, W, G, u0, u1);
+  split_setup<kTcAttnThreads>(a.p, a.s, tab, a.min_units, blockIdx.x, gridDim.x, W, G, u0, u1);
   SplitWalk w(a.s, tab, u0, u1);
 
   auto edges = [&]() -> EdgeRange {
@@ -451,6 +449,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     const uint32_t ts = taddr + lanes + x * 128, to = taddr + lanes + 256 + x * D;
     const int t = r / a.group, g = r - t * a.group;
     uint8_t* mine = stage + warp * 2048;
+    const uint32_t none = a.c < 0.f ? 0x7F800000u : 0xFF800000u;
     uint32_t sn = 0, on = 0;
     int seg = 0;
     bool ok = true;
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         // is made again with the new one: S stays in TMEM until the weights
         // replace it. A segment's first tile starts from the maximum of its
         // first 32 columns.
-        if (er.in(key0, kTcKeys)) row_mask(ts, lo - key0, hi - key0);
+        if (er.in(key0, kTcKeys)) row_mask(ts, lo - key0, hi - key0, none);
         uint32_t pk[64];
         float top, sum;
         if (k == 0) m = row_start(ts, a.c);
@@ -701,15 +700,15 @@ cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, vo
   a.lse = c.lse;
   a.ldo = c.ldo;
   a.hq = c.hq;
-  a.c = c.scale * 1.4426950408889634f;
+  // a scale of 0 (all weights equal): one that no score outgrows, so that masked
+  // scores stay infinite
+  a.c = c.scale == 0.f ? 1e-30f : c.scale * 1.4426950408889634f;
   a.split = static_cast<int*>(ws);
   a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + (size_t)cx.sms * 16);
-  a.s.start = 2;
+  a.s.start = 3;
   a.min_units = 4;
   a.timeout_ns = cx.timeout_ns;
-  // few pairs, each split over many CTAs: spread each join over more blocks
-  const long long pairs = ((long long)c.tokens / a.s.tq + v.batch) * v.hkv;
-  const int join_y = pairs * 4 < cx.sms ? v.dim / 4 : 8;
+  const int join_y = v.dim / (4 * 2);  // 4 columns at a time, twice
   return v.dim == 64 ? launch_tc_d<64>(cx, kv, q, a, join_y) : launch_tc_d<128>(cx, kv, q, a, join_y);
 }
 

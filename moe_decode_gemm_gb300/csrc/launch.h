@@ -185,7 +185,7 @@ struct AttnCall {
   float scale;
 };
 
-// Attention for row tiles of 16 * rt rows (rt 1, 2 or 4) on mma.sync; ws of
+// Attention for row tiles of 16 * rt rows (rt 1 or 2) on mma.sync; ws of
 // attn_mma_ws bytes, ctr of one zero int per SM.
 size_t attn_mma_ws(int dim, int rt, int sms);
 cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCall& c, float* ws,
@@ -197,7 +197,7 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
 bool make_tmap_heads(CUtensorMap* map, const void* q, int tokens, int heads, int dim, long long ld,
                      int box_heads, int box_tokens);
 
-// Attention for longer chunks on tcgen05 (scale > 0); two kernels; ws of
+// Attention for longer chunks on tcgen05; two kernels; ws of
 // attn_tc_ws bytes.
 size_t attn_tc_ws(int dim, int sms);
 cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, void* ws);

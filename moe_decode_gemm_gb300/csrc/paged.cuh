@@ -206,13 +206,14 @@ struct SplitTables {
   }
 };
 
-// Fill the tables and find this CTA's range [u0, u1) of the W units and where
-// it begins. Called by all NT threads of the CTA; ends with a barrier.
-// G: CTAs that take part (W / min_units at most, and the grid).
+// Fill the tables and find the range [u0, u1) of the W units that worker c of
+// `workers` (a CTA or a cluster) has, and where it begins. Called by all NT
+// threads of the CTA; ends with a barrier. G: workers that take part.
 template <int NT>
 __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape& s,
-                                            const SplitTables& t, int min_units, long long& W,
-                                            long long& G, long long& u0, long long& u1) {
+                                            const SplitTables& t, int min_units, long long c,
+                                            long long workers, long long& W, long long& G,
+                                            long long& u0, long long& u1) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) t.loc[4] = 0;
   __syncthreads();
@@ -270,12 +271,11 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
   if (tid == 0) t.base[0] = 0;
   __syncthreads();
   W = t.base[p.batch];
-  // no more CTAs than give each min_units, but one for each row tile
+  // no more workers than give each min_units, but one for each row tile
   G = W / min_units;
   if (G < (long long)t.loc[4] * s.hkv) G = (long long)t.loc[4] * s.hkv;
   if (G < 1) G = 1;
-  if (G > (long long)gridDim.x) G = gridDim.x;
-  const long long c = blockIdx.x;
+  if (G > workers) G = workers;
   u0 = c < G ? cta_start(c, W, G) : 0;
   u1 = c < G ? cta_start(c + 1, W, G) : 0;
   if (warp == 0 && u0 < u1) {
