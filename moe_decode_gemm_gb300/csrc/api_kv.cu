@@ -144,7 +144,7 @@ int kv_resize(const dec_kv_pool* pool, const int32_t* seqs, const int32_t* lens,
   Ctx cx;
   void* ws;
   if ((rc = kv_context(stream, (size_t)2 * n * sizeof(int), 0, &cx, &ws, nullptr))) return rc;
-  return result(launch_kv_resize(cx, p, seqs, lens, n, static_cast<int*>(ws)), 2);
+  return result(launch_kv_resize(cx, p, seqs, lens, n, static_cast<int*>(ws)), 1);
 }
 
 int kv_free(const dec_kv_pool* pool, const int32_t* seqs, int n, void* stream) {

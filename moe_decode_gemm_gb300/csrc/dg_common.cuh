@@ -216,9 +216,15 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // Every thread of every CTA of the cluster arrives (release) and waits
 // (acquire): shared-memory writes before it are visible to the whole cluster
 // after it.
-__device__ __forceinline__ void cluster_sync_all() {
+__device__ __forceinline__ void cluster_arrive_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_all() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  cluster_arrive_all();
+  cluster_wait_all();
 }
 // fp32 load from the shared memory of CTA `rank` of this cluster, at the
 // address `local` has in this CTA's shared memory.
@@ -474,6 +480,12 @@ __device__ __forceinline__ float silu_f(float z) { return z / (1.0f + expf(-z));
 // T units over G CTAs in contiguous ranges: the first unit of CTA c.
 __device__ __forceinline__ long long cta_start(long long c, long long T, long long G) {
   return (c * T) / G;
+}
+
+// n / d for n >= 0, d > 0: in 32 bits, a fifth of the instructions, when both fit.
+__device__ __forceinline__ long long div_small(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return (long long)((uint32_t)n / (uint32_t)d);
+  return n / d;
 }
 
 // CTA whose unit range contains unit v: largest c with start(c) <= v.

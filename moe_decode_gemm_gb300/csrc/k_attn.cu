@@ -59,7 +59,7 @@ struct AttnShape {
   static constexpr int kStage = 2 * kKBytes;
   static constexpr int kStages = (CL > 1 ? 96 : 128) * 1024 / kStage;
   static constexpr int kLd = D + 8;                    // floats between rows of the join scratch
-  static constexpr int kScratch = kWarps * 16 * kLd * 4 + kWarps * 16 * 8;
+  static constexpr int kScratch = kWarps * 16 * kLd * 4 + kWarps * 16 * 8;  // o; m and l
   static constexpr int kItems = kRows * (D / 4);       // four columns of a row each
   static constexpr int kSlot = kItems * 6;             // floats of a partial tile: o, then m and l
   static constexpr int kMerged = CL > 1 ? kRows * (D + 2) * 4 : 0;  // a CTA's part of a cluster's tile
@@ -87,20 +87,23 @@ struct State {
   }
 };
 
-// Non-finite values at the edge that the row at position p sees, in columns d ..
-// d + 3 of the key tile at key0 (out of line: it hardly ever runs).
-template <int D>
+// Adds the non-finite values at the edge that row r (at position pos) sees, in
+// columns d .. d + 3 of this CTA's key tiles, to the part of the warp that had
+// them (out of line: it hardly ever runs).
+template <int D, int KEYS, int BLK, int KS>
 __device__ __noinline__ void add_edge_values(const PagedArgs& p, int window, int b, int h,
-                                             const EdgeRange& er, int pos, int key0, int d, State& s) {
-  edge_values<D>(p, paged_row(p, b), h, er, window > 0 ? pos - window + 1 : 0, pos, key0,
-                 key0 + (1 << attn_keys_shift(D)), d, [&](const uint16_t* e) {
-                   const uint2 pk = __ldg(reinterpret_cast<const uint2*>(e));
-                   const float f[4] = {bf16lo(pk.x), bf16hi(pk.x), bf16lo(pk.y), bf16hi(pk.y)};
-                   if (!isfinite(f[0])) s.v.x += f[0];
-                   if (!isfinite(f[1])) s.v.y += f[1];
-                   if (!isfinite(f[2])) s.v.z += f[2];
-                   if (!isfinite(f[3])) s.v.w += f[3];
-                 });
+                                             const EdgeRange& er, int pos, int j, int n, int rank,
+                                             int step, int r, int d, float* scratch) {
+  for (int k = rank; k < n; k += step)
+    edge_values<D>(p, paged_row(p, b), h, er, window > 0 ? pos - window + 1 : 0, pos, (j + k) * KEYS,
+                   (j + k + 1) * KEYS, d, [&](const uint16_t* e, int key) {
+                     const int row = ((r >> 4) * KS + key % KEYS / BLK) * 16 + (r & 15);
+                     float* o = scratch + row * (D + 8) + d;
+                     for (int c = 0; c < 4; ++c) {
+                       const float f = bf_bits2f(__ldg(e + c));
+                       if (!isfinite(f)) o[c] += f;
+                     }
+                   });
 }
 
 template <int D, int RT, int CL>
@@ -138,12 +141,16 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
     prefetch_tmap(&kvmap);
   }
   griddep_launch_dependents();
+  if (CL > 1) {  // the barriers of all its CTAs are set up
+    __syncwarp();
+    cluster_arrive_all();
+  }
   griddep_wait();
   long long W, G, u0, u1;
   const long long worker = blockIdx.x / CL;
   const int rank = CL > 1 ? (int)cluster_rank() : 0;
-  if (CL > 1) cluster_sync_all();  // the barriers of all its CTAs are set up
-  split_setup<Sh::kThreads>(a.p, a.s, tab, a.min_units, worker, gridDim.x / CL, W, G, u0, u1);
+  split_setup(a.p, a.s, tab, a.min_units, worker, gridDim.x / CL, W, G, u0, u1);
+  if (CL > 1) cluster_wait_all();
   SplitWalk w(a.s, tab, u0, u1);
   const int page_mask = a.p.page - 1;
 
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
       if (lane == 0) mbar_arrive(&empty[st]);
     }
 
-    // join the warps that share this row tile's positions
+    // the warps' parts to shared memory
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(~0u, l[e], 1);
@@ -361,9 +368,15 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
     }
     if (found) s_flag[2 + (seg & 1)] = seg + 1;
     named_bar_sync(1, kCons);
+    const int ct = threadIdx.x, items = rows * (D / 4);
+    if (s_flag[2 + (seg & 1)] == seg + 1) {
+      for (int x = ct; x < items; x += kCons)
+        add_edge_values<D, kKeys, kBlk, kKS>(a.p, a.s.window, w.b, w.h, er,
+                                             pos0 + x / (D / 4) / a.group, w.j, w.n, rank, CL,
+                                             x / (D / 4), (x % (D / 4)) * 4, scratch);
+      named_bar_sync(1, kCons);
+    }
     const bool aborted = s_flag[0] != 0;
-    const bool poison = s_flag[2 + (seg & 1)] == seg + 1;
-    const int ct = threadIdx.x;
     const long long ut = w.tile_unit();
     auto store = [&](int r, int d, const State& s) {
       const int t = r / a.group, g = r - t * a.group;
@@ -376,79 +389,96 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
         a.lse[tok * a.hq + head] =
             s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * 0.6931471805599453f;
     };
-    // the state of four columns of a row over the warps that share the row tile
+    // four columns of a row over the warps that share the row tile
     auto own = [&](int r, int d) -> State {
-      const int wr = (r >> 4) * kKS, rr = r & 15;
+      const int at = ((r >> 4) * kKS * 16) + (r & 15);
       State s = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
-#pragma unroll
-      for (int k = 0; k < kKS; ++k) s.m = fmaxf(s.m, sc_ml[((wr + k) * 16 + rr) * 2]);
+      float2 ml[kKS];
 #pragma unroll
       for (int k = 0; k < kKS; ++k) {
-        const float mk = sc_ml[((wr + k) * 16 + rr) * 2];
-        const float f = s.m == -INFINITY ? 1.f : exp2_approx(mk - s.m);
-        const float4 q4 =
-            *reinterpret_cast<const float4*>(scratch + ((wr + k) * 16 + rr) * Sh::kLd + d);
-        s.l += f * sc_ml[((wr + k) * 16 + rr) * 2 + 1];
-        s.v.x += f * q4.x;
-        s.v.y += f * q4.y;
-        s.v.z += f * q4.z;
-        s.v.w += f * q4.w;
+        ml[k] = *reinterpret_cast<const float2*>(sc_ml + (at + k * 16) * 2);
+        s.m = fmaxf(s.m, ml[k].x);
       }
-      if (poison)
-        for (int k = rank; k < w.n; k += CL)  // the positions of this CTA
-          add_edge_values<D>(a.p, a.s.window, w.b, w.h, er, pos0 + r / a.group,
-                             (w.j + k) * kKeys, d, s);
+#pragma unroll
+      for (int k = 0; k < kKS; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(scratch + (at + k * 16) * Sh::kLd + d);
+        const float f = s.m == -INFINITY ? 1.f : exp2_approx(ml[k].x - s.m);
+        s.l += f * ml[k].y;
+        s.v.x += f * v.x;
+        s.v.y += f * v.y;
+        s.v.z += f * v.z;
+        s.v.w += f * v.w;
+      }
       return s;
     };
-    const int items = rows * (D / 4);
-    if (CL > 1) {
-      // in a cluster: this CTA's part to shared memory; then each CTA joins
-      // every CL-th run of columns from all of them. Two buffers: whoever
-      // writes one again has seen every CTA arrive for the other, after
-      // reading this one.
-      float* buf = merged + (seg & 1) * (Sh::kMerged / 4);
-#pragma unroll 1
-      for (int x = ct; x < items; x += kCons) {
-        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-        const State s = own(r, d);
-        *reinterpret_cast<float4*>(buf + r * D + d) = s.v;
-        if (d == 0) *reinterpret_cast<float2*>(buf + Sh::kRows * D + r * 2) = make_float2(s.m, s.l);
-      }
-      named_bar_sync(1, kCons);
-      if (ct < CL) mbar_arrive_remote(peers, ct);
-      if (!mbar_wait_cluster(peers, seg & 1, a.timeout_ns, a.p.status)) s_flag[0] = 1;
-    }
-    // the item's state over the whole segment
-    auto part = [&](int r, int d) -> State {
-      if (CL == 1) return own(r, d);
-      const float* buf = merged + (seg & 1) * (Sh::kMerged / 4);
-      float4 v[CL];
-      float2 ml[CL];
-#pragma unroll
-      for (int k = 0; k < CL; ++k) {
-        v[k] = ld_dsmem_f32x4(buf + r * D + d, k);
-        ml[k] = ld_dsmem_f32x2(buf + Sh::kRows * D + r * 2, k);
-      }
-      State s = {v[0], ml[0].x, ml[0].y};
-#pragma unroll
-      for (int k = 1; k < CL; ++k) s.add(v[k], ml[k].x, ml[k].y);
-      return s;
-    };
-    const int x0 = rank * kCons + ct;
     // A tile shared with other workers: its first one ends its range with it
     // (slot 1), the others begin with it (slot 0). The CTAs of rank r of each
     // see to the same columns, so that the last of them joins these.
     auto slot_of = [&](long long c, bool first) { return a.ws + (c * 2 + (first ? 1 : 0)) * Sh::kSlot; };
     float* mine = slot_of(worker, ut >= u0);
-#pragma unroll 1
-    for (int x = x0; x < items; x += CL * kCons) {
-      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-      const State s = part(r, d);
+    auto put = [&](int x, const State& s) {
       if (w.whole) {
-        if (!aborted) store(r, d, s);
+        if (!aborted) store(x / (D / 4), (x % (D / 4)) * 4, s);
       } else {
         __stcg(reinterpret_cast<float4*>(DG_AT(a.p.status, mine, x * 4, Sh::kSlot - 3)), s.v);
         __stcg(reinterpret_cast<float2*>(mine + Sh::kItems * 4 + x * 2), make_float2(s.m, s.l));
+      }
+    };
+    // In a cluster this CTA's part goes to shared memory first. Two buffers:
+    // whoever writes one again has seen every CTA arrive for the other, after
+    // reading this one.
+    float* buf = merged + (seg & 1) * (Sh::kMerged / 4);
+    constexpr int kBatch = 4;  // items whose loads are in flight together
+#pragma unroll 1
+    for (int x0 = ct; x0 < items; x0 += kBatch * kCons) {
+      State s[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int x = x0 + q * kCons < items ? x0 + q * kCons : x0;
+        s[q] = own(x / (D / 4), (x % (D / 4)) * 4);
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int x = x0 + q * kCons, r = x / (D / 4), d = (x % (D / 4)) * 4;
+        if (x >= items) break;
+        if (CL == 1) {
+          put(x, s[q]);
+        } else {
+          *reinterpret_cast<float4*>(buf + r * D + d) = s[q].v;
+          if (d == 0)
+            *reinterpret_cast<float2*>(buf + Sh::kRows * D + r * 2) = make_float2(s[q].m, s[q].l);
+        }
+      }
+    }
+    // the items this CTA sees to: in a cluster one run of them, joined over all
+    // its CTAs, two lanes to an item with half of the CTAs each
+    const int per = CL > 1 ? (items + CL - 1) / CL : items;
+    const int first = rank * per, last = first + per < items ? first + per : items;
+    if (CL > 1) {
+      named_bar_sync(1, kCons);
+      if (ct < CL) mbar_arrive_remote(peers, ct);
+      if (!mbar_wait_cluster(peers, seg & 1, a.timeout_ns, a.p.status)) s_flag[0] = 1;
+#pragma unroll 1
+      for (int x0 = first; x0 < last; x0 += kCons / 2) {
+        const int x = x0 + ct / 2, xr = x < last ? x : first;
+        const int r = xr / (D / 4), d = (xr % (D / 4)) * 4;
+        float4 v[CL / 2 + 1];
+        float2 ml[CL / 2 + 1];
+#pragma unroll
+        for (int k = 0; k < CL / 2; ++k) {
+          const uint32_t cta = (ct & 1) * (CL / 2) + k;
+          v[k] = ld_dsmem_f32x4(buf + r * D + d, cta);
+          ml[k] = ld_dsmem_f32x2(buf + Sh::kRows * D + r * 2, cta);
+        }
+        State s = {v[0], ml[0].x, ml[0].y};
+#pragma unroll
+        for (int k = 1; k < CL / 2; ++k) s.add(v[k], ml[k].x, ml[k].y);
+        const float4 v2 = make_float4(__shfl_xor_sync(~0u, s.v.x, 1), __shfl_xor_sync(~0u, s.v.y, 1),
+                                      __shfl_xor_sync(~0u, s.v.z, 1), __shfl_xor_sync(~0u, s.v.w, 1));
+        const float m2 = __shfl_xor_sync(~0u, s.m, 1), l2 = __shfl_xor_sync(~0u, s.l, 1);
+        if (x >= last || (ct & 1)) continue;
+        s.add(v2, m2, l2);
+        put(x, s);
       }
     }
     if (w.whole) {
@@ -470,7 +500,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
     if (s_flag[1] && !aborted) {
       constexpr int kAhead = 4;  // parts in flight
 #pragma unroll 1
-      for (int x = x0; x < items; x += CL * kCons) {
+      for (int x = first + ct; x < last; x += kCons) {
         State s = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
 #pragma unroll 1
         for (int k0 = 0; k0 < nc; k0 += kAhead) {

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   long long W, G, u0, u1;
-  split_setup<kTcAttnThreads>(a.p, a.s, tab, a.min_units, blockIdx.x, gridDim.x, W, G, u0, u1);
+  split_setup(a.p, a.s, tab, a.min_units, blockIdx.x, gridDim.x, W, G, u0, u1);
   SplitWalk w(a.s, tab, u0, u1);
 
   auto edges = [&]() -> EdgeRange {
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
           tmem_settle<16>(o);
           if (live)
             edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, lo, hi, w.j * kTcKeys,
-                           (w.j + w.n) * kTcKeys, q, [&](const uint16_t* v) {
+                           (w.j + w.n) * kTcKeys, q, [&](const uint16_t* v, int) {
 #pragma unroll
                              for (int e = 0; e < 16; ++e) {
                                const float f = bf_bits2f(__ldg(v + e));

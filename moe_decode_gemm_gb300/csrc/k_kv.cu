@@ -202,6 +202,41 @@ cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c) {
   return v.dim == 64 ? launch_append_d<64>(cx, a) : launch_append_d<128>(cx, a);
 }
 
+// ------------------------------------------------------------------ page copies
+// Pages move in chunks of 16 KB (256 threads): a chunk of one page of one layer
+// for each pass of a CTA, 64 bytes in flight per thread.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyChunk = kCopyThreads * 64;
+
+template <int NT, typename Pair>
+__device__ __forceinline__ void copy_pages(const KvPool& p, int n, const Pair& pair) {
+  constexpr int kChunk = NT * 64;
+  const int chunks = (int)((p.page_bytes + kChunk - 1) / kChunk);
+  const long long total = (long long)n * p.layers * chunks;
+  for (long long x = blockIdx.x; x < total; x += gridDim.x) {
+    const int i = (int)(x / ((long long)p.layers * chunks));
+    const int rest = (int)(x - (long long)i * p.layers * chunks);
+    const int layer = rest / chunks;
+    const long long at = (long long)(rest - layer * chunks) * kChunk;
+    int src, dst;
+    if (!pair(i, src, dst)) continue;
+    const uint8_t* s = p.data + layer * p.layer_stride + src * p.page_stride + at;
+    uint8_t* d = p.data + layer * p.layer_stride + dst * p.page_stride + at;
+    const long long left = p.page_bytes - at;
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int o = (k * NT + threadIdx.x) * 16;
+      if (o < left) v[k] = __ldcs(reinterpret_cast<const uint4*>(s + o));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int o = (k * NT + threadIdx.x) * 16;
+      if (o < left) __stcs(reinterpret_cast<uint4*>(d + o), v[k]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ page state
 // refs[page] counts the table entries that hold a page; 0 is free. A call's
 // new pages are the lowest free ones, in the order of its requests: a rank
@@ -430,39 +465,17 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     p.info[1] = lacking ? free_pages : free_pages - total + freed;
     p.info[2] = lacking ? 0 : copies;
   }
-}
-
-// ------------------------------------------------------------------ page copies
-// Pages move in chunks of 16 KB: a chunk of one page of one layer for each
-// pass of a CTA, 64 bytes in flight per thread.
-constexpr int kCopyThreads = 256;
-constexpr int kCopyChunk = kCopyThreads * 64;
-
-template <typename Pair>
-__device__ __forceinline__ void copy_pages(const KvPool& p, int n, const Pair& pair) {
-  const int chunks = (int)((p.page_bytes + kCopyChunk - 1) / kCopyChunk);
-  const long long total = (long long)n * p.layers * chunks;
-  for (long long x = blockIdx.x; x < total; x += gridDim.x) {
-    const int i = (int)(x / ((long long)p.layers * chunks));
-    const int rest = (int)(x - (long long)i * p.layers * chunks);
-    const int layer = rest / chunks;
-    const long long at = (long long)(rest - layer * chunks) * kCopyChunk;
-    int src, dst;
-    if (!pair(i, src, dst)) continue;
-    const uint8_t* s = p.data + layer * p.layer_stride + src * p.page_stride + at;
-    uint8_t* d = p.data + layer * p.layer_stride + dst * p.page_stride + at;
-    const long long left = p.page_bytes - at;
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int o = (k * kCopyThreads + threadIdx.x) * 16;
-      if (o < left) v[k] = __ldcs(reinterpret_cast<const uint4*>(s + o));
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int o = (k * kCopyThreads + threadIdx.x) * 16;
-      if (o < left) __stcs(reinterpret_cast<uint4*>(d + o), v[k]);
-    }
+  // A cut sequence's copies of pages that others hold are few, mostly none:
+  // this cluster makes them itself, where a second kernel would cost every
+  // call 2 us and its launch. A fork copies a page for most of its sequences:
+  // that takes the whole device.
+  if (!FORK && copies && !lacking) {
+    cluster_sync_all();
+    copy_pages<kPoolThreads>(p, a.n, [&](int i, int& s, int& d) {
+      s = __ldcg(a.pairs + 2 * i);
+      d = __ldcg(a.pairs + 2 * i + 1);
+      return s >= 0;
+    });
   }
 }
 
@@ -470,7 +483,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     kv_copy_kernel(const KvPool p, const int32_t* src, const int32_t* dst, int step, int n, int* status) {
   griddep_launch_dependents();
   griddep_wait();
-  copy_pages(p, n, [&](int i, int& s, int& d) {
+  copy_pages<kCopyThreads>(p, n, [&](int i, int& s, int& d) {
     s = __ldcg(src + (long long)i * step);
     if (s == -1) return false;
     d = __ldcg(dst + (long long)i * step);
@@ -553,7 +566,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_move_kernel(const KvPool p, c
     const int m = __ldcg(ranks + pg) - l0;
     if (m < moves) *t = __ldcg(holes + m);
   }
-  copy_pages(p, moves, [&](int i, int& s, int& d) {
+  copy_pages<kCopyThreads>(p, moves, [&](int i, int& s, int& d) {
     s = __ldcg(movers + l0 + i);
     d = __ldcg(holes + i);
     return true;
@@ -576,10 +589,8 @@ cudaError_t launch_kv_copy(const Ctx& cx, const KvPool& p, const int32_t* src, c
 cudaError_t launch_kv_resize(const Ctx& cx, const KvPool& p, const int32_t* seqs,
                              const int32_t* len, int n, int* pairs) {
   PoolArgs a = {p, seqs, nullptr, len, n, pairs, cx.status};
-  cudaError_t e = launch_k(kv_change_kernel<false>, dim3(kPoolCtas), dim3(kPoolThreads), 0, cx.stream,
-                           cx.pdl, a);
-  if (e != cudaSuccess || !len) return e;  // all lengths 0: nothing to copy
-  return launch_kv_copy(cx, p, pairs, pairs + 1, 2, n);
+  return launch_k(kv_change_kernel<false>, dim3(kPoolCtas), dim3(kPoolThreads), 0, cx.stream, cx.pdl,
+                  a);
 }
 
 cudaError_t launch_kv_fork(const Ctx& cx, const KvPool& p, const int32_t* src, const int32_t* dst,

@@ -165,7 +165,7 @@ __device__ __forceinline__ bool clean_edge_value(uint4* at, const EdgeRange& er,
   return any;
 }
 
-// Calls f(pointer to column d) for each position in [kbeg, kend) that a row
+// Calls f(pointer to column d, position) for each position in [kbeg, kend) that a row
 // seeing [lo, hi] sees and some other row of its tile does not.
 template <int D, typename F>
 __device__ __forceinline__ void edge_values(const PagedArgs& p, int row, int h, const EdgeRange& er,
@@ -182,7 +182,7 @@ __device__ __forceinline__ void edge_values(const PagedArgs& p, int row, int h, 
       const int pg = __ldg(p.table + row * p.table_stride + (key >> p.page_shift));
       if (pg < 0 || pg >= p.pages) continue;
       f(p.cache + pg * p.page_stride +
-        ((long long)(p.hkv + h) * p.page + (key & (p.page - 1))) * D + d);
+        ((long long)(p.hkv + h) * p.page + (key & (p.page - 1))) * D + d, key);
     }
   }
 }
@@ -190,134 +190,155 @@ __device__ __forceinline__ void edge_values(const PagedArgs& p, int row, int h, 
 // Shared-memory tables of a call's sequences (sized for the batch).
 struct SplitTables {
   long long* base;   // [batch + 1] first unit of each sequence
-  long long* wsum;   // [32] scan scratch
+  long long* head;   // [4] the call's units and workers, this worker's range
   int* qn;           // [batch] new tokens
   int* kv;           // positions
-  int* loc;          // [4] this CTA's first sequence, head, row tile, unit in it; row tiles
+  int* loc;          // [4] this worker's first sequence, head, row tile, unit in it
   static __host__ __device__ constexpr int bytes(int batch) {
-    return 8 * (batch + 1) + 8 * 32 + 8 * batch + 24;
+    return 8 * (batch + 1) + 8 * 4 + 8 * batch + 16;
   }
   __device__ explicit SplitTables(void* smem, int batch) {
     base = reinterpret_cast<long long*>(smem);
-    wsum = base + batch + 1;
-    qn = reinterpret_cast<int*>(wsum + 32);
+    head = base + batch + 1;
+    qn = reinterpret_cast<int*>(head + 4);
     kv = qn + batch;
     loc = kv + batch;
   }
 };
 
 // Fill the tables and find the range [u0, u1) of the W units that worker c of
-// `workers` (a CTA or a cluster) has, and where it begins. Called by all NT
+// `workers` (a CTA or a cluster) has, and where it begins. Called by all
 // threads of the CTA; ends with a barrier. G: workers that take part.
-template <int NT>
+//
+// One warp does it, a lane for each of 32 sequences at a time: every call waits
+// for this before it can do anything else, and the other warps would add
+// barriers, not speed.
 __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape& s,
                                             const SplitTables& t, int min_units, long long c,
                                             long long workers, long long& W, long long& G,
                                             long long& u0, long long& u1) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) t.loc[4] = 0;
-  __syncthreads();
-  constexpr int kFew = 4;  // row tiles of a sequence that one thread counts by itself
-  // units of each sequence and head, into base[b + 1]
-  for (int b = tid; b < p.batch; b += NT) {
-    int q0, qn;
-    paged_tokens(p, b, q0, qn);
-    const int row = paged_row(p, b);
-    const int kv = paged_len(p, row);
-    t.qn[b] = qn;
-    t.kv[b] = kv;
-    const int tiles = (qn + s.tq - 1) / s.tq;
-    long long u = 0;
-    if (tiles <= kFew)
-      for (int i = 0; i < tiles; ++i) u += tile_range(s, qn, kv, i).n + s.start;
-    t.base[b + 1] = u;
-    if (tiles) atomicAdd(&t.loc[4], tiles);
-  }
-  __syncthreads();
-  for (int b = warp; b < p.batch; b += NT / 32) {
-    const int qn = t.qn[b], tiles = (qn + s.tq - 1) / s.tq;
-    if (tiles <= kFew) continue;
-    long long u = 0;
-    for (int i = lane; i < tiles; i += 32) u += tile_range(s, qn, t.kv[b], i).n + s.start;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    constexpr int kFew = 2;  // row tiles of a sequence that one lane counts by itself
+    struct Raw {
+      int a, e, row, kv;
+    };
+    auto fetch = [&](int b) -> Raw {
+      Raw r = {0, 0, 0, 0};
+      if (b < p.batch) {
+        r.row = p.rows ? __ldg(p.rows + b) : b;
+        r.a = __ldg(p.cu_q + b);
+        r.e = __ldg(p.cu_q + b + 1);
+        if (r.row >= 0 && r.row < p.table_rows) r.kv = __ldg(p.kv_len + r.row);
+      }
+      return r;
+    };
+    const long long cap = (long long)p.width << p.page_shift;
+    long long units = 0;
+    int all_tiles = 0;
+    Raw next = fetch(lane);
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const Raw r = next;
+      const int b = b0 + lane;
+      if (b0 + 32 < p.batch) next = fetch(b + 32);
+      const int q0 = r.a < 0 ? 0 : (r.a > p.tokens ? p.tokens : r.a);
+      const int q1 = r.e < q0 ? q0 : (r.e > p.tokens ? p.tokens : r.e);
+      const int kv = r.kv < 0 ? 0 : (r.kv > cap ? (int)cap : r.kv), qn = q1 - q0;
+      if (b < p.batch) {
+        t.qn[b] = qn;
+        t.kv[b] = kv;
+        if (p.status && (q0 != r.a || q1 != r.e || kv != r.kv || r.row < 0 || r.row >= p.table_rows))
+          atomicOr(p.status, kStatusBounds);
+      }
+      const int tiles = (qn + s.tq - 1) / s.tq;
+      long long u = 0;
+      if (tiles <= kFew)
+        for (int i = 0; i < tiles; ++i) u += tile_range(s, qn, kv, i).n + s.start;
+#pragma unroll 1
+      for (unsigned big = __ballot_sync(~0u, tiles > kFew); big; big &= big - 1) {
+        const int l = __ffs(big) - 1, n = __shfl_sync(~0u, tiles, l);
+        const int lq = __shfl_sync(~0u, qn, l), lkv = __shfl_sync(~0u, kv, l);
+        long long sum = 0;
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) sum += tile_range(s, lq, lkv, i).n + s.start;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(~0u, u, o);
-    if (lane == 0) t.base[b + 1] = u;
-  }
-  __syncthreads();
-  // inclusive scan of base[1 .. batch] (units of all heads)
-  const int per = (p.batch + NT - 1) / NT;
-  long long mine = 0;
-  for (int k = 0; k < per; ++k) {
-    const int b = tid * per + k;
-    if (b < p.batch) mine += t.base[b + 1] * s.hkv;
-  }
-  long long inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(~0u, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) t.wsum[warp] = inc;
-  __syncthreads();
-  long long at = inc - mine;
-  for (int w = 0; w < warp; ++w) at += t.wsum[w];
-  for (int k = 0; k < per; ++k) {
-    const int b = tid * per + k;
-    if (b < p.batch) {
-      at += t.base[b + 1] * s.hkv;
-      t.base[b + 1] = at;
-    }
-  }
-  if (tid == 0) t.base[0] = 0;
-  __syncthreads();
-  W = t.base[p.batch];
-  // no more workers than give each min_units, but one for each row tile
-  G = W / min_units;
-  if (G < (long long)t.loc[4] * s.hkv) G = (long long)t.loc[4] * s.hkv;
-  if (G < 1) G = 1;
-  if (G > workers) G = workers;
-  u0 = c < G ? cta_start(c, W, G) : 0;
-  u1 = c < G ? cta_start(c + 1, W, G) : 0;
-  if (warp == 0 && u0 < u1) {
-    int lo = 0, hi = p.batch - 1;  // last sequence with base <= u0 (and units)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (t.base[mid] <= u0) lo = mid;
-      else hi = mid - 1;
-    }
-    const int b = lo;
-    const long long U = (t.base[b + 1] - t.base[b]) / s.hkv;
-    const long long r = u0 - t.base[b];
-    const int h = (int)(r / U);
-    long long off = r - h * U;
-    int i = 0;
-    const int qn = t.qn[b], kv = t.kv[b];
-    for (;; i += 32) {
-      // past the last row tile the ranges are not used: off ends before them
-      const int n = tile_range(s, qn, kv, i + lane).n + s.start;
-      int sum = n;
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == l) u = sum;
+      }
+      u *= s.hkv;
+      all_tiles += __reduce_add_sync(~0u, tiles);
+      long long inc = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(~0u, sum, o);
-        if (lane >= o) sum += v;
+        const long long v = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += v;
       }
-      const unsigned past = __ballot_sync(~0u, (long long)sum > off);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        off -= __shfl_sync(~0u, sum - n, l);
-        i += l;
-        break;
-      }
-      off -= __shfl_sync(~0u, sum, 31);
+      if (b < p.batch) t.base[b] = units + inc - u;
+      units += __shfl_sync(~0u, inc, 31);
     }
+    if (lane == 0) t.base[p.batch] = units;
+    __syncwarp();
+    // no more workers than give each min_units, but one for each row tile
+    long long g = div_small(units, min_units);
+    if (g < (long long)all_tiles * s.hkv) g = (long long)all_tiles * s.hkv;
+    if (g < 1) g = 1;
+    if (g > workers) g = workers;
+    const long long from = c < g ? div_small(c * units, g) : 0;
+    const long long to = c < g ? div_small((c + 1) * units, g) : 0;
     if (lane == 0) {
-      t.loc[0] = b;
-      t.loc[1] = h;
-      t.loc[2] = i;
-      t.loc[3] = (int)off;
+      t.head[0] = units;
+      t.head[1] = g;
+      t.head[2] = from;
+      t.head[3] = to;
+    }
+    if (from < to) {
+      int b = -1;  // the last sequence with base <= from
+#pragma unroll 1
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int n = __popc(
+            __ballot_sync(~0u, b0 + lane < p.batch && t.base[b0 + lane < p.batch ? b0 + lane : 0] <= from));
+        b += n;
+        if (n < 32) break;
+      }
+      const long long U = div_small(t.base[b + 1] - t.base[b], s.hkv);
+      const long long r = from - t.base[b];
+      const int h = (int)div_small(r, U);
+      long long off = r - h * U;
+      int i = 0;
+      const int qn = t.qn[b], kv = t.kv[b];
+#pragma unroll 1
+      for (;; i += 32) {
+        // past the last row tile the ranges are not used: off ends before them
+        const int n = tile_range(s, qn, kv, i + lane).n + s.start;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(~0u, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const unsigned past = __ballot_sync(~0u, (long long)sum > off);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          off -= __shfl_sync(~0u, sum - n, l);
+          i += l;
+          break;
+        }
+        off -= __shfl_sync(~0u, sum, 31);
+      }
+      if (lane == 0) {
+        t.loc[0] = b;
+        t.loc[1] = h;
+        t.loc[2] = i;
+        t.loc[3] = (int)off;
+      }
     }
   }
   __syncthreads();
+  W = t.head[0];
+  G = t.head[1];
+  u0 = t.head[2];
+  u1 = t.head[3];
 }
 
 // Walks this CTA's range segment by segment: a segment is the part of one row

@@ -60,20 +60,54 @@ def _same(what, device, t, dtype, dims=None, shape=None, row_stride=False):
     return t
 
 
+def _rows(what, h, t, dtype):
+    """A matrix whose rows may be further apart than their length: its rows,
+    row length and row stride. (The calls of a decode step are short: what they
+    pass is looked over in few steps, and _same says what is wrong with it.)"""
+    try:
+        if t.dtype is dtype and t.get_device() == h._index:
+            n, width = t.shape
+            ld, one = t.stride()
+            if one == 1:
+                # a single row's stride says nothing
+                return n, width, (ld if n > 1 or ld > width else width)
+    except (AttributeError, ValueError):
+        pass
+    _same(what, h.device, t, dtype, dims=2, row_stride=True)
+    raise ValueError("%s: needs unit column stride" % what)  # a column of length 1
+
+
+def _list(what, h, t, dtype, n=None):
+    """A contiguous vector (of n elements); its length."""
+    try:
+        if (t.dtype is dtype and t.get_device() == h._index and t.dim() == 1
+                and t.is_contiguous() and (n is None or t.shape[0] == n)):
+            return t.shape[0]
+    except AttributeError:
+        pass
+    _same(what, h.device, t, dtype, dims=1, shape=None if n is None else (n,))
+
+
+class _Handle:
+    """What both handles keep: the device, and torch's names that the calls use."""
+
+    def _bind(self, device):
+        import torch
+
+        self.device, self._index = device, device.index
+        self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
+        self._empty, self._current = torch.empty, torch._C._cuda_getCurrentRawStream
+
+    def _stream(self, stream):
+        return self._current(self._index) if stream is None else stream.cuda_stream
+
+
 def _row_stride(t):
     """Elements between rows (a single row's stride says nothing)."""
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
 
 
-def _raw_stream(device, stream):
-    import torch
-
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-class PagedKV:
+class PagedKV(_Handle):
     """One layer's cache and the batch of sequences that calls work on.
 
     cache [pages, 2, heads, page_size, dim] bf16 (pages may be further apart
@@ -106,7 +140,7 @@ class PagedKV:
                                                                    cu_q.shape[0] - 1))
         _same("kv_len", dev, kv_len, i32, shape=(table.shape[0],))
         self.cache, self.table, self.cu_q, self.kv_len, self.rows = cache, table, cu_q, kv_len, rows
-        self.device = dev
+        self._bind(dev)
         pages, _, self.heads, self.page_size, self.dim = cache.shape
         page = 2 * self.heads * self.page_size * self.dim
         self._view = _View(
@@ -125,7 +159,7 @@ class PagedKV:
         self._view.max_q = int(n)
 
 
-class KVPool:
+class KVPool(_Handle):
     """The pages of all layers of a cache and the state of its sequences.
 
     data [layers, pages, ...] of any type (a page of a layer is contiguous;
@@ -158,7 +192,7 @@ class KVPool:
             if info.shape[0] < 3:
                 raise ValueError("info: expected 3 elements or more")
         self.data, self.refs, self.table, self.lens, self.info = data, refs, table, lens, info
-        self.device = dev
+        self._bind(dev)
         size = data.element_size()
         page = data[0, 0].numel() * size
         self._pool = _Pool(
@@ -183,35 +217,38 @@ def kv_append(qkv, kv, rope, wq=None, wk=None, eps=1e-6, q=None, positions=None,
     fp32: rot/2 cosines, then rot/2 sines. wq, wk: [dim] bf16 norm weights, or
     both None. Returns q [T, Hq*dim] bf16 (a new tensor if None; may be
     qkv[:, :Hq*dim])."""
-    import torch
-
-    dev, dim = kv.device, kv.dim
-    bf = torch.bfloat16
-    _same("qkv", dev, qkv, bf, dims=2, row_stride=True)
-    T, width = qkv.shape
+    dim, bf = kv.dim, kv._bf16
+    T, width, ld = _rows("qkv", kv, qkv, bf)
     hq = width // dim - 2 * kv.heads
     if hq < 1 or width % dim:
         raise ValueError("qkv: expected [T, (Hq + %d)*%d], got shape %s"
                          % (2 * kv.heads, dim, tuple(qkv.shape)))
-    _same("rope", dev, rope, torch.float32, dims=2)
-    if (wq is None) != (wk is None):
+    positions_at, rot, ld_rope = _rows("rope", kv, rope, kv._f32)
+    if ld_rope != rot:
+        raise ValueError("rope: must be contiguous")
+    wqp = wkp = pos = None
+    if wq is not None and wk is not None:
+        _list("wq", kv, wq, bf, dim)
+        _list("wk", kv, wk, bf, dim)
+        wqp, wkp = wq.data_ptr(), wk.data_ptr()
+    elif wq is not wk:
         raise ValueError("wq and wk: give both or neither")
-    if wq is not None:
-        _same("wq", dev, wq, bf, shape=(dim,))
-        _same("wk", dev, wk, bf, shape=(dim,))
     if positions is not None:
-        _same("positions", dev, positions, torch.int32, shape=(T,))
+        _list("positions", kv, positions, kv._i32, T)
+        pos = positions.data_ptr()
     if q is None:
-        q = torch.empty((T, hq * dim), dtype=bf, device=dev)
+        q = kv._empty((T, hq * dim), dtype=bf, device=kv.device)
+        ldq = hq * dim
     else:
-        _same("q", dev, q, bf, shape=(T, hq * dim), row_stride=True)
-    if T == 0:
-        return q
-    _check(lib().kv_append(
-        kv._ref, qkv.data_ptr(), _row_stride(qkv), None if wq is None else wq.data_ptr(),
-        None if wk is None else wk.data_ptr(), eps, rope.data_ptr(), rope.shape[0], rope.shape[1],
-        1 if interleaved else 0, None if positions is None else positions.data_ptr(), q.data_ptr(),
-        _row_stride(q), T, hq, _raw_stream(dev, stream)), "kv_append")
+        rows, cols, ldq = _rows("q", kv, q, bf)
+        if rows != T or cols != hq * dim:
+            raise ValueError("q: expected shape %s, got %s" % ((T, hq * dim), tuple(q.shape)))
+    if T:
+        rc = lib().kv_append(kv._ref, qkv.data_ptr(), ld, wqp, wkp, eps, rope.data_ptr(),
+                             positions_at, rot, 1 if interleaved else 0, pos, q.data_ptr(), ldq, T,
+                             hq, kv._stream(stream))
+        if rc:
+            _check(rc, "kv_append")
     return q
 
 
@@ -220,27 +257,32 @@ def kv_attention(q, kv, out=None, lse=None, scale=None, window=0, stream=None):
     up to its own (the last ``window`` of them if window > 0). q [T, Hq*dim]
     bf16 (rows may be further apart); scale: 1/sqrt(dim) by default; lse:
     optional [T, Hq] fp32 output. Returns out [T, Hq*dim] bf16."""
-    import torch
-
-    dev, dim = kv.device, kv.dim
-    _same("q", dev, q, torch.bfloat16, dims=2, row_stride=True)
-    T, width = q.shape
+    dim, bf = kv.dim, kv._bf16
+    T, width, ldq = _rows("q", kv, q, bf)
     hq = width // dim
     if hq < 1 or width % dim or hq % kv.heads:
         raise ValueError("q: expected [T, Hq*%d] with Hq a multiple of %d, got shape %s"
                          % (dim, kv.heads, tuple(q.shape)))
     if out is None:
-        out = torch.empty((T, width), dtype=torch.bfloat16, device=dev)
+        out = kv._empty((T, width), dtype=bf, device=kv.device)
+        ldo = width
     else:
-        _same("out", dev, out, torch.bfloat16, shape=(T, width), row_stride=True)
+        rows, cols, ldo = _rows("out", kv, out, bf)
+        if rows != T or cols != width:
+            raise ValueError("out: expected shape %s, got %s" % ((T, width), tuple(out.shape)))
+    lsep = None
     if lse is not None:
-        _same("lse", dev, lse, torch.float32, shape=(T, hq))
-    if T == 0:
-        return out
-    _check(lib().kv_attention(
-        kv._ref, q.data_ptr(), _row_stride(q), out.data_ptr(), _row_stride(out),
-        None if lse is None else lse.data_ptr(), T, hq, dim ** -0.5 if scale is None else scale,
-        window, _raw_stream(dev, stream)), "kv_attention")
+        rows, cols, ld = _rows("lse", kv, lse, kv._f32)
+        if rows != T or cols != hq or ld != hq:
+            raise ValueError("lse: expected contiguous of shape %s, got %s" % ((T, hq),
+                                                                            tuple(lse.shape)))
+        lsep = lse.data_ptr()
+    if T:
+        rc = lib().kv_attention(kv._ref, q.data_ptr(), ldq, out.data_ptr(), ldo, lsep, T, hq,
+                                dim ** -0.5 if scale is None else scale, window,
+                                kv._stream(stream))
+        if rc:
+            _check(rc, "kv_attention")
     return out
 
 
@@ -250,51 +292,45 @@ def last_attention() -> str:
 
 
 # ---------------------------------------------------------------- the pages
-def _list(pool, what, t, n=None):
-    import torch
-
-    return _same(what, pool.device, t, torch.int32, dims=1, shape=None if n is None else (n,))
-
-
 def kv_resize(pool, seqs, lens, stream=None):
     """Set the lengths of sequences ``seqs`` to ``lens`` (int32 on the device):
     pages are taken (the lowest free ones, in order) or given back. All or
     nothing: pool.info[0] is the number of pages that were lacking."""
-    n = _list(pool, "seqs", seqs).shape[0]
-    _list(pool, "lens", lens, n)
+    n = _list("seqs", pool, seqs, pool._i32)
+    _list("lens", pool, lens, pool._i32, n)
     if n:
         _check(lib().kv_resize(pool._ref, seqs.data_ptr(), lens.data_ptr(), n,
-                               _raw_stream(pool.device, stream)), "kv_resize")
+                               pool._stream(stream)), "kv_resize")
 
 
 def kv_free(pool, seqs, stream=None):
     """Give back every page of sequences ``seqs``; their lengths become 0."""
-    n = _list(pool, "seqs", seqs).shape[0]
+    n = _list("seqs", pool, seqs, pool._i32)
     if n:
-        _check(lib().kv_free(pool._ref, seqs.data_ptr(), n, _raw_stream(pool.device, stream)),
+        _check(lib().kv_free(pool._ref, seqs.data_ptr(), n, pool._stream(stream)),
                "kv_free")
 
 
 def kv_fork(pool, src, dst, stream=None):
     """Sequence dst[i] becomes a copy of src[i]: full pages are shared, a last
     page that is partly filled is copied. What dst[i] held is given back."""
-    n = _list(pool, "src", src).shape[0]
-    _list(pool, "dst", dst, n)
+    n = _list("src", pool, src, pool._i32)
+    _list("dst", pool, dst, pool._i32, n)
     if n:
         _check(lib().kv_fork(pool._ref, src.data_ptr(), dst.data_ptr(), n,
-                             _raw_stream(pool.device, stream)), "kv_fork")
+                             pool._stream(stream)), "kv_fork")
 
 
 def kv_copy(pool, src, dst, stream=None):
     """Copy page src[i] to page dst[i] in every layer."""
-    n = _list(pool, "src", src).shape[0]
-    _list(pool, "dst", dst, n)
+    n = _list("src", pool, src, pool._i32)
+    _list("dst", pool, dst, pool._i32, n)
     if n:
         _check(lib().kv_copy(pool._ref, src.data_ptr(), dst.data_ptr(), n,
-                             _raw_stream(pool.device, stream)), "kv_copy")
+                             pool._stream(stream)), "kv_copy")
 
 
 def kv_compact(pool, stream=None):
     """Move pages so that the n pages in use are pages 0 .. n-1; the table and
     the reference counts follow."""
-    _check(lib().kv_compact(pool._ref, _raw_stream(pool.device, stream)), "kv_compact")
+    _check(lib().kv_compact(pool._ref, pool._stream(stream)), "kv_compact")
