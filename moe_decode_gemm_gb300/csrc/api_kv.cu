@@ -120,6 +120,7 @@ int kv_append(const dec_kv_view* kv, const void* qkv, int64_t ldqkv, const void*
     return DEC_EINVAL;
   if (!al(qkv, 16) || !al(q, 16) || !al(rope, 16) || !al(wq, 16) || !al(wk, 16) || !al(positions, 4))
     return DEC_EINVAL;
+  if ((int64_t)q_heads + 2 * v.hkv > 32768) return DEC_EUNSUPPORTED;
   Ctx cx;
   if ((rc = kv_context(stream, 0, 0, &cx, nullptr, nullptr))) return rc;
   const AppendCall c = {qkv, wq, wk, rope, positions, q, ldqkv, ldq, tokens, q_heads, rope_len, rot,
@@ -129,7 +130,7 @@ int kv_append(const dec_kv_view* kv, const void* qkv, int64_t ldqkv, const void*
 
 int kv_attention(const dec_kv_view* kv, const void* q, int64_t ldq, void* out, int64_t ldo, float* lse,
                  int tokens, int q_heads, float scale, int window, void* stream) {
-  const AttnCall c = {q, out, lse, ldq, ldo, tokens, q_heads, window, scale};
+  const AttnCall c = {q, out, lse, ldq, ldo, tokens, q_heads, window, kv ? kv->max_q : 0, scale};
   return attention(kv, c, stream);
 }
 

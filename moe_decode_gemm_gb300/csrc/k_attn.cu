@@ -600,14 +600,20 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
   a.ctr = ctr;
   a.ws_len = cx.ws_len;
   a.ctr_len = (int)cx.ctr_len;
-  a.s.start = 3;
-  a.min_units = 7;
+  a.s.start = 4;
+  a.min_units = 12;
   a.timeout_ns = cx.timeout_ns;
   const bool d64 = v.dim == 64;
   // Few row tiles: a cluster of 8 CTAs for each part of one, so that the parts
   // are joined through distributed shared memory and only a few partial tiles
-  // go through the workspace.
-  const long long tiles = ((long long)c.tokens / a.s.tq + v.batch) * v.hkv;
+  // go through the workspace. Its key tiles are read 8 at a time, so that what
+  // a row tile costs at its start weighs 8 times as many.
+  const long long tiles =
+      (c.max_q > 0 && c.max_q <= a.s.tq ? v.batch : (long long)c.tokens / a.s.tq + v.batch) * v.hkv;
+  if (tiles <= kClusterTiles) {
+    a.s.start = 40;
+    a.min_units = 96;
+  }
   if (rt == 1 && tiles <= kClusterTiles)
     return d64 ? launch_rt<64, 1, 8>(cx, map, a) : launch_rt<128, 1, 8>(cx, map, a);
   if (tiles <= kClusterTiles)

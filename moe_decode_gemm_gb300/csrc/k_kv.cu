@@ -18,8 +18,12 @@ namespace dg {
 // dependent loads (sequence, page, row of angles) at few.
 //
 // D/8 lanes hold a head, 8 elements each, so that the sum of squares is a few
-// shuffles and a pair's other half is in this lane or one shuffle away. A
-// thread has `U` heads' loads in flight before it looks up where they go.
+// shuffles and a pair's other half is in this lane or one shuffle away. A CTA
+// has one token's heads, or some of them: where the token goes and its angles
+// are looked up once, and a lane keeps the angles and weights of its elements
+// for all its heads. (Heads of any token on any lane, each with its own places
+// and angles, took twice the instructions and were bound by them: 80 us for
+// 7.9k tokens of 64 heads of 128.)
 constexpr int kAppendThreads = 256;
 
 struct AppendArgs {
@@ -32,154 +36,134 @@ struct AppendArgs {
   uint16_t* q;
   uint16_t* cache;
   long long ldqkv, ldq;
-  int hq, rope_len, rot, interleaved;
+  int hq, rope_len, rot;
   float eps;
 };
 
-template <int D, int U>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+template <int D, int U, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppendThreads, U > 1 && INTERLEAVED ? 5 : 4) append_kernel(const AppendArgs a) {
   constexpr int LG = D / 8;                      // lanes of a head
   constexpr int kGroups = kAppendThreads / LG;   // heads at a time
-  constexpr int kUnits = kGroups * U;            // heads of this CTA
-  extern __shared__ int s_cu[];                  // [batch + 1]
-  __shared__ int s_pos[kUnits], s_rope[kUnits], s_page[kUnits];
   const int H = a.hq + 2 * a.p.hkv;
-  const int tid = threadIdx.x, g = tid / LG, l = tid % LG;
-  const long long unit0 = (long long)blockIdx.x * kUnits;
-  const long long units = (long long)a.p.tokens * H;
+  const int tid = threadIdx.x, l = tid % LG, tok = blockIdx.x;
+  const int head0 = blockIdx.y * (kGroups * U) + tid / LG;
   griddep_launch_dependents();
   griddep_wait();
 
   uint4 x[U];
+  const uint16_t* src = a.qkv + tok * a.ldqkv + head0 * D + l * 8;
 #pragma unroll
   for (int k = 0; k < U; ++k) {
-    const long long u = unit0 + k * kGroups + g;
     x[k] = make_uint4(0, 0, 0, 0);
-    if (u < units) {
-      const int tok = (int)(u / H), head = (int)(u - (long long)tok * H);
-      x[k] = *reinterpret_cast<const uint4*>(a.qkv + tok * a.ldqkv + head * D + l * 8);
-    }
+    if (head0 + k * kGroups < H) x[k] = *reinterpret_cast<const uint4*>(src + k * kGroups * D);
   }
-  for (int b = tid; b <= a.p.batch; b += kAppendThreads) s_cu[b] = __ldg(a.p.cu_q + b);
-  __syncthreads();
-  const int tok0 = (int)(unit0 / H);
-  const long long last = unit0 + kUnits < units ? unit0 + kUnits : units;
-  const int ntok = (int)((last - 1) / H) - tok0 + 1;
-  for (int t = tid; t < ntok; t += kAppendThreads) {
-    const int tok = tok0 + t;
-    int lo = 0, hi = a.p.batch - 1;  // the last sequence that begins at or before tok
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_cu[mid] <= tok) lo = mid;
-      else hi = mid - 1;
-    }
-    int pos = -1, page = -1, rp = -1;  // rp < 0: the token belongs to no sequence
-    if (s_cu[lo] <= tok && tok < s_cu[lo + 1]) {
-      const int row = paged_row(a.p, lo);
-      pos = paged_len(a.p, row) - s_cu[lo + 1] + tok;
-      if (row >= 0 && pos >= 0) {
-        page = __ldg(a.p.table + row * a.p.table_stride + (pos >> a.p.page_shift));
-        if (page < 0 || page >= a.p.pages) page = -1;
-      }
-      rp = a.positions ? __ldg(a.positions + tok) : (pos < 0 ? 0 : pos);
-      if (rp < 0 || rp >= a.rope_len) {
-        if (a.p.status) atomicOr(a.p.status, kStatusBounds);
-        rp = rp < 0 ? 0 : a.rope_len - 1;
-      }
-      if (page < 0 && a.p.status) atomicOr(a.p.status, kStatusBounds);
-    }
-    s_pos[t] = pos;
-    s_page[t] = page;
-    s_rope[t] = rp;
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (a.wq) {
+    wq = __ldg(reinterpret_cast<const uint4*>(a.wq) + l);
+    wk = __ldg(reinterpret_cast<const uint4*>(a.wk) + l);
   }
-  __syncthreads();
+  // the token's sequence: as many as end at or before it come first
+  int b = 0;
+  for (int i = 0; i < a.p.batch; i += kAppendThreads)
+    b += __syncthreads_count(i + tid < a.p.batch && __ldg(a.p.cu_q + i + tid + 1) <= tok);
+  if (b >= a.p.batch) return;  // past the last sequence
+  const int first = __ldg(a.p.cu_q + b), end = __ldg(a.p.cu_q + b + 1);
+  const int row = paged_row(a.p, b);
+  if (first > tok) return;
+  const int pos = paged_len(a.p, row) - end + tok;
+  int rp = a.positions ? __ldg(a.positions + tok) : (pos < 0 ? 0 : pos);
+  int page = -1;
+  if (row >= 0 && pos >= 0) {
+    page = __ldg(a.p.table + row * a.p.table_stride + (pos >> a.p.page_shift));
+    if (page >= a.p.pages) page = -1;
+  }
+  if (a.p.status && (page < 0 || rp < 0 || rp >= a.rope_len)) atomicOr(a.p.status, kStatusBounds);
+  rp = rp < 0 ? 0 : (rp >= a.rope_len ? a.rope_len - 1 : rp);
 
+  // this lane's cosines and sines: of its 8 elements, or of its 4 pairs
   const int half = a.rot >> 1;
+  const bool turned = l * 8 < a.rot, second = !INTERLEAVED && l * 8 >= half;
+  const int other = turned ? (second ? l - half / 8 : l + half / 8) : l;
+  float c[INTERLEAVED ? 4 : 8], s[INTERLEAVED ? 4 : 8];
+  if (turned) {
+    const float* at = a.rope + (long long)rp * a.rot + (INTERLEAVED ? l * 4 : l * 8 - (second ? half : 0));
+#pragma unroll
+    for (int q = 0; q < (INTERLEAVED ? 1 : 2); ++q) {
+      const float4 cs = __ldg(reinterpret_cast<const float4*>(at) + q);
+      const float4 sn = __ldg(reinterpret_cast<const float4*>(at + half) + q);
+      const float sign = INTERLEAVED || second ? 1.f : -1.f;
+      c[q * 4] = cs.x, c[q * 4 + 1] = cs.y, c[q * 4 + 2] = cs.z, c[q * 4 + 3] = cs.w;
+      s[q * 4] = sign * sn.x, s[q * 4 + 1] = sign * sn.y;
+      s[q * 4 + 2] = sign * sn.z, s[q * 4 + 3] = sign * sn.w;
+    }
+  }
   // the lanes of this head: heads of one warp may take different branches
   const unsigned gmask = ((1u << LG) - 1) << (tid & 31 & ~(LG - 1));
+  uint16_t* const qdst = a.q + tok * a.ldq + l * 8;
+  // key heads, then value heads, as the cache has them
+  const long long step = (long long)a.p.page * D;
+  uint16_t* const kdst = a.cache + (page < 0 ? 0 : page) * a.p.page_stride +
+                         (long long)(pos & (a.p.page - 1)) * D + l * 8;
 #pragma unroll
   for (int k = 0; k < U; ++k) {
-    const long long u = unit0 + k * kGroups + g;
-    const bool live = u < units;
-    const int tok = live ? (int)(u / H) : tok0, head = live ? (int)(u - (long long)tok * H) : 0;
-    const int rp = s_rope[tok - tok0];
+    const int head = head0 + k * kGroups;
+    if (head >= H) break;
     uint4 out = x[k];
     if (head < a.hq + a.p.hkv) {
       float y[8];
-      unpack8(x[k], y);
+      unpack8(out, y);
       if (a.wq) {
         float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
         for (int o = LG / 2; o; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o, LG);
         const float r = rsqrtf(ss * (1.f / D) + a.eps);
         float w[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(head < a.hq ? a.wq : a.wk) + l), w);
+        unpack8(head < a.hq ? wq : wk, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
       }
-      const float* row = a.rope + (long long)(rp < 0 ? 0 : rp) * a.rot;
-      if (a.interleaved) {
-        if (l * 8 < a.rot) {
-          const float4 cs = __ldg(reinterpret_cast<const float4*>(row + l * 4));
-          const float4 sn = __ldg(reinterpret_cast<const float4*>(row + half + l * 4));
-          const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
+      if (INTERLEAVED) {
+        if (turned) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float e = y[2 * j], f = y[2 * j + 1];
-            y[2 * j] = e * c[j] - f * s[j];
-            y[2 * j + 1] = f * c[j] + e * s[j];
+          for (int e = 0; e < 4; ++e) {
+            const float p = y[2 * e], q = y[2 * e + 1];
+            y[2 * e] = p * c[e] - q * s[e];
+            y[2 * e + 1] = q * c[e] + p * s[e];
           }
         }
       } else {
-        const bool second = l * 8 >= half;
-        const int other = l * 8 < a.rot ? (second ? l - half / 8 : l + half / 8) : l;
         float z[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = __shfl_sync(gmask, y[j], other, LG);
-        if (l * 8 < a.rot) {
-          const float4* cp = reinterpret_cast<const float4*>(row + l * 8 - (second ? half : 0));
-          const float4* sp = cp + half / 4;
-          const float sign = second ? 1.f : -1.f;
+        for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(gmask, y[e], other, LG);
+        if (turned) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float4 cs = __ldg(cp + q), sn = __ldg(sp + q);
-            const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              y[q * 4 + j] = y[q * 4 + j] * c[j] + sign * (z[q * 4 + j] * s[j]);
-          }
+          for (int e = 0; e < 8; ++e)
+            y[e] = y[e] * c[INTERLEAVED ? 0 : e] + z[e] * s[INTERLEAVED ? 0 : e];
         }
       }
       out = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
                        pack_bf16(y[6], y[7]));
     }
-    if (!live || rp < 0) continue;
-    if (head < a.hq) {
-      *reinterpret_cast<uint4*>(a.q + tok * a.ldq + head * D + l * 8) = out;
-    } else {
-      const int page = s_page[tok - tok0], pos = s_pos[tok - tok0];
-      if (page >= 0)  // head - hq: key heads, then value heads, as the cache has them
-        *reinterpret_cast<uint4*>(a.cache + page * a.p.page_stride +
-                                  ((long long)(head - a.hq) * a.p.page + (pos & (a.p.page - 1))) * D +
-                                  l * 8) = out;
-    }
+    if (head < a.hq) *reinterpret_cast<uint4*>(qdst + head * D) = out;
+    else if (page >= 0) *reinterpret_cast<uint4*>(kdst + (head - a.hq) * step) = out;
   }
 }
 
-template <int D>
+template <int D, bool INTERLEAVED>
 static cudaError_t launch_append_d(const Ctx& cx, const AppendArgs& a) {
   constexpr int kGroups = kAppendThreads / (D / 8);
-  const long long units = (long long)a.p.tokens * (a.hq + 2 * a.p.hkv);
-  const size_t smem = (size_t)(a.p.batch + 1) * 4;
-  // few heads: one per thread group, spread over the SMs; many: four loads in
-  // flight per thread
-  if (units <= 2LL * cx.sms * kGroups)
-    return launch_k(append_kernel<D, 1>, dim3((unsigned)((units + kGroups - 1) / kGroups)),
-                    dim3(kAppendThreads), smem, cx.stream, cx.pdl, a);
-  return launch_k(append_kernel<D, 4>, dim3((unsigned)((units + 4 * kGroups - 1) / (4 * kGroups))),
-                  dim3(kAppendThreads), smem, cx.stream, cx.pdl, a);
+  const int heads = a.hq + 2 * a.p.hkv;
+  // few tokens: a head for each thread group, spread over the SMs; many: four,
+  // whose loads are in flight together
+  if ((long long)a.p.tokens * heads <= 2LL * cx.sms * kGroups)
+    return launch_k(append_kernel<D, 1, INTERLEAVED>,
+                    dim3((unsigned)a.p.tokens, (unsigned)((heads + kGroups - 1) / kGroups)),
+                    dim3(kAppendThreads), 0, cx.stream, cx.pdl, a);
+  return launch_k(append_kernel<D, 4, INTERLEAVED>,
+                  dim3((unsigned)a.p.tokens, (unsigned)((heads + 4 * kGroups - 1) / (4 * kGroups))),
+                  dim3(kAppendThreads), 0, cx.stream, cx.pdl, a);
 }
 
 cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c) {
@@ -197,9 +181,10 @@ cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c) {
   a.hq = c.hq;
   a.rope_len = c.rope_len;
   a.rot = c.rot;
-  a.interleaved = c.interleaved;
   a.eps = c.eps;
-  return v.dim == 64 ? launch_append_d<64>(cx, a) : launch_append_d<128>(cx, a);
+  if (c.interleaved)
+    return v.dim == 64 ? launch_append_d<64, true>(cx, a) : launch_append_d<128, true>(cx, a);
+  return v.dim == 64 ? launch_append_d<64, false>(cx, a) : launch_append_d<128, false>(cx, a);
 }
 
 // ------------------------------------------------------------------ page copies

@@ -182,6 +182,7 @@ struct AttnCall {
   float* lse;
   long long ldq, ldo;
   int tokens, hq, window;
+  int max_q;       // most new tokens of a sequence as far as known, 0 if not
   float scale;
 };
 
