@@ -27,8 +27,7 @@
 // memory, and the rows that do see a non-finite value get it added at the end.
 //
 // The work is split into equal ranges of (row tile pair, key tile) units, see
-// paged.cuh. A pair that spans several CTAs leaves its unnormalised O, m and
-// sum in the workspace, and a second small kernel joins them.
+// paged.cuh.
 #include <type_traits>
 
 #include "launch.h"
@@ -53,7 +52,7 @@ struct TcAttnArgs {
   int group, hq, tq;   // tq: tokens of one row tile (s.tq: of the pair)
   float c;
   float* ws;
-  int* split;          // [grid][4] the split pairs, by their first CTA
+  int* ctr;            // [grid * 32] arrivals, zero at rest
   long long ws_len;
   int min_units;
   long long timeout_ns;
@@ -68,7 +67,8 @@ struct TcAttnShape {
   static constexpr int kTile = kTcKeys * D * 2;          // a tile of Q, K or V
   static constexpr int kSlots = 64 * 1024 / kTile;       // of 2 tiles
   static constexpr int kStage = 16 * 1024;               // output rows on their way: 2 KB a warp
-  static constexpr int kPart = 2 * kTcRowsA * (D + 2);   // floats of a split pair's partial
+  // floats of a split pair's partial: for A and B o [D / 4][row][4], m and l [row]
+  static constexpr int kPart = 2 * kTcRowsA * (D + 2);
   static int smem(int batch) {
     return 1024 + 2 * kTile + kSlots * 2 * kTile + kStage + 8 * (3 * kSlots + 16) + 64 +
            SplitTables::bytes(batch) + 16;
@@ -511,25 +511,42 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       // while the last P·V runs: where the rows go and their sums. Four lanes
       // write a row, 64 bytes of it at a time.
       const long long tok0 = paged_first(a.p, w.b) + t0;
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
-      const long long slot = (long long)blockIdx.x * 2 + (w.tile_unit() >= u0 ? 1 : 0);
-      float* part = a.ws + slot * Sh::kPart + x * kTcRowsA * (D + 2) + r;
+      auto inverse = [](float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); };  // NaN stays NaN
       uint16_t* dst[4];
-      if (w.whole) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = (warp & 3) * 32 + e * 8 + (lane >> 2), tt = row / a.group;
-          dst[e] = tt >= nt ? nullptr
-                            : a.out + (tok0 + tt) * a.ldo +
-                                  (long long)(w.h * a.group + row - tt * a.group) * D + (lane & 3) * 8;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int row = (warp & 3) * 32 + e * 8 + (lane >> 2), tt = row / a.group;
+        dst[e] = tt >= nt ? nullptr
+                          : a.out + (tok0 + tt) * a.ldo +
+                                (long long)(w.h * a.group + row - tt * a.group) * D + (lane & 3) * 8;
+      }
+      auto put_lse = [&](float top, float sum) {
         if (live && a.lse)
           a.lse[(tok0 + t) * a.hq + w.h * a.group + g] =
-              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      } else {
-        __stcg(part + D * kTcRowsA, m);
-        __stcg(part + (D + 1) * kTcRowsA, l);
-      }
+              sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      };
+      // 32 columns of this warp's rows, through shared memory so that four lanes
+      // write 64 bytes of a row
+      auto put_rows = [&](const uint32_t* o, int q, float scale) {
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t* v = o + e * 8;
+          auto at = [&](int n) { return __uint_as_float(v[n]) * scale; };
+          *reinterpret_cast<uint4*>(mine + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) =
+              make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
+                         pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int rr = e * 8 + (lane >> 2);
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              mine + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
+          if (dst[e]) *reinterpret_cast<uint4*>(dst[e] + q) = v;
+        }
+      };
+      if (w.whole) put_lse(m, l);
       ok = wait(&o_full[x], on++);
       if (!ok) break;
       tc_fence_after();
@@ -556,6 +573,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         tmem_st_wait();
       }
       if (w.whole) {
+        const float inv = inverse(l);
 #pragma unroll 1
         for (int q = 0; q < D; q += 64) {
           uint32_t o[64];
@@ -563,60 +581,117 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
           tmem_ld32(to + q + 32, o + 32);
           tmem_ld_wait();
           tmem_settle<64>(o);
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t* v = o + hh * 32 + e * 8;
-              auto at = [&](int n) { return __uint_as_float(v[n]) * inv; };
-              *reinterpret_cast<uint4*>(mine + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) =
-                  make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
-                             pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
-            }
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int rr = e * 8 + (lane >> 2);
-              const uint4 v = *reinterpret_cast<const uint4*>(
-                  mine + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
-              if (dst[e]) *reinterpret_cast<uint4*>(dst[e] + q + hh * 32) = v;
-            }
-          }
+          put_rows(o, q, inv);
+          put_rows(o + 32, q + 32, inv);
         }
-      } else {
+        // O is read: P of the next segment may be followed by its first P·V
+        tc_fence_before();
+        continue;
+      }
+      // The pair is shared with other CTAs: the first of them ends its range with
+      // it (slot 1), the others begin with it (slot 0). This warp leaves its rows'
+      // O, m and sum; the last of the CTAs' warps with these rows joins them, in
+      // CTA order. Above 8 CTAs in two steps, first within groups of about the
+      // square root of their number, as the join of each reads 64 KB a row tile.
+      const long long cf = cta_of(w.tile_unit(), W, G);
+      const int nc = (int)(cta_of(w.tile_unit() + w.tr.n - 1, W, G) - cf + 1);
+      auto part_of = [&](int k) -> float* {
+        return a.ws + ((cf + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kPart + x * (Sh::kPart / 2);
+      };
+      const int self = (int)(blockIdx.x - cf);
+      {
+        float* part = part_of(self);
 #pragma unroll 1
         for (int q = 0; q < D; q += 32) {
           uint32_t o[32];
           tmem_ld32(to + q, o);
           tmem_ld_wait();
           tmem_settle<32>(o);
-          float* col = DG_AT(a.p.status, part, q * kTcRowsA, Sh::kPart - 31 * kTcRowsA);
+          float4* col = reinterpret_cast<float4*>(
+              DG_AT(a.p.status, part, q * kTcRowsA + r * 4, Sh::kPart / 2 - 28 * kTcRowsA));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) __stcg(col + e * kTcRowsA, __uint_as_float(o[e]));
+          for (int e = 0; e < 8; ++e)
+            __stcg(col + e * kTcRowsA,
+                   make_float4(__uint_as_float(o[e * 4]), __uint_as_float(o[e * 4 + 1]),
+                               __uint_as_float(o[e * 4 + 2]), __uint_as_float(o[e * 4 + 3])));
         }
+        __stcg(reinterpret_cast<float2*>(part + D * kTcRowsA) + r, make_float2(m, l));
       }
-      // O is read: P of the next segment may be followed by its first P·V
       tc_fence_before();
-    }
-  }
-  // what the second kernel joins: the pair that begins in this CTA's range and
-  // goes on past it
-  if (threadIdx.x == 0) {
-    SplitWalk f(a.s, tab, u0, u1);
-    int n = 0, q0 = 0, rows = 0, h = 0;
-    while (f.more()) {
-      if (!f.whole && f.tile_unit() >= u0) {
-        const int qn = tab.qn[f.b], t0 = f.i * a.s.tq;
-        n = (int)(cta_of(f.tile_unit() + f.tr.n - 1, W, G) - blockIdx.x + 1);
-        q0 = paged_first(a.p, f.b) + t0;
-        rows = (qn - t0 < a.s.tq ? qn - t0 : a.s.tq);
-        h = f.h;
+      // the counter of a group is its first CTA's, by slot, warp and step
+      auto last_of = [&](int first, int step, int count) -> bool {
+        __syncwarp();
+        int old = 0;
+        if (lane == 0) {
+          int* ctr = a.ctr + (((cf + first) * 2 + (first == 0 ? 1 : 0)) * 8 + warp) * 2 + step;
+          old = atomic_add_acq_rel_gpu(ctr, 1);
+          if (old == count - 1) *ctr = 0;
+        }
+        return __shfl_sync(~0u, old, 0) == count - 1;
+      };
+      int size = nc;
+      if (nc > 8)
+        for (size = 3; size * size < nc;) ++size;
+      const int groups = (nc + size - 1) / size;
+      int first = self / size * size, stride = 1;
+      int count = nc - first < size ? nc - first : size;
+      bool joined = groups == 1;
+#pragma unroll 1
+      for (int step = 0; last_of(joined && step ? 0 : first, step, count); ++step) {
+        float M = -INFINITY, L = 0.f;
+        auto ml = [&](int k) {
+          return __ldcg(reinterpret_cast<const float2*>(part_of(first + k * stride) + D * kTcRowsA) + r);
+        };
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) M = fmaxf(M, ml(k).x);
+        // a state that has seen nothing (m = -inf) counts for nothing
+        auto factor = [&](float mk) { return M == -INFINITY ? 1.f : exp2_approx(mk - M); };
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+          const float2 s = ml(k);
+          L += factor(s.x) * s.y;
+        }
+        const float inv = inverse(L);
+#pragma unroll 1
+        for (int q = 0; q < D; q += 32) {
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 2
+          for (int k = 0; k < count; ++k) {
+            const float4* col =
+                reinterpret_cast<const float4*>(part_of(first + k * stride) + q * kTcRowsA + r * 4);
+            const float f = factor(ml(k).x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = __ldcg(col + e * kTcRowsA);
+              o[e * 4] += f * v.x;
+              o[e * 4 + 1] += f * v.y;
+              o[e * 4 + 2] += f * v.z;
+              o[e * 4 + 3] += f * v.w;
+            }
+          }
+          if (joined) {
+            put_rows(reinterpret_cast<const uint32_t*>(o), q, inv);
+          } else {
+            float4* col = reinterpret_cast<float4*>(part_of(first) + q * kTcRowsA + r * 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              __stcg(col + e * kTcRowsA, make_float4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]));
+          }
+        }
+        if (joined) {
+          put_lse(M, L);
+          break;
+        }
+        __stcg(reinterpret_cast<float2*>(part_of(first) + D * kTcRowsA) + r, make_float2(M, L));
+        // the groups' states, which the last group joins
+        joined = true;
+        first = 0;
+        stride = size;
+        count = groups;
       }
-      f.next();
     }
-    int4* dst = reinterpret_cast<int4*>(a.split + blockIdx.x * 4);
-    *dst = make_int4(s_flag[0] ? 0 : n, q0, rows, h);
   }
   tc_fence_before();
   __syncthreads();
@@ -626,64 +701,22 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   }
 }
 
-// Joins the partial results of the pairs that span several CTAs: block (c, y)
-// takes 4 columns at a time of the pair that begins in CTA c's range, a thread
-// for each of its rows; the CTAs' parts are summed in their order.
-template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(const TcAttnArgs a) {
-  using Sh = TcAttnShape<D>;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int c = blockIdx.x;
-  const int4 s = __ldcg(reinterpret_cast<const int4*>(a.split + c * 4));
-  const int n = s.x, x = threadIdx.x >> 7, r = threadIdx.x & 127;
-  const int t = r / a.group, g = r - t * a.group, tt = x * a.tq + t;
-  if (n == 0 || t >= a.tq || tt >= s.z) return;
-  auto part = [&](int k) -> const float* {
-    return a.ws + ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kPart + x * kTcRowsA * (D + 2) + r;
-  };
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(part(k) + D * kTcRowsA));
-  const long long tok = s.y + tt;
-  const int head = s.w * a.group + g;
-  for (int d = blockIdx.y * 4; d < D; d += gridDim.y * 4) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float* p = part(k);
-      const float m = __ldcg(p + D * kTcRowsA), l = __ldcg(p + (D + 1) * kTcRowsA);
-      const float f = M == -INFINITY ? 1.f : exp2_approx(m - M);
-      L += f * l;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += f * __ldcg(p + (d + e) * kTcRowsA);
-    }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (long long)head * D + d) =
-        make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
-    if (a.lse && d == 0)
-      a.lse[tok * a.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-  }
-}
-
 // ------------------------------------------------------------------ launch
 template <int D>
 static cudaError_t launch_tc_d(const Ctx& cx, const CUtensorMap& kv, const CUtensorMap& q,
-                               const TcAttnArgs& a, int join_y) {
+                               const TcAttnArgs& a) {
   static DevOnce once;
   cudaError_t e = setup_smem(once, attn_tc_kernel<D>, kMaxDynSmem);
   if (e != cudaSuccess) return e;
-  e = launch_k(attn_tc_kernel<D>, dim3(cx.sms), dim3(kTcAttnThreads), TcAttnShape<D>::smem(a.p.batch),
-               cx.stream, cx.pdl, kv, q, a);
-  if (e != cudaSuccess) return e;
-  return launch_k(attn_join_kernel<D>, dim3(cx.sms, join_y), dim3(256), 0, cx.stream, cx.pdl, a);
+  return launch_k(attn_tc_kernel<D>, dim3(cx.sms), dim3(kTcAttnThreads),
+                  TcAttnShape<D>::smem(a.p.batch), cx.stream, cx.pdl, kv, q, a);
 }
 
 size_t attn_tc_ws(int dim, int sms) {
-  return (size_t)sms * (2 * (size_t)(2 * kTcRowsA * (dim + 2)) * sizeof(float) + 16);
+  return (size_t)sms * 2 * (2 * kTcRowsA * (dim + 2)) * sizeof(float);
 }
 
-cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, void* ws) {
+cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, float* ws, int* ctr) {
   CUtensorMap kv, q;
   TcAttnArgs a = {};
   a.group = c.hq / v.hkv;
@@ -703,13 +736,12 @@ cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, vo
   // a scale of 0 (all weights equal): one that no score outgrows, so that masked
   // scores stay infinite
   a.c = c.scale == 0.f ? 1e-30f : c.scale * 1.4426950408889634f;
-  a.split = static_cast<int*>(ws);
-  a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + (size_t)cx.sms * 16);
+  a.ws = ws;
+  a.ctr = ctr;
   a.s.start = 3;
   a.min_units = 4;
   a.timeout_ns = cx.timeout_ns;
-  const int join_y = v.dim / (4 * 2);  // 4 columns at a time, twice
-  return v.dim == 64 ? launch_tc_d<64>(cx, kv, q, a, join_y) : launch_tc_d<128>(cx, kv, q, a, join_y);
+  return v.dim == 64 ? launch_tc_d<64>(cx, kv, q, a) : launch_tc_d<128>(cx, kv, q, a);
 }
 
 }  // namespace dg

@@ -198,10 +198,10 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
 bool make_tmap_heads(CUtensorMap* map, const void* q, int tokens, int heads, int dim, long long ld,
                      int box_heads, int box_tokens);
 
-// Attention for longer chunks on tcgen05; two kernels; ws of
-// attn_tc_ws bytes.
+// Attention for longer chunks on tcgen05; ws of attn_tc_ws bytes, ctr of 32 zero
+// ints per SM.
 size_t attn_tc_ws(int dim, int sms);
-cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, void* ws);
+cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, float* ws, int* ctr);
 
 struct AppendCall {
   const void* qkv;
