@@ -70,7 +70,9 @@ static int attention(const dec_kv_view* kv, const AttnCall& c, void* stream) {
   if (tc) {
     if ((rc = kv_context(stream, attn_tc_ws(v.dim, sms), 32 * sms, &cx, &ws, &ctr))) return rc;
     t_last_attention = DEC_REGIME_TC;
-    return result(launch_attn_tc(cx, v, c, static_cast<float*>(ws), ctr), 1);
+    int kernels = 0;
+    const cudaError_t e = launch_attn_tc(cx, v, c, static_cast<float*>(ws), ctr, &kernels);
+    return result(e, kernels);
   }
   const int rt = rows <= 16 && group <= 16 ? 1 : 2;
   if ((rc = kv_context(stream, attn_mma_ws(v.dim, rt, sms), sms, &cx, &ws, &ctr))) return rc;

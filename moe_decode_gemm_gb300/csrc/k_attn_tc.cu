@@ -41,6 +41,7 @@ constexpr int kTcKeys = 128;         // positions of a key tile
 constexpr int kTcKeysShift = 7;
 constexpr int kTcRowsA = 128;        // rows of a row tile
 constexpr int kTcAttnThreads = 384;
+constexpr int kTcFew = 4;             // CTAs that may share a pair which one of them joins
 constexpr float kTcLazy = 8.f;       // growth of the maximum (log2) that is left in P
 
 struct TcAttnArgs {
@@ -53,6 +54,7 @@ struct TcAttnArgs {
   float c;
   float* ws;
   int* ctr;            // [grid * 32] arrivals, zero at rest
+  int4* deep;          // [grid] pairs that many CTAs share, by their first CTA; null: none is left
   long long ws_len;
   int min_units;
   long long timeout_ns;
@@ -481,7 +483,9 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
 #pragma unroll 1
         for (;;) {
           row_pass(ts, a.c, m == -INFINITY ? 0.f : m, pk, top, sum);
-          if (!__any_sync(~0u, top > m + kTcLazy)) break;
+          // (rows of the tile that hold no token hold whatever was there: they have
+          // no say, so that results do not depend on it)
+          if (!__any_sync(~0u, live && top > m + kTcLazy)) break;
           // m was -inf before the first visible position: O and l are 0 then
           const float mn = fmaxf(m, top);
           const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
@@ -592,7 +596,10 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       // it (slot 1), the others begin with it (slot 0). This warp leaves its rows'
       // O, m and sum; the last of the CTAs' warps with these rows joins them, in
       // CTA order. Above 8 CTAs in two steps, first within groups of about the
-      // square root of their number, as the join of each reads 64 KB a row tile.
+      // square root of their number, as the join of each reads 64 KB a row tile;
+      // calls of few pairs leave those that more than 4 CTAs share to a second
+      // kernel that spreads them over the SMs (60 tokens over 9000 positions 39
+      // -> 33 us; for calls of many pairs that kernel costs more than it saves).
       const long long cf = cta_of(w.tile_unit(), W, G);
       const int nc = (int)(cta_of(w.tile_unit() + w.tr.n - 1, W, G) - cf + 1);
       auto part_of = [&](int k) -> float* {
@@ -618,6 +625,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         __stcg(reinterpret_cast<float2*>(part + D * kTcRowsA) + r, make_float2(m, l));
       }
       tc_fence_before();
+      if (a.deep && nc > kTcFew) continue;
       // the counter of a group is its first CTA's, by slot, warp and step
       auto last_of = [&](int first, int step, int count) -> bool {
         __syncwarp();
@@ -627,6 +635,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
           old = atomic_add_acq_rel_gpu(ctr, 1);
           if (old == count - 1) *ctr = 0;
         }
+        __syncwarp();
         return __shfl_sync(~0u, old, 0) == count - 1;
       };
       int size = nc;
@@ -693,11 +702,70 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       }
     }
   }
+  if (a.deep && threadIdx.x == 0) {
+    // the pair that begins in this CTA's range and goes on past it, for the
+    // second kernel: CTAs, first token, tokens, head
+    SplitWalk f(a.s, tab, u0, u1);
+    int4 d = make_int4(0, 0, 0, 0);
+    for (; f.more(); f.next())
+      if (!f.whole && f.tile_unit() >= u0) {
+        const int n = (int)(cta_of(f.tile_unit() + f.tr.n - 1, W, G) - blockIdx.x + 1);
+        const int t0 = f.i * a.s.tq, left = tab.qn[f.b] - t0;
+        if (n > kTcFew && !s_flag[0])
+          d = make_int4(n, paged_first(a.p, f.b) + t0, left < a.s.tq ? left : a.s.tq, f.h);
+      }
+    a.deep[blockIdx.x] = d;
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(taddr, 512);
+  }
+}
+
+// Joins the pairs that more than kTcFew CTAs share: block (c, y) takes 4 columns
+// at a time of the pair that begins in CTA c's range, a thread for each row; the
+// CTAs' parts are summed in their order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const TcAttnArgs a) {
+  using Sh = TcAttnShape<D>;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x;
+  const int4 s = __ldcg(a.deep + c);
+  const int n = s.x, x = threadIdx.x >> 7, r = threadIdx.x & 127;
+  const int t = r / a.group, tt = x * a.tq + t;
+  if (n == 0 || t >= a.tq || tt >= s.z) return;
+  auto part = [&](int k) -> const float* {
+    return a.ws + ((long long)(c + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kPart + x * (Sh::kPart / 2);
+  };
+  auto ml = [&](int k) {
+    return __ldcg(reinterpret_cast<const float2*>(part(k) + D * kTcRowsA) + r);
+  };
+  float M = -INFINITY;
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) M = fmaxf(M, ml(k).x);
+  const long long tok = s.y + tt;
+  const int head = s.w * a.group + r - t * a.group;
+  for (int d = blockIdx.y * 4; d < D; d += gridDim.y * 4) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, L = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float2 s2 = ml(k);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(part(k) + d * kTcRowsA + r * 4));
+      const float f = M == -INFINITY ? 1.f : exp2_approx(s2.x - M);
+      L += f * s2.y;
+      v[0] += f * o.x;
+      v[1] += f * o.y;
+      v[2] += f * o.z;
+      v[3] += f * o.w;
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (long long)head * D + d) =
+        make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+    if (a.lse && d == 0)
+      a.lse[tok * a.hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
   }
 }
 
@@ -708,15 +776,18 @@ static cudaError_t launch_tc_d(const Ctx& cx, const CUtensorMap& kv, const CUten
   static DevOnce once;
   cudaError_t e = setup_smem(once, attn_tc_kernel<D>, kMaxDynSmem);
   if (e != cudaSuccess) return e;
-  return launch_k(attn_tc_kernel<D>, dim3(cx.sms), dim3(kTcAttnThreads),
-                  TcAttnShape<D>::smem(a.p.batch), cx.stream, cx.pdl, kv, q, a);
+  e = launch_k(attn_tc_kernel<D>, dim3(cx.sms), dim3(kTcAttnThreads),
+               TcAttnShape<D>::smem(a.p.batch), cx.stream, cx.pdl, kv, q, a);
+  if (e != cudaSuccess || !a.deep) return e;
+  return launch_k(attn_join_kernel<D>, dim3(cx.sms, D / 8), dim3(256), 0, cx.stream, cx.pdl, a);
 }
 
 size_t attn_tc_ws(int dim, int sms) {
-  return (size_t)sms * 2 * (2 * kTcRowsA * (dim + 2)) * sizeof(float);
+  return (size_t)sms * (2 * (2 * kTcRowsA * (size_t)(dim + 2)) * sizeof(float) + sizeof(int4));
 }
 
-cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, float* ws, int* ctr) {
+cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, float* ws, int* ctr,
+                           int* kernels) {
   CUtensorMap kv, q;
   TcAttnArgs a = {};
   a.group = c.hq / v.hkv;
@@ -739,8 +810,12 @@ cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, fl
   a.ws = ws;
   a.ctr = ctr;
   a.s.start = 3;
-  a.min_units = 4;
+  a.min_units = 6;
   a.timeout_ns = cx.timeout_ns;
+  const long long pairs = ((long long)c.tokens / a.s.tq + v.batch) * v.hkv;
+  if (pairs * 4 <= cx.sms)
+    a.deep = reinterpret_cast<int4*>(ws + (size_t)cx.sms * 2 * (2 * kTcRowsA * (v.dim + 2)));
+  *kernels = a.deep ? 2 : 1;
   return v.dim == 64 ? launch_tc_d<64>(cx, kv, q, a) : launch_tc_d<128>(cx, kv, q, a);
 }
 

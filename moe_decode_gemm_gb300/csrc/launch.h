@@ -199,9 +199,10 @@ bool make_tmap_heads(CUtensorMap* map, const void* q, int tokens, int heads, int
                      int box_heads, int box_tokens);
 
 // Attention for longer chunks on tcgen05; ws of attn_tc_ws bytes, ctr of 32 zero
-// ints per SM.
+// ints per SM; *kernels: how many it launched.
 size_t attn_tc_ws(int dim, int sms);
-cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, float* ws, int* ctr);
+cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, float* ws, int* ctr,
+                           int* kernels);
 
 struct AppendCall {
   const void* qkv;

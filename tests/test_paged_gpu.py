@@ -170,6 +170,30 @@ def test_two_streams_and_graph_follow_the_lengths():
     pg.check_attention(bt, out, lse)
 
 
+@pytest.mark.parametrize("dim,hq,hkv,new,long", [
+    (128, 14, 1, 40, 20000), (64, 8, 2, 60, 9000), (128, 4, 1, 1, 30000), (64, 8, 4, 5, 12000)])
+def test_one_long_sequence_among_many_short_ones(dim, hq, hkv, new, long):
+    # shared by many CTAs while the others' row tiles fit into one
+    n = 44
+    bt = pg.Batch([new] * n, [long if b == 17 else new + 3 * b for b in range(n)], hq, hkv, dim, 64,
+                  seed=13)
+    kv = bt.device(dg, max_q=new)
+    out, lse = run(bt, kv=kv)
+    pg.check_attention(bt, out, lse)
+    o2, l2 = run(bt, kv=kv)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dim,hq,hkv,new,total", [(128, 14, 1, 20, 15000), (64, 16, 2, 70, 30000)])
+def test_few_row_tiles_shared_by_all_sms(dim, hq, hkv, new, total):
+    bt = pg.Batch([new], [total], hq, hkv, dim, 128, seed=14)
+    kv = bt.device(dg, max_q=new)
+    out, lse = run(bt, kv=kv)
+    pg.check_attention(bt, out, lse)
+    o2, l2 = run(bt, kv=kv)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
 # ------------------------------------------------------------------ append
 def _append(bt, rot, interleaved, norm, positions=None, seed=0, alias=False):
     g = pg.gen(seed)
