@@ -479,3 +479,81 @@ def test_regimes_and_forced_regimes(monkeypatch):
             res[force, max_q] = run(bt, max_q=max_q)
             pg.check_attention(bt, *res[force, max_q], what="%s %d" % (force, max_q))
             assert dg.last_attention() == (force or ("mma" if max_q == 1 else "tc"))
+
+
+# ------------------------------------------------------------------ the rest
+def test_index_checks_find_nothing():
+    """The index-checking build of the library over shapes that split and join."""
+    old = dg.use_library(dg.DEBUG_LIB_PATH)
+    try:
+        assert dg.lib().dec_debug_build() == 1
+        for new, total, max_q in (([1], [5000], 1), ([1] * 9, list(range(30, 1200, 130)), 1),
+                                  ([70, 3], [2000, 40], 70), ([40] * 20, [40 + 60 * i for i in range(20)], 40)):
+            bt = pg.Batch(new, total, 14, 1, 128, 32, seed=70)
+            pg.check_attention(bt, *run(bt, max_q=max_q))
+        _append(pg.Batch([1, 0, 5, 33, 1], [1, 9, 70, 33, 129], 14, 1, 128, 16, seed=71), 64, True,
+                norm=True)
+    finally:
+        dg.use_library(old)
+
+
+def test_calls_after_shutdown():
+    bt = pg.Batch([1, 70], [300, 200], 14, 1, 128, 64, seed=72)
+    for _ in range(2):
+        for max_q in (1, 70):
+            pg.check_attention(bt, *run(bt, max_q=max_q))
+        torch.cuda.synchronize()
+        dg.shutdown()
+
+
+def test_binding_refuses():
+    bt = pg.Batch([1, 2], [30, 40], 4, 2, 64, 16, seed=73)
+    kv = bt.device(dg)
+    q, f32 = bt.q.cuda(), dict(dtype=torch.float32, device="cuda")
+    rope = torch.zeros(64, 64, device="cuda")
+    qkv = torch.zeros(3, 8 * 64, dtype=BF, device="cuda")
+    w = torch.zeros(64, dtype=BF, device="cuda")
+    i3 = _i32([0, 1, 2])
+    for exc, msg, call in (
+            (TypeError, "q: expected torch.bfloat16", lambda: dg.kv_attention(q.float(), kv)),
+            (TypeError, "q: expected a torch tensor", lambda: dg.kv_attention(None, kv)),
+            (ValueError, "q: expected a CUDA tensor", lambda: dg.kv_attention(bt.q, kv)),
+            (ValueError, "q: expected 2 dimensions", lambda: dg.kv_attention(q[0], kv)),
+            (ValueError, "unit column stride", lambda: dg.kv_attention(q.t().contiguous().t(), kv)),
+            (ValueError, "q: expected [T, Hq*64]", lambda: dg.kv_attention(q[:, :192], kv)),
+            (ValueError, "out: expected shape", lambda: dg.kv_attention(q, kv, out=q[:2])),
+            (ValueError, "lse: expected", lambda: dg.kv_attention(q, kv, lse=torch.zeros(3, 5, **f32))),
+            (TypeError, "lse: expected torch.float32", lambda: dg.kv_attention(q, kv, lse=q)),
+            (ValueError, "qkv: expected [T, (Hq + 4)*64]", lambda: dg.kv_append(qkv[:, :256], kv, rope)),
+            (TypeError, "rope: expected torch.float32", lambda: dg.kv_append(qkv, kv, rope.bfloat16())),
+            (ValueError, "rope: must be contiguous", lambda: dg.kv_append(qkv, kv, rope[:, :32])),
+            (ValueError, "give both or neither", lambda: dg.kv_append(qkv, kv, rope, w)),
+            (ValueError, "wk: expected shape", lambda: dg.kv_append(qkv, kv, rope, w, w[:32])),
+            (ValueError, "positions: expected shape", lambda: dg.kv_append(qkv, kv, rope, positions=i3[:2])),
+            (ValueError, "q: expected shape", lambda: dg.kv_append(qkv, kv, rope, q=q[:2])),
+            (dg.DecError, "kv_append failed", lambda: dg.kv_append(qkv, kv, rope[:, :8].contiguous())),
+            (ValueError, "kv_len: expected shape",
+             lambda: dg.PagedKV(kv.cache, kv.table, kv.cu_q, kv.kv_len[:1])),
+            (ValueError, "table: 2 rows for a batch of 4",
+             lambda: dg.PagedKV(kv.cache, kv.table, _i32([0] * 5), kv.kv_len)),
+            (TypeError, "table: expected torch.int32",
+             lambda: dg.PagedKV(kv.cache, kv.table.long(), kv.cu_q, kv.kv_len))):
+        with pytest.raises(exc) as e:
+            call()
+        assert msg in str(e.value), (msg, str(e.value))
+    pool, _ = _pool(74, seqs=3, width=4, page=16, pages=20)
+    for exc, msg, call in (
+            (TypeError, "seqs: expected torch.int32", lambda: dg.kv_free(pool, i3.long())),
+            (ValueError, "lens: expected shape", lambda: dg.kv_resize(pool, i3, i3[:2])),
+            (ValueError, "dst: expected shape", lambda: dg.kv_fork(pool, i3, i3[:1])),
+            (ValueError, "src: expected a CUDA tensor", lambda: dg.kv_copy(pool, i3.cpu(), i3)),
+            (ValueError, "seqs: must be contiguous", lambda: dg.kv_free(pool, _i32([0, 1, 2, 0])[::2])),
+            (ValueError, "refs: expected shape",
+             lambda: dg.KVPool(pool.data, pool.refs[:5], pool.table, pool.lens))):
+        with pytest.raises(exc) as e:
+            call()
+        assert msg in str(e.value), (msg, str(e.value))
+    # nothing to do is no error
+    assert dg.kv_attention(q[:0], kv).shape == (0, 256)
+    dg.kv_free(pool, i3[:0])
+    assert dg.sync_check() == dg.DEC_OK
