@@ -601,6 +601,7 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
   a.ws_len = cx.ws_len;
   a.ctr_len = (int)cx.ctr_len;
   a.s.start = 4;
+  a.s.snap = 20;
   a.min_units = 12;
   a.timeout_ns = cx.timeout_ns;
   const bool d64 = v.dim == 64;
@@ -612,6 +613,7 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
       (c.max_q > 0 && c.max_q <= a.s.tq ? v.batch : (long long)c.tokens / a.s.tq + v.batch) * v.hkv;
   if (tiles <= kClusterTiles) {
     a.s.start = 40;
+    a.s.snap = 100;
     a.min_units = 96;
   }
   if (rt == 1 && tiles <= kClusterTiles)

@@ -284,22 +284,30 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         return pg < 0 || pg >= a.p.pages ? a.p.pages : pg;
       };
       auto place = [&](int j) { return (j * kTcKeys + piece * rows) & page_mask; };
+      auto load_q = [&] {
+        if (lane == 0) {
+          const uint32_t bytes = a.group * a.tq * 128;
+          const int tok = paged_first(a.p, w.b) + w.i * a.s.tq;
+          mbar_arrive_expect_tx(q_full, bytes * (D / 64) * (two ? 2 : 1));
+          for (int x = 0; x < (two ? 2 : 1); ++x)
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(sq + x * Sh::kTile + h * Sh::kHalf, &qmap, h * 64, w.h * a.group,
+                          tok + x * a.tq, q_full, pol);
+        }
+        __syncwarp();
+      };
       const int pg0 = page_at(w.j);
       int pg_next = w.n > 1 ? page_at(w.j + 1) : -1;
-      // the first slot also brings the values that the segment before ends with
-      ok = put(pg0, place(w.j), w.h) && (seg == 0 || wait(q_empty, seg - 1));
-      if (!ok) break;
-      if (lane == 0) {
-        const uint32_t bytes = a.group * a.tq * 128;
-        const int tok = paged_first(a.p, w.b) + w.i * a.s.tq;
-        mbar_arrive_expect_tx(q_full, bytes * (D / 64) * (two ? 2 : 1));
-        for (int x = 0; x < (two ? 2 : 1); ++x)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sq + x * Sh::kTile + h * Sh::kHalf, &qmap, h * 64, w.h * a.group,
-                        tok + x * a.tq, q_full, pol);
+      // the first slot also brings the values that the segment before ends with:
+      // they do not wait for that segment's last Q·Kᵀ, as its Q's place does
+      if (seg == 0) load_q();
+      ok = put(pg0, place(w.j), w.h);
+      if (seg > 0) {
+        ok = ok && wait(q_empty, seg - 1);
+        if (!ok) break;
+        load_q();
       }
       ++seg;
-      __syncwarp();
       for (int k = 1; k < w.n && ok; ++k) {
         const int pg = pg_next;
         if (k + 1 < w.n) pg_next = page_at(w.j + k + 1);
@@ -420,24 +428,44 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         uint8_t* v = ring + st * 2 * Sh::kTile;
         int k0, k1;
         edge_steps(er, key0, k0, k1);
+        auto at = [&](int x) {  // 8 values: x / (D / 8) positions into the tile
+          const int key = x / (D / 8), ch = x % (D / 8);
+          return reinterpret_cast<uint4*>(v + (ch >> 3) * Sh::kHalf + key * 128 +
+                                          (((ch & 7) ^ (key & 7)) << 4));
+        };
+        // positions [from, to) of the tile: 0 where no row sees them; where not
+        // all do, first one look over all of them (0 * x is not 0 if x is not
+        // finite)
         bool found = false;
-        auto clean = [&](int from, int to) {  // positions of the tile
+        auto none = [&](int from, int to) {
+#pragma unroll 1
+          for (int x = from * (D / 8) + lane; x < to * (D / 8); x += 32) *at(x) = make_uint4(0, 0, 0, 0);
+        };
+        auto some = [&](int from, int to) {
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+          __nv_bfloat162 sum = zero;
 #pragma unroll 4
           for (int x = from * (D / 8) + lane; x < to * (D / 8); x += 32) {
-            const int key = x / (D / 8), ch = x % (D / 8);
-            found |= clean_edge_value(
-                reinterpret_cast<uint4*>(v + (ch >> 3) * Sh::kHalf + key * 128 +
-                                         (((ch & 7) ^ (key & 7)) << 4)),
-                er, key0 + key);
+            const uint4 e = *at(x);
+            const uint32_t w4[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w4[q]), zero, sum);
           }
+          if (__all_sync(~0u, __low2float(sum) == 0.f && __high2float(sum) == 0.f)) return;
+#pragma unroll 1
+          for (int x = from * (D / 8) + lane; x < to * (D / 8); x += 32)
+            found |= clean_edge_value(at(x), er, key0 + x / (D / 8));
         };
         auto within = [&](int pos) {
           const int n = pos - key0;
           return n < k0 * 16 ? k0 * 16 : (n > k1 * 16 ? k1 * 16 : n);
         };
-        const int lo_end = within(er.all_lo);
-        clean(k0 * 16, lo_end);
-        clean(within(er.all_hi > er.all_lo ? er.all_hi : er.all_lo), k1 * 16);
+        const int seen0 = within(er.klo), seen1 = within(er.khi);
+        none(k0 * 16, seen0);
+        some(seen0, within(er.all_lo < er.khi ? er.all_lo : er.khi));
+        some(within(er.all_hi > er.all_lo ? er.all_hi : er.all_lo), seen1);
+        none(seen1 > seen0 ? seen1 : seen0, k1 * 16);
         if (__any_sync(~0u, found) && lane == 0) s_poison[seg & 3] = seg + 1;
         fence_async_shared();
         __syncwarp();
@@ -810,6 +838,7 @@ cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, fl
   a.ws = ws;
   a.ctr = ctr;
   a.s.start = 3;
+  a.s.snap = 12;
   a.min_units = 6;
   a.timeout_ns = cx.timeout_ns;
   const long long pairs = ((long long)c.tokens / a.s.tq + v.batch) * v.hkv;

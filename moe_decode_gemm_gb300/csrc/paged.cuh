@@ -13,8 +13,10 @@
 // head, and `start` more at the beginning of each row tile for what it costs
 // whatever its length (queries in, output out). The units of a call, in the
 // order sequence, key head, row tile, key tile, are cut into equal contiguous
-// ranges, one per CTA; the partial softmax states of a row tile that spans
-// several ranges are joined in CTA order.
+// ranges, one per CTA, except that a row tile of at most `snap` units is not
+// cut: the cut goes to its nearer end, as joining costs more than it evens out.
+// The partial softmax states of a row tile that spans several ranges are joined
+// in CTA order.
 #pragma once
 
 #include "dg_common.cuh"
@@ -100,6 +102,7 @@ struct SplitShape {
   int window;    // 0: none
   int hkv;
   int start;     // units of a row tile before its first key tile
+  int snap;      // units up to which a row tile is one CTA's
 };
 
 // Key tiles [j0, j0 + n) of row tile i of a sequence with qn new tokens and kv
@@ -284,28 +287,34 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     if (g < (long long)all_tiles * s.hkv) g = (long long)all_tiles * s.hkv;
     if (g < 1) g = 1;
     if (g > workers) g = workers;
-    const long long from = c < g ? div_small(c * units, g) : 0;
-    const long long to = c < g ? div_small((c + 1) * units, g) : 0;
     if (lane == 0) {
       t.head[0] = units;
       t.head[1] = g;
-      t.head[2] = from;
-      t.head[3] = to;
     }
-    if (from < to) {
-      int b = -1;  // the last sequence with base <= from
+  }
+  __syncthreads();
+  W = t.head[0];
+  G = t.head[1];
+  // The range's two ends, a warp each: the row tile that unit u falls into, and
+  // the cut moved to an end of it if it is short.
+  if (warp < 2) {
+    long long u = c + warp;
+    u = c < G ? (u < G ? div_small(u * W, G) : W) : 0;
+#pragma unroll 1
+    for (int round = 0; round < 2 && c < G && u < W; ++round) {
+      int b = -1;  // the last sequence with base <= u
 #pragma unroll 1
       for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int n = __popc(
-            __ballot_sync(~0u, b0 + lane < p.batch && t.base[b0 + lane < p.batch ? b0 + lane : 0] <= from));
+            __ballot_sync(~0u, b0 + lane < p.batch && t.base[b0 + lane < p.batch ? b0 + lane : 0] <= u));
         b += n;
         if (n < 32) break;
       }
       const long long U = div_small(t.base[b + 1] - t.base[b], s.hkv);
-      const long long r = from - t.base[b];
+      const long long r = u - t.base[b];
       const int h = (int)div_small(r, U);
       long long off = r - h * U;
-      int i = 0;
+      int i = 0, cost = 0;
       const int qn = t.qn[b], kv = t.kv[b];
 #pragma unroll 1
       for (;; i += 32) {
@@ -321,22 +330,34 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
         if (past) {
           const int l = __ffs(past) - 1;
           off -= __shfl_sync(~0u, sum - n, l);
+          cost = __shfl_sync(~0u, n, l);
           i += l;
           break;
         }
         off -= __shfl_sync(~0u, sum, 31);
       }
-      if (lane == 0) {
+      bool found = true;
+      if (off > 0 && cost <= s.snap) {
+        if (2 * off < cost) {
+          u -= off;
+          off = 0;
+        } else {
+          u += cost - off;  // the next row tile's start: look for it
+          found = false;
+        }
+      }
+      if (!found) continue;
+      if (warp == 0 && lane == 0) {
         t.loc[0] = b;
         t.loc[1] = h;
         t.loc[2] = i;
         t.loc[3] = (int)off;
       }
+      break;
     }
+    if (lane == 0) t.head[2 + warp] = u;
   }
   __syncthreads();
-  W = t.head[0];
-  G = t.head[1];
   u0 = t.head[2];
   u1 = t.head[3];
 }
