@@ -602,7 +602,7 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
   a.ctr_len = (int)cx.ctr_len;
   a.s.start = 4;
   a.s.snap = 20;
-  a.min_units = 12;
+  a.min_units = 8;
   a.timeout_ns = cx.timeout_ns;
   const bool d64 = v.dim == 64;
   // Few row tiles: a cluster of 8 CTAs for each part of one, so that the parts

@@ -282,9 +282,10 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     }
     if (lane == 0) t.base[p.batch] = units;
     __syncwarp();
-    // no more workers than give each min_units, but one for each row tile
+    // no more workers than give each min_units, but two for each row tile: of
+    // tiles that are not cut, ranges of less than one leave no worker two
     long long g = div_small(units, min_units);
-    if (g < (long long)all_tiles * s.hkv) g = (long long)all_tiles * s.hkv;
+    if (g < 2LL * all_tiles * s.hkv) g = 2LL * all_tiles * s.hkv;
     if (g < 1) g = 1;
     if (g > workers) g = workers;
     if (lane == 0) {
