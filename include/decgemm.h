@@ -386,7 +386,8 @@ typedef struct dec_kv_view {
  * (a cos - c sin, c cos + a sin), pairs being (i, i + rot/2), or (2i, 2i+1) with
  * interleaved. fp32 throughout, rounded once to bf16. Values are copied. Token
  * t of sequence b goes to position kv_len - (its new tokens) + t. Tokens past
- * cu_q[batch] belong to no sequence and are left alone (a padded batch).
+ * cu_q[batch] belong to no sequence and are left alone (a padded batch). A row
+ * number outside rope is taken as the nearest one (and DEC_EBOUNDS reported).
  */
 int kv_append(const dec_kv_view* kv, const void* qkv, int64_t ldqkv, const void* wq, const void* wk,
               float eps, const float* rope, int rope_len, int rot, int interleaved,
@@ -452,7 +453,9 @@ typedef struct dec_kv_pool {
  * of the last one if that is partly filled, so that both can be appended to.
  * Pages that dst[i] held are given back. All or nothing, as kv_resize.
  *
- * Pages that a call gives back are free from the next call on.
+ * Pages that a call gives back are free from the next call on. kv_resize, kv_fork
+ * and kv_compact use the library's workspace, as kv_attention does: order such
+ * calls on one stream, and make a first one before capturing them in a graph.
  */
 int kv_resize(const dec_kv_pool* pool, const int32_t* seqs, const int32_t* lens, int n, void* stream);
 int kv_free(const dec_kv_pool* pool, const int32_t* seqs, int n, void* stream);

@@ -68,8 +68,11 @@ __global__ void __launch_bounds__(kAppendThreads, U > 1 && INTERLEAVED ? 5 : 4) 
     b += __syncthreads_count(i + tid < a.p.batch && __ldg(a.p.cu_q + i + tid + 1) <= tok);
   if (b >= a.p.batch) return;  // past the last sequence
   const int first = __ldg(a.p.cu_q + b), end = __ldg(a.p.cu_q + b + 1);
+  if (first > tok || end <= tok) {  // before the first sequence, or cu_q does not rise
+    if (b > 0 && a.p.status) atomicOr(a.p.status, kStatusBounds);
+    return;
+  }
   const int row = paged_row(a.p, b);
-  if (first > tok) return;
   const int pos = paged_len(a.p, row) - end + tok;
   int rp = a.positions ? __ldg(a.positions + tok) : (pos < 0 ? 0 : pos);
   int page = -1;

@@ -80,16 +80,7 @@ __device__ __forceinline__ int paged_len(const PagedArgs& p, int row) {
   return n < 0 ? 0 : (int)cap;
 }
 
-// First token and token count of sequence b, within [0, tokens].
-__device__ __forceinline__ void paged_tokens(const PagedArgs& p, int b, int& q0, int& qn) {
-  const int a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
-  q0 = a < 0 ? 0 : (a > p.tokens ? p.tokens : a);
-  const int q1 = e < q0 ? q0 : (e > p.tokens ? p.tokens : e);
-  qn = q1 - q0;
-  if ((a != q0 || e != q1) && p.status) atomicOr(p.status, kStatusBounds);
-}
-
-// First token of sequence b.
+// First token of sequence b, within [0, tokens].
 __device__ __forceinline__ int paged_first(const PagedArgs& p, int b) {
   const int a = __ldg(p.cu_q + b);
   return a < 0 ? 0 : (a > p.tokens ? p.tokens : a);

@@ -16,6 +16,7 @@
     python -m moe_decode_gemm_gb300.profiling case router TOKENS [CALLS]
     python -m moe_decode_gemm_gb300.profiling case shared TOKENS [CALLS]
     python -m moe_decode_gemm_gb300.profiling case prefetch M ON [CALLS]
+    python -m moe_decode_gemm_gb300.profiling case attention BATCH TOKENS LENGTH [CALLS]
         A small case to run under `ncu --set full` (needs a GPU): CALLS
         (default 3) MoE blocks of TOKENS tokens over a bank of EXPERTS routed
         experts (hidden 7168, intermediate 2048, top-8, no shared expert),
@@ -26,7 +27,10 @@
         the shared expert's kernels), or CALLS 7168 x 7168 projections of M
         tokens, each after a write of 256 MB that evicts L2 and -- with ON = 1
         -- an l2_prefetch of the weight's first half-L2 bytes (for the L2 hit
-        rate of the projection under `ncu --cache-control none`). Inputs are
+        rate of the projection under `ncu --cache-control none`), or CALLS
+        appends and attentions of BATCH sequences with TOKENS new tokens each
+        over LENGTH positions in pages of 64 (56 query and 4 key/value heads of
+        128), between two layers' caches in turn. Inputs are
         seeded and synthetic; each expert is 88 MB, so a bank of 32 (2.8 GB)
         is far larger than L2 and its DRAM counters mean what they say.
 
@@ -87,7 +91,11 @@ def kernel_label(name):
         return "projection [tcgen05 %s cluster%s]" % (_EPI.get(m.group(1), m.group(1)), stage)
     for k, lab in (("schedule_gather_kernel", "schedule + gather"),
                    ("combine_kernel", "combine"), ("add_kernel", "residual add"),
-                   ("prefetch_kernel", "l2_prefetch")):
+                   ("prefetch_kernel", "l2_prefetch"), ("append_kernel", "append"),
+                   ("attn_tc_kernel", "attention [tcgen05]"), ("attn_join_kernel", "attention join"),
+                   ("attn_mma_kernel", "attention [mma.sync]"), ("kv_change_kernel", "page state"),
+                   ("kv_copy_kernel", "page copies"), ("kv_rank_kernel", "compact: ranks"),
+                   ("kv_move_kernel", "compact: moves")):
         if k in name:
             return lab
     return name[:60]
@@ -223,6 +231,26 @@ def case(kind, *args):
             dg.dec_linear(x, W, y)
             torch.cuda.synchronize()
         print("prefetch M=%d on=%d calls=%d regime=%s" % (M, on, calls, dg.last_choice()))
+    elif kind == "attention":
+        B, T, N = int(args[0]), int(args[1]), int(args[2])
+        calls = int(args[3]) if len(args) > 3 else 3
+        Hq, Hkv, D, page = 56, 4, 128, 64
+        width = -(-N // page)
+        i32 = torch.int32
+        cache = normal_bf16_cuda((2, B * width, 2, Hkv, page, D), 1.0, "profile", "cache")
+        table = torch.randperm(B * width, device="cuda").to(i32).view(B, width)
+        cu_q = torch.arange(0, (B + 1) * T, T, dtype=i32, device="cuda")
+        lens = torch.full((B,), N, dtype=i32, device="cuda")
+        kvs = [dg.PagedKV(cache[l], table, cu_q, lens, max_q=T) for l in range(2)]
+        qkv = normal_bf16_cuda((B * T, (Hq + 2 * Hkv) * D), 1.0, "profile", "qkv")
+        w = normal_bf16_cuda((2, D), 1.0, "profile", "norms")
+        rope = torch.rand((N, D), device="cuda")
+        for i in range(calls):
+            q = dg.kv_append(qkv, kvs[i % 2], rope, w[0], w[1])
+            dg.kv_attention(q, kvs[i % 2])
+        torch.cuda.synchronize()
+        print("attention batch=%d tokens=%d length=%d regime=%s calls=%d"
+              % (B, T, N, dg.last_attention(), calls))
     else:
         sys.exit(__doc__)
     if dg.sync_check() != 0:

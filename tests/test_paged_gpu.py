@@ -266,6 +266,19 @@ def test_append_out_of_range_is_reported():
     assert dg.sync_check() == dg.DEC_OK
 
 
+def test_token_ranges_that_do_not_rise_are_reported():
+    # some tokens lie past the end of the sequence that the offsets point to
+    for max_q in (1, 40):
+        bt = pg.Batch([9, 2, 2, 15], [80] * 4, 4, 2, 64, 16, seed=26)
+        bt.cu_q = torch.tensor([0, 9, 3, 5, 28], dtype=torch.int32)
+        kv = bt.device(dg, max_q=max_q)
+        dg.kv_append(pg.normal(pg.gen(1), 28, 8 * 64).cuda(), kv, torch.zeros(128, 64, device="cuda"))
+        assert dg.sync_check() == dg.DEC_EBOUNDS
+        dg.kv_attention(bt.q.cuda(), kv)
+        assert dg.sync_check() == dg.DEC_EBOUNDS
+        assert dg.sync_check() == dg.DEC_OK
+
+
 # ------------------------------------------------------------------ pages
 def _pool(seed, **kw):
     data, refs, table, lens = pg.random_pool(seed, **kw)
