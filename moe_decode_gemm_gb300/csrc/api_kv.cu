@@ -68,7 +68,7 @@ static int attention(const dec_kv_view* kv, const AttnCall& c, void* stream) {
   if (force && !std::strcmp(force, "mma") && group <= 32) tc = false;
   if (force && !std::strcmp(force, "tc")) tc = true;
   if (tc) {
-    if ((rc = kv_context(stream, attn_tc_ws(v.dim, sms), 32 * sms, &cx, &ws, &ctr))) return rc;
+    if ((rc = kv_context(stream, attn_tc_ws(v.dim, sms), 32 * sms + 1, &cx, &ws, &ctr))) return rc;
     t_last_attention = DEC_REGIME_TC;
     int kernels = 0;
     const cudaError_t e = launch_attn_tc(cx, v, c, static_cast<float*>(ws), ctr, &kernels);

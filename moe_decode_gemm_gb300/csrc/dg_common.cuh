@@ -314,32 +314,6 @@ __device__ __forceinline__ void named_bar_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// Named barrier over `count` threads that also tells every one of them whether
-// any has p set.
-__device__ __forceinline__ bool named_bar_any(int id, int count, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\t"
-      "setp.ne.u32 a, %3, 0;\n\t"
-      "barrier.cta.red.or.pred b, %1, %2, a;\n\t"
-      "selp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"((uint32_t)p)
-      : "memory");
-  return r != 0;
-}
-
-// Moves registers between the warps of a block: all warps of a warpgroup call
-// with the same count (a multiple of 8).
-template <int N>
-__device__ __forceinline__ void regs_take() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_give() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ------------------------------------------------------------------ mma.sync
 __device__ __forceinline__ void ldmatrix_x4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3,
                                             uint32_t addr) {

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
   long long W, G, u0, u1;
   const long long worker = blockIdx.x / CL;
   const int rank = CL > 1 ? (int)cluster_rank() : 0;
-  split_setup(a.p, a.s, tab, a.min_units, worker, gridDim.x / CL, W, G, u0, u1);
+  split_setup<false>(a.p, a.s, tab, a.min_units, worker, gridDim.x / CL, W, G, u0, u1);
   if (CL > 1) cluster_wait_all();
   SplitWalk w(a.s, tab, u0, u1);
   const int page_mask = a.p.page - 1;

@@ -53,7 +53,7 @@ struct TcAttnArgs {
   int group, hq, tq;   // tq: tokens of one row tile (s.tq: of the pair)
   float c;
   float* ws;
-  int* ctr;            // [grid * 32] arrivals, zero at rest
+  int* ctr;            // [grid * 32 + 1] arrivals, row tile pairs drawn; zero at rest
   int4* deep;          // [grid] pairs that many CTAs share, by their first CTA; null: none is left
   long long ws_len;
   int min_units;
@@ -72,7 +72,7 @@ struct TcAttnShape {
   // floats of a split pair's partial: for A and B o [D / 4][row][4], m and l [row]
   static constexpr int kPart = 2 * kTcRowsA * (D + 2);
   static int smem(int batch) {
-    return 1024 + 2 * kTile + kSlots * 2 * kTile + kStage + 8 * (3 * kSlots + 16) + 64 +
+    return 1024 + 2 * kTile + kSlots * 2 * kTile + kStage + 8 * (3 * kSlots + 24) + 64 + 64 +
            SplitTables::bytes(batch) + 16;
   }
 };
@@ -184,10 +184,14 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   uint64_t* q_full = o_full + 2;
   uint64_t* q_empty = q_full + 1;
   uint64_t* mma_done = q_empty + 1;
-  volatile int* s_flag = reinterpret_cast<volatile int*>(full + 3 * kSlots + 16);  // [0] abort
+  uint64_t* seg_full = mma_done + 1;    // [4] a drawn pair written to s_seg
+  volatile int* s_flag = reinterpret_cast<volatile int*>(full + 3 * kSlots + 24);  // [0] abort
   volatile int* s_poison = s_flag + 4;  // [4] segment number + 1 with a non-finite edge value
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(const_cast<int*>(s_flag) + 8);
-  const SplitTables tab(reinterpret_cast<uint8_t*>(const_cast<int*>(s_flag)) + 64, a.p.batch);
+  int4* s_seg = reinterpret_cast<int4*>(const_cast<int*>(s_flag) + 16);  // [4] drawn pairs
+  // (four segments' worth of both: no warp is more than two segments ahead of
+  // another, as the TMA warp waits with Q for the segment before)
+  const SplitTables tab(s_seg + 4, a.p.batch);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -204,6 +208,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(mma_done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&seg_full[i], 1);
     s_flag[0] = 0;
     for (int i = 0; i < 4; ++i) s_poison[i] = 0;
     fence_mbar_init();
@@ -221,8 +226,14 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   long long W, G, u0, u1;
-  split_setup(a.p, a.s, tab, a.min_units, blockIdx.x, gridDim.x, W, G, u0, u1);
+  split_setup<true>(a.p, a.s, tab, a.min_units, blockIdx.x, gridDim.x, W, G, u0, u1);
   SplitWalk w(a.s, tab, u0, u1);
+  // Where there are pairs enough and none is long, equal ranges lose more to
+  // their ends (a pair cut and joined, or left whole beside a range that is
+  // then shorter) than CTAs that draw whole pairs as they become free, long
+  // ones first.
+  const bool draws = tab.head[4] >= 2 * gridDim.x && tab.head[4] < 1 << 30 &&
+                     tab.head[5] * 5 * gridDim.x <= 3 * W;
 
   auto edges = [&]() -> EdgeRange {
     const int qn = tab.qn[w.b], t0 = w.i * a.s.tq;
@@ -239,6 +250,20 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       if (!ok) s_flag[0] = 1;
     }
     return __all_sync(~0u, ok);
+  };
+
+  int drawn = 0;  // segments so far
+  // To the next segment; false once a wait has run out.
+  auto next = [&]() -> bool {
+    if (!draws) {
+      if (drawn++) w.next();
+      return true;
+    }
+    const int k = drawn++;
+    if (!wait(&seg_full[k & 3], k >> 2)) return false;
+    const int4 e = s_seg[k & 3];
+    w.jump(e.x, e.y, e.z);
+    return true;
   };
 
   if (warp == 9) {
@@ -271,7 +296,59 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       h_prev = h;
       return true;
     };
-    for (; w.more() && ok; w.next()) {
+    // Draws the CTA's next pair for all its warps: number k of the pairs in the
+    // order sequence, row tile pair (last first, as it sees most), key head; the
+    // sequences whose last pair is longest first, by powers of two.
+    int level = 31 - __clz((int)tab.head[5] - a.s.start), from = 0, seq = 0, base = 0, count = 0, last = 0;
+    auto draw = [&] {
+      const int jobs = (int)tab.head[4];
+      int k = 0;
+      if (lane == 0) k = atomicAdd(a.ctr + 32 * gridDim.x, 1);
+      k = __shfl_sync(~0u, k, 0);
+      // every CTA draws until it gets none: after the last of them the counter rests
+      if (lane == 0 && k == jobs + (int)gridDim.x - 1) a.ctr[32 * gridDim.x] = 0;
+      if (k >= jobs) {
+        seq = -1;
+      } else {
+        while (k >= base + count) {
+          base += count;
+          int n = 0;
+          unsigned found;
+          for (;;) {
+            const int b = (from & ~31) + lane;
+            n = b >= from && b < a.p.batch ? (tab.qn[b] + a.s.tq - 1) / a.s.tq : 0;
+            found = __ballot_sync(
+                ~0u, n > 0 && 31 - __clz(tile_range(a.s, tab.qn[b], tab.kv[b], n - 1).n) == level);
+            if (found || level < 0) break;
+            from = (from & ~31) + 32;
+            if (from >= a.p.batch) from = 0, --level;
+          }
+          if (level < 0) {
+            seq = -1;
+            break;
+          }
+          const int l = __ffs(found) - 1;
+          seq = (from & ~31) + l;
+          from = seq + 1;
+          if (from >= a.p.batch) from = 0, --level;
+          last = __shfl_sync(~0u, n, l) - 1;
+          count = (last + 1) * a.s.hkv;
+        }
+      }
+      const int r = k - base, up = r / a.s.hkv;
+      w.jump(seq, r - up * a.s.hkv, last - up);
+      if (lane == 0) {
+        s_seg[drawn & 3] = make_int4(seq, r - up * a.s.hkv, last - up, 0);
+        mbar_arrive(&seg_full[drawn & 3]);
+      }
+      ++drawn;
+      __syncwarp();
+    };
+    auto advance = [&] {
+      if (draws) draw();
+      else next();
+    };
+    for (advance(); w.more() && ok; advance()) {
       const bool two = has_b();
       const int row = paged_row(a.p, w.b);
       const int32_t* trow = a.p.table + (long long)(row < 0 ? 0 : row) * a.p.table_stride;
@@ -352,9 +429,9 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     const std::integral_constant<int, 1> B;
     int i = 0, seg = 0;
     uint32_t pa = 0, pb = 0, clean = 0;  // phases: P of A and B; edge tiles of each slot
-    bool ok = w.more() && wait(&full[0], 0);
+    bool ok = next() && w.more() && wait(&full[0], 0);
 #pragma unroll 1
-    for (; ok; w.next(), ++seg) {
+    for (; ok; ok = ok && next(), ++seg) {
       // the segment's first Q·Kᵀ, while the output of the one before is read
       ok = w.more() && wait(q_full, seg);
       if (!ok) break;
@@ -415,8 +492,8 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   } else if (warp == 10) {
     // ---------------------------------------------------------------- edge values
     int i = 0, seg = 0;
-    bool ok = true;
-    for (; w.more() && ok; w.next(), ++seg) {
+    bool ok = next();
+    for (; ok && w.more(); ok = ok && next(), ++seg) {
       const EdgeRange er = edges();
       for (int k = 0; k < w.n && ok; ++k) {
         ++i;
@@ -482,8 +559,8 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     const uint32_t none = a.c < 0.f ? 0x7F800000u : 0xFF800000u;
     uint32_t sn = 0, on = 0;
     int seg = 0;
-    bool ok = true;
-    for (; w.more() && ok; w.next(), ++seg) {
+    bool ok = next();
+    for (; ok && w.more(); ok = ok && next(), ++seg) {
       if (x == 1 && !has_b()) continue;
       const EdgeRange er = edges();
       const int qn = tab.qn[w.b];
@@ -736,7 +813,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     SplitWalk f(a.s, tab, u0, u1);
     int4 d = make_int4(0, 0, 0, 0);
     for (; f.more(); f.next())
-      if (!f.whole && f.tile_unit() >= u0) {
+      if (!draws && !f.whole && f.tile_unit() >= u0) {
         const int n = (int)(cta_of(f.tile_unit() + f.tr.n - 1, W, G) - blockIdx.x + 1);
         const int t0 = f.i * a.s.tq, left = tab.qn[f.b] - t0;
         if (n > kTcFew && !s_flag[0])

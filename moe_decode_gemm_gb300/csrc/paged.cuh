@@ -184,17 +184,17 @@ __device__ __forceinline__ void edge_values(const PagedArgs& p, int row, int h, 
 // Shared-memory tables of a call's sequences (sized for the batch).
 struct SplitTables {
   long long* base;   // [batch + 1] first unit of each sequence
-  long long* head;   // [4] the call's units and workers, this worker's range
+  long long* head;   // [6] the call's units and workers, this worker's range, row tiles, the longest
   int* qn;           // [batch] new tokens
   int* kv;           // positions
   int* loc;          // [4] this worker's first sequence, head, row tile, unit in it
   static __host__ __device__ constexpr int bytes(int batch) {
-    return 8 * (batch + 1) + 8 * 4 + 8 * batch + 16;
+    return 8 * (batch + 1) + 8 * 6 + 8 * batch + 16;
   }
   __device__ explicit SplitTables(void* smem, int batch) {
     base = reinterpret_cast<long long*>(smem);
     head = base + batch + 1;
-    qn = reinterpret_cast<int*>(head + 4);
+    qn = reinterpret_cast<int*>(head + 6);
     kv = qn + batch;
     loc = kv + batch;
   }
@@ -202,11 +202,13 @@ struct SplitTables {
 
 // Fill the tables and find the range [u0, u1) of the W units that worker c of
 // `workers` (a CTA or a cluster) has, and where it begins. Called by all
-// threads of the CTA; ends with a barrier. G: workers that take part.
+// threads of the CTA; ends with a barrier. G: workers that take part. TILES: also
+// count the row tiles of all heads and the units of the longest.
 //
 // One warp does it, a lane for each of 32 sequences at a time: every call waits
 // for this before it can do anything else, and the other warps would add
 // barriers, not speed.
+template <bool TILES>
 __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape& s,
                                             const SplitTables& t, int min_units, long long c,
                                             long long workers, long long& W, long long& G,
@@ -229,7 +231,7 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     };
     const long long cap = (long long)p.width << p.page_shift;
     long long units = 0;
-    int all_tiles = 0;
+    int all_tiles = 0, longest = 0;
     Raw next = fetch(lane);
 #pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -261,6 +263,10 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
         if (lane == l) u = sum;
       }
       u *= s.hkv;
+      if (TILES && tiles > 0) {
+        const int n = tile_range(s, qn, kv, tiles - 1).n + s.start;
+        if (n > longest) longest = n;
+      }
       all_tiles += __reduce_add_sync(~0u, tiles);
       long long inc = u;
 #pragma unroll
@@ -279,9 +285,14 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     if (g < 2LL * all_tiles * s.hkv) g = 2LL * all_tiles * s.hkv;
     if (g < 1) g = 1;
     if (g > workers) g = workers;
+    if (TILES) longest = __reduce_max_sync(~0u, longest);
     if (lane == 0) {
       t.head[0] = units;
       t.head[1] = g;
+      if (TILES) {
+        t.head[4] = (long long)all_tiles * s.hkv;
+        t.head[5] = longest;
+      }
     }
   }
   __syncthreads();
@@ -377,6 +388,17 @@ struct SplitWalk {
     }
   }
   __device__ bool more() const { return u < u1; }
+  // instead of the range: all of one row tile, or nothing (b < 0)
+  __device__ void jump(int b_, int h_, int i_) {
+    u = 0;
+    u1 = b_ < 0 ? 0 : 1ll << 62;
+    if (b_ < 0) return;
+    b = b_;
+    h = h_;
+    i = i_;
+    off = 0;
+    load();
+  }
   __device__ void load() {
     tr = tile_range(s, t.qn[b], t.kv[b], i);
     const long long left = u1 - u;

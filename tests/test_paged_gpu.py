@@ -116,6 +116,24 @@ def test_strides_and_row_numbers(max_q):
     assert torch.all(res[:, 14 * 128:] == 3.0)
 
 
+@pytest.mark.parametrize("dim,page,window", [(64, 32, 0), (128, 16, 0), (64, 128, 130)])
+@pytest.mark.parametrize("many", [False, True])
+def test_many_row_tiles(dim, page, window, many):
+    # several times as many pairs of row tiles (4 tokens here) as SMs
+    if many:
+        new = [28 if b % 7 else 0 for b in range(45)]
+        bt = pg.Batch(new, [28 + (b * 331) % 900 for b in range(45)], 128, 2, dim, page, seed=12)
+    else:
+        bt = pg.Batch([3, 500, 290, 201, 1], [3, 500, 320, 700, 64], 128, 2, dim, page, seed=13)
+    kv = bt.device(dg, max_q=max(bt.new))
+    out, lse = run(bt, window, kv=kv)
+    assert dg.last_attention() == "tc"
+    for _ in range(3):
+        again, lse2 = run(bt, window, kv=kv)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    pg.check_attention(bt, out, lse, window)
+
+
 def test_padded_batch_leaves_other_rows_alone():
     bt = pg.Batch([1, 2], [30, 40], 4, 2, 64, 16, seed=9, pad=5)
     kv = bt.device(dg)
