@@ -228,12 +228,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   long long W, G, u0, u1;
   split_setup<true>(a.p, a.s, tab, a.min_units, blockIdx.x, gridDim.x, W, G, u0, u1);
   SplitWalk w(a.s, tab, u0, u1);
-  // Where there are pairs enough and none is long, equal ranges lose more to
-  // their ends (a pair cut and joined, or left whole beside a range that is
-  // then shorter) than CTAs that draw whole pairs as they become free, long
-  // ones first.
-  const bool draws = tab.head[4] >= 2 * gridDim.x && tab.head[4] < 1 << 30 &&
-                     tab.head[5] * 5 * gridDim.x <= 3 * W;
+  const bool draws = tab.head[4] != 0;
 
   auto edges = [&]() -> EdgeRange {
     const int qn = tab.qn[w.b], t0 = w.i * a.s.tq;
@@ -266,7 +261,266 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     return true;
   };
 
-  if (warp == 9) {
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int x = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = taddr + lanes + x * 128, to = taddr + lanes + 256 + x * D;
+    const int t = r / a.group, g = r - t * a.group;
+    uint8_t* mine = stage + warp * 2048;
+    const uint32_t none = a.c < 0.f ? 0x7F800000u : 0xFF800000u;
+    uint32_t sn = 0, on = 0;
+    int seg = 0;
+    bool ok = next();
+    for (; ok && w.more(); ok = ok && next(), ++seg) {
+      if (x == 1 && !has_b()) continue;
+      const EdgeRange er = edges();
+      const int qn = tab.qn[w.b];
+      const int t0 = w.i * a.s.tq + x * a.tq;
+      const int nt = qn - t0 < a.tq ? qn - t0 : a.tq;
+      const bool live = t < nt;
+      const int pos = tab.kv[w.b] - qn + t0 + t;
+      const int hi = live ? pos : -1;
+      const int lo = live && a.s.window > 0 ? pos - a.s.window + 1 : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < w.n; ++k) {
+        const int key0 = (w.j + k) * kTcKeys;
+        ok = wait(&s_full[x], sn++);
+        if (!ok) break;
+        tc_fence_after();
+        // One pass over the row with the maximum of the tiles before: weights,
+        // their sum and the row's own maximum. If that has outgrown m the pass
+        // is made again with the new one: S stays in TMEM until the weights
+        // replace it. A segment's first tile starts from the maximum of its
+        // first 32 columns.
+        if (er.in(key0, kTcKeys)) row_mask(ts, lo - key0, hi - key0, none);
+        uint32_t pk[64];
+        float top, sum;
+        if (k == 0) m = row_start(ts, a.c);
+#pragma unroll 1
+        for (;;) {
+          row_pass(ts, a.c, m == -INFINITY ? 0.f : m, pk, top, sum);
+          // (the first positions that a row sees need no other m than 0 if that is near)
+          if (m == -INFINITY && fabsf(top) <= kTcLazy) m = 0.f;
+          // (rows of the tile that hold no token hold whatever was there: they have
+          // no say, so that results do not depend on it)
+          if (!__any_sync(~0u, live && top > m + kTcLazy)) break;
+          // m was -inf before the first visible position: O and l are 0 then
+          const float mn = fmaxf(m, top);
+          const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+          m = mn;
+          l *= f;
+          if (k == 0) continue;
+#pragma unroll 1
+          for (int q = 0; q < D; q += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + q, o);
+            tmem_ld_wait();
+            tmem_settle<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(to + q, o);
+          }
+        }
+        l += sum;
+        tmem_st32(ts, pk);
+        tmem_st32(ts + 32, pk + 32);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      // while the last P·V runs: where the rows go and their sums. Four lanes
+      // write a row, 64 bytes of it at a time.
+      const long long tok0 = paged_first(a.p, w.b) + t0;
+      auto inverse = [](float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); };  // NaN stays NaN
+      uint16_t* dst[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = (warp & 3) * 32 + e * 8 + (lane >> 2), tt = row / a.group;
+        dst[e] = tt >= nt ? nullptr
+                          : a.out + (tok0 + tt) * a.ldo +
+                                (long long)(w.h * a.group + row - tt * a.group) * D + (lane & 3) * 8;
+      }
+      auto put_lse = [&](float top, float sum) {
+        if (live && a.lse)
+          a.lse[(tok0 + t) * a.hq + w.h * a.group + g] =
+              sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      };
+      // 32 columns of this warp's rows, through shared memory so that four lanes
+      // write 64 bytes of a row
+      auto put_rows = [&](const uint32_t* o, int q, float scale) {
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t* v = o + e * 8;
+          auto at = [&](int n) { return __uint_as_float(v[n]) * scale; };
+          *reinterpret_cast<uint4*>(mine + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) =
+              make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
+                         pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
+        }
+        __syncwarp();
+        uint4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int rr = e * 8 + (lane >> 2);
+          v[e] = *reinterpret_cast<const uint4*>(mine + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (dst[e]) *reinterpret_cast<uint4*>(dst[e] + q) = v[e];
+      };
+      const float inv = inverse(l);
+      if (w.whole) put_lse(m, l);
+      ok = wait(&o_full[x], on++);
+      if (!ok) break;
+      tc_fence_after();
+      if (s_poison[seg & 3] == seg + 1) {
+        // rows that see a non-finite edge value get it here
+#pragma unroll 1
+        for (int q = 0; q < D; q += 16) {
+          uint32_t o[16];
+          tmem_ld16(to + q, o);
+          tmem_ld_wait();
+          tmem_settle<16>(o);
+          if (live)
+            edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, lo, hi, w.j * kTcKeys,
+                           (w.j + w.n) * kTcKeys, q, [&](const uint16_t* v, int) {
+#pragma unroll
+                             for (int e = 0; e < 16; ++e) {
+                               const float f = bf_bits2f(__ldg(v + e));
+                               if (!isfinite(f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
+                             }
+                           });
+          __syncwarp();
+          tmem_st16(to + q, o);
+        }
+        tmem_st_wait();
+      }
+      if (w.whole) {
+#pragma unroll 1
+        for (int q = 0; q < D; q += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + q, o);
+          tmem_ld_wait();
+          tmem_settle<32>(o);
+          put_rows(o, q, inv);
+        }
+        // O is read: P of the next segment may be followed by its first P·V
+        tc_fence_before();
+        continue;
+      }
+      // The pair is shared with other CTAs: the first of them ends its range with
+      // it (slot 1), the others begin with it (slot 0). This warp leaves its rows'
+      // O, m and sum; the last of the CTAs' warps with these rows joins them, in
+      // CTA order. Above 8 CTAs in two steps, first within groups of about the
+      // square root of their number, as the join of each reads 64 KB a row tile;
+      // calls of few pairs leave those that more than 4 CTAs share to a second
+      // kernel that spreads them over the SMs (60 tokens over 9000 positions 39
+      // -> 33 us; for calls of many pairs that kernel costs more than it saves).
+      const long long cf = cta_of(w.tile_unit(), W, G);
+      const int nc = (int)(cta_of(w.tile_unit() + w.tr.n - 1, W, G) - cf + 1);
+      auto part_of = [&](int k) -> float* {
+        return a.ws + ((cf + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kPart + x * (Sh::kPart / 2);
+      };
+      const int self = (int)(blockIdx.x - cf);
+      {
+        float* part = part_of(self);
+#pragma unroll 1
+        for (int q = 0; q < D; q += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + q, o);
+          tmem_ld_wait();
+          tmem_settle<32>(o);
+          float4* col = reinterpret_cast<float4*>(
+              DG_AT(a.p.status, part, q * kTcRowsA + r * 4, Sh::kPart / 2 - 28 * kTcRowsA));
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            __stcg(col + e * kTcRowsA,
+                   make_float4(__uint_as_float(o[e * 4]), __uint_as_float(o[e * 4 + 1]),
+                               __uint_as_float(o[e * 4 + 2]), __uint_as_float(o[e * 4 + 3])));
+        }
+        __stcg(reinterpret_cast<float2*>(part + D * kTcRowsA) + r, make_float2(m, l));
+      }
+      tc_fence_before();
+      if (a.deep && nc > kTcFew) continue;
+      // the counter of a group is its first CTA's, by slot, warp and step
+      auto last_of = [&](int first, int step, int count) -> bool {
+        __syncwarp();
+        int old = 0;
+        if (lane == 0) {
+          int* ctr = a.ctr + (((cf + first) * 2 + (first == 0 ? 1 : 0)) * 8 + warp) * 2 + step;
+          old = atomic_add_acq_rel_gpu(ctr, 1);
+          if (old == count - 1) *ctr = 0;
+        }
+        __syncwarp();
+        return __shfl_sync(~0u, old, 0) == count - 1;
+      };
+      int size = nc;
+      if (nc > 8)
+        for (size = 3; size * size < nc;) ++size;
+      const int groups = (nc + size - 1) / size;
+      int first = self / size * size, stride = 1;
+      int count = nc - first < size ? nc - first : size;
+      bool joined = groups == 1;
+#pragma unroll 1
+      for (int step = 0; last_of(joined && step ? 0 : first, step, count); ++step) {
+        float M = -INFINITY, L = 0.f;
+        auto ml = [&](int k) {
+          return __ldcg(reinterpret_cast<const float2*>(part_of(first + k * stride) + D * kTcRowsA) + r);
+        };
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) M = fmaxf(M, ml(k).x);
+        // a state that has seen nothing (m = -inf) counts for nothing
+        auto factor = [&](float mk) { return M == -INFINITY ? 1.f : exp2_approx(mk - M); };
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+          const float2 s = ml(k);
+          L += factor(s.x) * s.y;
+        }
+        const float inv = inverse(L);
+#pragma unroll 1
+        for (int q = 0; q < D; q += 32) {
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 2
+          for (int k = 0; k < count; ++k) {
+            const float4* col =
+                reinterpret_cast<const float4*>(part_of(first + k * stride) + q * kTcRowsA + r * 4);
+            const float f = factor(ml(k).x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = __ldcg(col + e * kTcRowsA);
+              o[e * 4] += f * v.x;
+              o[e * 4 + 1] += f * v.y;
+              o[e * 4 + 2] += f * v.z;
+              o[e * 4 + 3] += f * v.w;
+            }
+          }
+          if (joined) {
+            put_rows(reinterpret_cast<const uint32_t*>(o), q, inv);
+          } else {
+            float4* col = reinterpret_cast<float4*>(part_of(first) + q * kTcRowsA + r * 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              __stcg(col + e * kTcRowsA, make_float4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]));
+          }
+        }
+        if (joined) {
+          put_lse(M, L);
+          break;
+        }
+        __stcg(reinterpret_cast<float2*>(part_of(first) + D * kTcRowsA) + r, make_float2(M, L));
+        // the groups' states, which the last group joins
+        joined = true;
+        first = 0;
+        stride = size;
+        count = groups;
+      }
+    }
+  } else if (warp == 9) {
     // ---------------------------------------------------------------- TMA
     const uint64_t pol = policy_evict_last();
     const int rows = a.p.page < kTcKeys ? a.p.page : kTcKeys;
@@ -302,11 +556,13 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     int level = 31 - __clz((int)tab.head[5] - a.s.start), from = 0, seq = 0, base = 0, count = 0, last = 0;
     auto draw = [&] {
       const int jobs = (int)tab.head[4];
-      int k = 0;
-      if (lane == 0) k = atomicAdd(a.ctr + 32 * gridDim.x, 1);
-      k = __shfl_sync(~0u, k, 0);
-      // every CTA draws until it gets none: after the last of them the counter rests
-      if (lane == 0 && k == jobs + (int)gridDim.x - 1) a.ctr[32 * gridDim.x] = 0;
+      int k = blockIdx.x;  // the first is the CTA's own
+      if (drawn > 0) {
+        if (lane == 0) k = gridDim.x + atomicAdd(a.ctr + 32 * gridDim.x, 1);
+        k = __shfl_sync(~0u, k, 0);
+        // every CTA draws until it gets none: after the last of them the counter rests
+        if (lane == 0 && k == jobs + (int)gridDim.x - 1) a.ctr[32 * gridDim.x] = 0;
+      }
       if (k >= jobs) {
         seq = -1;
       } else {
@@ -547,263 +803,6 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_clean[st]);
-      }
-    }
-  } else if (warp < 8) {
-    // ---------------------------------------------------------------- softmax
-    const int x = warp >> 2, r = threadIdx.x & 127;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = taddr + lanes + x * 128, to = taddr + lanes + 256 + x * D;
-    const int t = r / a.group, g = r - t * a.group;
-    uint8_t* mine = stage + warp * 2048;
-    const uint32_t none = a.c < 0.f ? 0x7F800000u : 0xFF800000u;
-    uint32_t sn = 0, on = 0;
-    int seg = 0;
-    bool ok = next();
-    for (; ok && w.more(); ok = ok && next(), ++seg) {
-      if (x == 1 && !has_b()) continue;
-      const EdgeRange er = edges();
-      const int qn = tab.qn[w.b];
-      const int t0 = w.i * a.s.tq + x * a.tq;
-      const int nt = qn - t0 < a.tq ? qn - t0 : a.tq;
-      const bool live = t < nt;
-      const int pos = tab.kv[w.b] - qn + t0 + t;
-      const int hi = live ? pos : -1;
-      const int lo = live && a.s.window > 0 ? pos - a.s.window + 1 : 0;
-      float m = -INFINITY, l = 0.f;
-      for (int k = 0; k < w.n; ++k) {
-        const int key0 = (w.j + k) * kTcKeys;
-        ok = wait(&s_full[x], sn++);
-        if (!ok) break;
-        tc_fence_after();
-        // One pass over the row with the maximum of the tiles before: weights,
-        // their sum and the row's own maximum. If that has outgrown m the pass
-        // is made again with the new one: S stays in TMEM until the weights
-        // replace it. A segment's first tile starts from the maximum of its
-        // first 32 columns.
-        if (er.in(key0, kTcKeys)) row_mask(ts, lo - key0, hi - key0, none);
-        uint32_t pk[64];
-        float top, sum;
-        if (k == 0) m = row_start(ts, a.c);
-#pragma unroll 1
-        for (;;) {
-          row_pass(ts, a.c, m == -INFINITY ? 0.f : m, pk, top, sum);
-          // (rows of the tile that hold no token hold whatever was there: they have
-          // no say, so that results do not depend on it)
-          if (!__any_sync(~0u, live && top > m + kTcLazy)) break;
-          // m was -inf before the first visible position: O and l are 0 then
-          const float mn = fmaxf(m, top);
-          const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-          m = mn;
-          l *= f;
-          if (k == 0) continue;
-#pragma unroll 1
-          for (int q = 0; q < D; q += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + q, o);
-            tmem_ld_wait();
-            tmem_settle<32>(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(to + q, o);
-          }
-        }
-        l += sum;
-        tmem_st32(ts, pk);
-        tmem_st32(ts + 32, pk + 32);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
-      }
-      if (!ok) break;
-      // while the last P·V runs: where the rows go and their sums. Four lanes
-      // write a row, 64 bytes of it at a time.
-      const long long tok0 = paged_first(a.p, w.b) + t0;
-      auto inverse = [](float sum) { return sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum); };  // NaN stays NaN
-      uint16_t* dst[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = (warp & 3) * 32 + e * 8 + (lane >> 2), tt = row / a.group;
-        dst[e] = tt >= nt ? nullptr
-                          : a.out + (tok0 + tt) * a.ldo +
-                                (long long)(w.h * a.group + row - tt * a.group) * D + (lane & 3) * 8;
-      }
-      auto put_lse = [&](float top, float sum) {
-        if (live && a.lse)
-          a.lse[(tok0 + t) * a.hq + w.h * a.group + g] =
-              sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-      };
-      // 32 columns of this warp's rows, through shared memory so that four lanes
-      // write 64 bytes of a row
-      auto put_rows = [&](const uint32_t* o, int q, float scale) {
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t* v = o + e * 8;
-          auto at = [&](int n) { return __uint_as_float(v[n]) * scale; };
-          *reinterpret_cast<uint4*>(mine + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) =
-              make_uint4(pack_bf16(at(0), at(1)), pack_bf16(at(2), at(3)),
-                         pack_bf16(at(4), at(5)), pack_bf16(at(6), at(7)));
-        }
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int rr = e * 8 + (lane >> 2);
-          const uint4 v = *reinterpret_cast<const uint4*>(
-              mine + rr * 64 + (((lane & 3) ^ (rr >> 1)) & 3) * 16);
-          if (dst[e]) *reinterpret_cast<uint4*>(dst[e] + q) = v;
-        }
-      };
-      if (w.whole) put_lse(m, l);
-      ok = wait(&o_full[x], on++);
-      if (!ok) break;
-      tc_fence_after();
-      if (s_poison[seg & 3] == seg + 1) {
-        // rows that see a non-finite edge value get it here
-#pragma unroll 1
-        for (int q = 0; q < D; q += 16) {
-          uint32_t o[16];
-          tmem_ld16(to + q, o);
-          tmem_ld_wait();
-          tmem_settle<16>(o);
-          if (live)
-            edge_values<D>(a.p, paged_row(a.p, w.b), w.h, er, lo, hi, w.j * kTcKeys,
-                           (w.j + w.n) * kTcKeys, q, [&](const uint16_t* v, int) {
-#pragma unroll
-                             for (int e = 0; e < 16; ++e) {
-                               const float f = bf_bits2f(__ldg(v + e));
-                               if (!isfinite(f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
-                             }
-                           });
-          __syncwarp();
-          tmem_st16(to + q, o);
-        }
-        tmem_st_wait();
-      }
-      if (w.whole) {
-        const float inv = inverse(l);
-#pragma unroll 1
-        for (int q = 0; q < D; q += 64) {
-          uint32_t o[64];
-          tmem_ld32(to + q, o);
-          tmem_ld32(to + q + 32, o + 32);
-          tmem_ld_wait();
-          tmem_settle<64>(o);
-          put_rows(o, q, inv);
-          put_rows(o + 32, q + 32, inv);
-        }
-        // O is read: P of the next segment may be followed by its first P·V
-        tc_fence_before();
-        continue;
-      }
-      // The pair is shared with other CTAs: the first of them ends its range with
-      // it (slot 1), the others begin with it (slot 0). This warp leaves its rows'
-      // O, m and sum; the last of the CTAs' warps with these rows joins them, in
-      // CTA order. Above 8 CTAs in two steps, first within groups of about the
-      // square root of their number, as the join of each reads 64 KB a row tile;
-      // calls of few pairs leave those that more than 4 CTAs share to a second
-      // kernel that spreads them over the SMs (60 tokens over 9000 positions 39
-      // -> 33 us; for calls of many pairs that kernel costs more than it saves).
-      const long long cf = cta_of(w.tile_unit(), W, G);
-      const int nc = (int)(cta_of(w.tile_unit() + w.tr.n - 1, W, G) - cf + 1);
-      auto part_of = [&](int k) -> float* {
-        return a.ws + ((cf + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kPart + x * (Sh::kPart / 2);
-      };
-      const int self = (int)(blockIdx.x - cf);
-      {
-        float* part = part_of(self);
-#pragma unroll 1
-        for (int q = 0; q < D; q += 32) {
-          uint32_t o[32];
-          tmem_ld32(to + q, o);
-          tmem_ld_wait();
-          tmem_settle<32>(o);
-          float4* col = reinterpret_cast<float4*>(
-              DG_AT(a.p.status, part, q * kTcRowsA + r * 4, Sh::kPart / 2 - 28 * kTcRowsA));
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            __stcg(col + e * kTcRowsA,
-                   make_float4(__uint_as_float(o[e * 4]), __uint_as_float(o[e * 4 + 1]),
-                               __uint_as_float(o[e * 4 + 2]), __uint_as_float(o[e * 4 + 3])));
-        }
-        __stcg(reinterpret_cast<float2*>(part + D * kTcRowsA) + r, make_float2(m, l));
-      }
-      tc_fence_before();
-      if (a.deep && nc > kTcFew) continue;
-      // the counter of a group is its first CTA's, by slot, warp and step
-      auto last_of = [&](int first, int step, int count) -> bool {
-        __syncwarp();
-        int old = 0;
-        if (lane == 0) {
-          int* ctr = a.ctr + (((cf + first) * 2 + (first == 0 ? 1 : 0)) * 8 + warp) * 2 + step;
-          old = atomic_add_acq_rel_gpu(ctr, 1);
-          if (old == count - 1) *ctr = 0;
-        }
-        __syncwarp();
-        return __shfl_sync(~0u, old, 0) == count - 1;
-      };
-      int size = nc;
-      if (nc > 8)
-        for (size = 3; size * size < nc;) ++size;
-      const int groups = (nc + size - 1) / size;
-      int first = self / size * size, stride = 1;
-      int count = nc - first < size ? nc - first : size;
-      bool joined = groups == 1;
-#pragma unroll 1
-      for (int step = 0; last_of(joined && step ? 0 : first, step, count); ++step) {
-        float M = -INFINITY, L = 0.f;
-        auto ml = [&](int k) {
-          return __ldcg(reinterpret_cast<const float2*>(part_of(first + k * stride) + D * kTcRowsA) + r);
-        };
-#pragma unroll 4
-        for (int k = 0; k < count; ++k) M = fmaxf(M, ml(k).x);
-        // a state that has seen nothing (m = -inf) counts for nothing
-        auto factor = [&](float mk) { return M == -INFINITY ? 1.f : exp2_approx(mk - M); };
-#pragma unroll 4
-        for (int k = 0; k < count; ++k) {
-          const float2 s = ml(k);
-          L += factor(s.x) * s.y;
-        }
-        const float inv = inverse(L);
-#pragma unroll 1
-        for (int q = 0; q < D; q += 32) {
-          float o[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 2
-          for (int k = 0; k < count; ++k) {
-            const float4* col =
-                reinterpret_cast<const float4*>(part_of(first + k * stride) + q * kTcRowsA + r * 4);
-            const float f = factor(ml(k).x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 v = __ldcg(col + e * kTcRowsA);
-              o[e * 4] += f * v.x;
-              o[e * 4 + 1] += f * v.y;
-              o[e * 4 + 2] += f * v.z;
-              o[e * 4 + 3] += f * v.w;
-            }
-          }
-          if (joined) {
-            put_rows(reinterpret_cast<const uint32_t*>(o), q, inv);
-          } else {
-            float4* col = reinterpret_cast<float4*>(part_of(first) + q * kTcRowsA + r * 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              __stcg(col + e * kTcRowsA, make_float4(o[e * 4], o[e * 4 + 1], o[e * 4 + 2], o[e * 4 + 3]));
-          }
-        }
-        if (joined) {
-          put_lse(M, L);
-          break;
-        }
-        __stcg(reinterpret_cast<float2*>(part_of(first) + D * kTcRowsA) + r, make_float2(M, L));
-        // the groups' states, which the last group joins
-        joined = true;
-        first = 0;
-        stride = size;
-        count = groups;
       }
     }
   }

@@ -202,13 +202,18 @@ struct SplitTables {
 
 // Fill the tables and find the range [u0, u1) of the W units that worker c of
 // `workers` (a CTA or a cluster) has, and where it begins. Called by all
-// threads of the CTA; ends with a barrier. G: workers that take part. TILES: also
-// count the row tiles of all heads and the units of the longest.
+// threads of the CTA; ends with a barrier. G: workers that take part.
+//
+// DRAW: where there are row tiles enough and none is long, equal ranges lose
+// more to their ends (a tile cut and joined, or left whole beside a range that
+// is then shorter) than workers that draw whole tiles as they become free, long
+// ones first: head[4] is then the number of row tiles of all heads (else 0),
+// head[5] the units of the longest, and there is no range.
 //
 // One warp does it, a lane for each of 32 sequences at a time: every call waits
 // for this before it can do anything else, and the other warps would add
 // barriers, not speed.
-template <bool TILES>
+template <bool DRAW>
 __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape& s,
                                             const SplitTables& t, int min_units, long long c,
                                             long long workers, long long& W, long long& G,
@@ -263,7 +268,7 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
         if (lane == l) u = sum;
       }
       u *= s.hkv;
-      if (TILES && tiles > 0) {
+      if (DRAW && tiles > 0) {
         const int n = tile_range(s, qn, kv, tiles - 1).n + s.start;
         if (n > longest) longest = n;
       }
@@ -285,12 +290,13 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
     if (g < 2LL * all_tiles * s.hkv) g = 2LL * all_tiles * s.hkv;
     if (g < 1) g = 1;
     if (g > workers) g = workers;
-    if (TILES) longest = __reduce_max_sync(~0u, longest);
+    if (DRAW) longest = __reduce_max_sync(~0u, longest);
     if (lane == 0) {
       t.head[0] = units;
       t.head[1] = g;
-      if (TILES) {
-        t.head[4] = (long long)all_tiles * s.hkv;
+      if (DRAW) {
+        const long long all = (long long)all_tiles * s.hkv;
+        t.head[4] = all >= 2 * workers && all < 1 << 30 && longest * 5 * workers <= 3 * units ? all : 0;
         t.head[5] = longest;
       }
     }
@@ -298,6 +304,8 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
   __syncthreads();
   W = t.head[0];
   G = t.head[1];
+  u0 = u1 = 0;
+  if (DRAW && t.head[4]) return;
   // The range's two ends, a warp each: the row tile that unit u falls into, and
   // the cut moved to an end of it if it is short.
   if (warp < 2) {
