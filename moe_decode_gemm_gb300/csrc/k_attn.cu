@@ -486,8 +486,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
       continue;
     }
     named_bar_sync(1, kCons);
-    const long long cf = cta_of(ut, W, G);
-    const int nc = (int)(cta_of(ut + w.tr.n - 1, W, G) - cf + 1);
+    const long long cf = worker_of(ut, W, G);
+    const int nc = (int)(worker_of(ut + w.tr.n - 1, W, G) - cf + 1);
     if (ct == 0) {
       // the tile's counters are its first worker's (which is first for no other)
       int* cp = DG_AT(a.p.status, a.ctr, cf * CL + rank, a.ctr_len);

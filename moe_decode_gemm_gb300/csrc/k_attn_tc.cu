@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       // calls of few pairs leave those that more than 4 CTAs share to a second
       // kernel that spreads them over the SMs (60 tokens over 9000 positions 39
       // -> 33 us; for calls of many pairs that kernel costs more than it saves).
-      const long long cf = cta_of(w.tile_unit(), W, G);
-      const int nc = (int)(cta_of(w.tile_unit() + w.tr.n - 1, W, G) - cf + 1);
+      const long long cf = worker_of(w.tile_unit(), W, G);
+      const int nc = (int)(worker_of(w.tile_unit() + w.tr.n - 1, W, G) - cf + 1);
       auto part_of = [&](int k) -> float* {
         return a.ws + ((cf + k) * 2 + (k == 0 ? 1 : 0)) * Sh::kPart + x * (Sh::kPart / 2);
       };
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     int4 d = make_int4(0, 0, 0, 0);
     for (; f.more(); f.next())
       if (!draws && !f.whole && f.tile_unit() >= u0) {
-        const int n = (int)(cta_of(f.tile_unit() + f.tr.n - 1, W, G) - blockIdx.x + 1);
+        const int n = (int)(worker_of(f.tile_unit() + f.tr.n - 1, W, G) - blockIdx.x + 1);
         const int t0 = f.i * a.s.tq, left = tab.qn[f.b] - t0;
         if (n > kTcFew && !s_flag[0])
           d = make_int4(n, paged_first(a.p, f.b) + t0, left < a.s.tq ? left : a.s.tq, f.h);

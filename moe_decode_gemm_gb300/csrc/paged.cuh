@@ -311,8 +311,7 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
   if (warp < 2) {
     long long u = c + warp;
     u = c < G ? (u < G ? div_small(u * W, G) : W) : 0;
-#pragma unroll 1
-    for (int round = 0; round < 2 && c < G && u < W; ++round) {
+    if (c < G && u < W) {
       int b = -1;  // the last sequence with base <= u
 #pragma unroll 1
       for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -323,7 +322,7 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
       }
       const long long U = div_small(t.base[b + 1] - t.base[b], s.hkv);
       const long long r = u - t.base[b];
-      const int h = (int)div_small(r, U);
+      int h = (int)div_small(r, U);
       long long off = r - h * U;
       int i = 0, cost = 0;
       const int qn = t.qn[b], kv = t.kv[b];
@@ -347,30 +346,38 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
         }
         off -= __shfl_sync(~0u, sum, 31);
       }
-      bool found = true;
       if (off > 0 && cost <= s.snap) {
-        if (2 * off < cost) {
-          u -= off;
-          off = 0;
-        } else {
-          u += cost - off;  // the next row tile's start: look for it
-          found = false;
+        u -= off;
+        if (2 * off >= cost) {  // to the next row tile
+          u += cost;
+          if (++i * s.tq >= qn) {
+            i = 0;
+            if (++h == s.hkv) {
+              h = 0;
+              do ++b;
+              while (b < p.batch && t.qn[b] == 0);
+            }
+          }
         }
+        off = 0;
       }
-      if (!found) continue;
       if (warp == 0 && lane == 0) {
         t.loc[0] = b;
         t.loc[1] = h;
         t.loc[2] = i;
         t.loc[3] = (int)off;
       }
-      break;
     }
     if (lane == 0) t.head[2 + warp] = u;
   }
   __syncthreads();
   u0 = t.head[2];
   u1 = t.head[3];
+}
+
+// The worker whose equal range of the W units has unit v.
+__device__ __forceinline__ long long worker_of(long long v, long long W, long long G) {
+  return div_small((v + 1) * G + W - 1, W) - 1;
 }
 
 // Walks this CTA's range segment by segment: a segment is the part of one row
