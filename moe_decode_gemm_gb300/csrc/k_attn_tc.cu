@@ -608,10 +608,13 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       const bool two = has_b();
       const int row = paged_row(a.p, w.b);
       const int32_t* trow = a.p.table + (long long)(row < 0 ? 0 : row) * a.p.table_stride;
-      auto page_at = [&](int j) -> int {
-        const int pos = j * kTcKeys + piece * rows;
-        if (piece >= pieces || pos >= w.tr.khi) return -1;
-        const int pg = __ldg(trow + (pos >> a.p.page_shift));
+      // this lane's piece of tile j: its entry of the page table, then its page
+      auto has = [&](int j) { return piece < pieces && j * kTcKeys + piece * rows < w.tr.khi; };
+      auto entry = [&](int j) -> int {
+        return has(j) ? __ldg(trow + ((j * kTcKeys + piece * rows) >> a.p.page_shift)) : -1;
+      };
+      auto page_of = [&](int j, int pg) -> int {
+        if (!has(j)) return -1;
         // a page that does not exist reads as zeros
         if ((pg < 0 || pg >= a.p.pages) && a.p.status) atomicOr(a.p.status, kStatusBounds);
         return pg < 0 || pg >= a.p.pages ? a.p.pages : pg;
@@ -629,12 +632,12 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         }
         __syncwarp();
       };
-      const int pg0 = page_at(w.j);
-      int pg_next = w.n > 1 ? page_at(w.j + 1) : -1;
+      const int pg0 = entry(w.j);
+      int pg_next = w.n > 1 ? entry(w.j + 1) : -1;
       // the first slot also brings the values that the segment before ends with:
       // they do not wait for that segment's last Q·Kᵀ, as its Q's place does
       if (seg == 0) load_q();
-      ok = put(pg0, place(w.j), w.h);
+      ok = put(page_of(w.j, pg0), place(w.j), w.h);
       if (seg > 0) {
         ok = ok && wait(q_empty, seg - 1);
         if (!ok) break;
@@ -643,8 +646,8 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       ++seg;
       for (int k = 1; k < w.n && ok; ++k) {
         const int pg = pg_next;
-        if (k + 1 < w.n) pg_next = page_at(w.j + k + 1);
-        ok = put(pg, place(w.j + k), w.h);
+        if (k + 1 < w.n) pg_next = entry(w.j + k + 1);
+        ok = put(page_of(w.j + k, pg), place(w.j + k), w.h);
       }
     }
     if (ok && i > 0) put(-1, 0, 0);

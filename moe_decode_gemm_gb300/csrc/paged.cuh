@@ -252,7 +252,9 @@ __device__ __forceinline__ void split_setup(const PagedArgs& p, const SplitShape
         if (p.status && (q0 != r.a || q1 != r.e || kv != r.kv || r.row < 0 || r.row >= p.table_rows))
           atomicOr(p.status, kStatusBounds);
       }
-      const int tiles = (qn + s.tq - 1) / s.tq;
+      // (a division only where it takes one)
+      int tiles = (qn > 0) + (qn > s.tq);
+      if (__any_sync(~0u, qn - s.tq > s.tq)) tiles = (qn + s.tq - 1) / s.tq;
       long long u = 0;
       if (tiles <= kFew)
         for (int i = 0; i < tiles; ++i) u += tile_range(s, qn, kv, i).n + s.start;
