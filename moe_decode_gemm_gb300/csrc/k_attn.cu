@@ -11,13 +11,23 @@
 // call reads 4*dim bytes per position and does 4*dim*14 flops on them: bound by
 // memory, and the matrix instructions only have to keep up with it.
 //
-// One producer warp brings key tiles of 64 positions (keys and values) into a
-// ring of shared-memory stages by TMA, page by page. The four consumer warps
-// split the row tile (16 rows a warp) and each tile's positions; every one keeps the
-// running maximum, sum and output of its own positions in registers, so that
-// the main loop has no barrier between warps, and they are joined once at the
-// end of a segment. Work over all sequences is cut into equal ranges (see
-// paged.cuh), so that one long sequence is shared by all SMs.
+// One producer warp brings key tiles of 64 positions (128 of small heads; keys
+// and values, 32 KB) into a ring of shared-memory stages by TMA, page by page.
+// Four or eight consumer warps split the row tile (16 rows a warp) and each
+// tile's positions; every one keeps the running maximum, sum and output of its
+// own positions in registers, so that the main loop has no barrier between
+// warps, and they are joined once at the end of a segment. Work over all
+// sequences is cut into equal ranges (see paged.cuh), so that one long sequence
+// is shared by all SMs; with up to 16 row tiles the ranges are clusters' of 8
+// CTAs, which join their parts through distributed shared memory (one token
+// over 509 positions 12 -> 7.5 us).
+//
+// Measured (56 query and 4 key heads of 128): 64 sequences of 2k to 32k
+// positions, 1.65 GB of keys and values, 240 us = 6.9 TB/s, what a copy reaches;
+// 11 sequences of 1.3k to 18k positions 31 us (27 of it their bytes). One token
+// over 509 positions 7.3 us, latency: about 0.5 us until the call before is
+// done, 2.5 for the lengths and the split, 1.5 until the first keys are there,
+// 1 of work, 1.5 for joining and the output.
 #include "launch.h"
 #include "launch_util.cuh"
 #include "paged.cuh"

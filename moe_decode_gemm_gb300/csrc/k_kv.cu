@@ -24,6 +24,10 @@ namespace dg {
 // for all its heads. (Heads of any token on any lane, each with its own places
 // and angles, took twice the instructions and were bound by them: 80 us for
 // 7.9k tokens of 64 heads of 128.)
+//
+// Measured: those 7.9k tokens, half of each head rotated, 262 MB in 48 us =
+// 5.5 TB/s, 81% of a copy's rate, instructions and memory about even; one token
+// 2.5 us, 64 tokens 3.2 us.
 constexpr int kAppendThreads = 256;
 
 struct AppendArgs {
@@ -192,7 +196,8 @@ cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c) {
 
 // ------------------------------------------------------------------ page copies
 // Pages move in chunks of 16 KB (256 threads): a chunk of one page of one layer
-// for each pass of a CTA, 64 bytes in flight per thread.
+// for each pass of a CTA, 64 bytes in flight per thread. Bound by memory: 701 pages
+// of four layers (735 MB read and written) 120 us = 6.1 TB/s.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = kCopyThreads * 64;
 
@@ -233,6 +238,7 @@ __device__ __forceinline__ void copy_pages(const KvPool& p, int n, const Pair& p
 // exchanged through distributed shared memory, and the cluster's barriers
 // separate reading refs, giving pages back and taking new ones. The state is
 // a few hundred KB at most, so that a call is bound by latency, not by bytes.
+// Measured: 4 to 5 us a call of 64 sequences of a pool of 4096 pages.
 constexpr int kPoolCtas = 8;
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
@@ -485,7 +491,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 // The live pages at or past n = (number of live pages) move, in order, to the
 // free pages before n. ws: [0] live pages before page n, [1] moves, then
 // holes[pages], movers[pages] (indexed by the live pages before them) and
-// rank[pages] (live pages before a page).
+// rank[pages] (live pages before a page). Bound by memory for a large pool: 9000
+// pages of four layers, half of them live in small holes, 1.14 GB in 186 us = 6.1 TB/s.
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
     kv_rank_kernel(const KvPool p, int* ws) {
   __shared__ int s_warp[32], s_cnt[kPoolCtas];

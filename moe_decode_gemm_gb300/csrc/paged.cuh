@@ -16,7 +16,8 @@
 // ranges, one per CTA, except that a row tile of at most `snap` units is not
 // cut: the cut goes to its nearer end, as joining costs more than it evens out.
 // The partial softmax states of a row tile that spans several ranges are joined
-// in CTA order.
+// in CTA order. (The figures: one token over 8k positions 15.5 us cut without
+// regard to ends, 14 with; 22 sequences of 100 to 300 positions 15 -> 10.)
 #pragma once
 
 #include "dg_common.cuh"
@@ -207,8 +208,11 @@ struct SplitTables {
 // DRAW: where there are row tiles enough and none is long, equal ranges lose
 // more to their ends (a tile cut and joined, or left whole beside a range that
 // is then shorter) than workers that draw whole tiles as they become free, long
-// ones first: head[4] is then the number of row tiles of all heads (else 0),
-// head[5] the units of the longest, and there is no range.
+// ones first (four prompts of up to 2047 tokens 168 -> 154 us, one of 2048 68 -> 59;
+// modelled over 300 batches of random lengths, those that the rule takes gain 3%
+// on average, the worst, of few long tiles, loses 24%). head[4] is then the number
+// of row tiles of all heads (else 0), head[5] the units of the longest, and there
+// is no range.
 //
 // One warp does it, a lane for each of 32 sequences at a time: every call waits
 // for this before it can do anything else, and the other warps would add
