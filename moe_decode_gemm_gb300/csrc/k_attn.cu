@@ -69,7 +69,13 @@ struct AttnShape {
   static constexpr int kStage = 2 * kKBytes;
   static constexpr int kStages = (CL > 1 ? 96 : 128) * 1024 / kStage;
   static constexpr int kLd = D + 8;                    // floats between rows of the join scratch
-  static constexpr int kScratch = kWarps * 16 * kLd * 4 + kWarps * 16 * 8;  // o; m and l
+  // Rows of 128 columns have their factors over the warps looked up (22 sequences
+  // of 100 to 300 positions 9.8 -> 9.2 us); for those of 64, and for the parts of a
+  // cluster, the barrier that takes costs more (12.7 -> 13.2, 7.2 -> 7.5).
+  static constexpr bool kFactors = D == 128 && CL == 1;
+  // o; m and l (or a warp's factor) of each warp's rows; of each row m, l and 1 / l
+  static constexpr int kScratch =
+      kWarps * 16 * kLd * 4 + kWarps * 16 * 8 + (kFactors ? kRows * 16 : 0);
   static constexpr int kItems = kRows * (D / 4);       // four columns of a row each
   static constexpr int kSlot = kItems * 6;             // floats of a partial tile: o, then m and l
   static constexpr int kMerged = CL > 1 ? kRows * (D + 2) * 4 : 0;  // a CTA's part of a cluster's tile
@@ -128,6 +134,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
                                              ~uintptr_t(1023));
   float* scratch = reinterpret_cast<float*>(smem + kStages * Sh::kStage);
   float* sc_ml = scratch + kWarps * 16 * Sh::kLd;  // [warp][16][m, l]
+  float4* sc_row = reinterpret_cast<float4*>(sc_ml + kWarps * 16 * 2);  // [row] m, l, 1 / l
   // [2] this CTA's part of a tile for its cluster: o [row][D], then m and l [row]
   float* merged = reinterpret_cast<float*>(smem + kStages * Sh::kStage + Sh::kScratch);
   uint64_t* full =
@@ -388,36 +395,69 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
     }
     const bool aborted = s_flag[0] != 0;
     const long long ut = w.tile_unit();
-    auto store = [&](int r, int d, const State& s) {
+    auto inverse = [](float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); };  // NaN stays NaN
+    auto store_lse = [&](int r, float m, float l) {
       const int t = r / a.group, g = r - t * a.group;
-      const long long tok = q0 + t0 + t;
-      const int head = w.h * a.group + g;
-      const float inv = s.l > 0.f ? 1.f / s.l : (s.l == 0.f ? 0.f : s.l);  // NaN stays NaN
-      *reinterpret_cast<uint2*>(a.out + tok * a.ldo + (long long)head * D + d) = make_uint2(
-          pack_bf16(s.v.x * inv, s.v.y * inv), pack_bf16(s.v.z * inv, s.v.w * inv));
-      if (a.lse && d == 0)
-        a.lse[tok * a.hq + head] =
-            s.l == 0.f ? -INFINITY : (s.m + log2f(s.l)) * 0.6931471805599453f;
+      if (a.lse)
+        a.lse[(long long)(q0 + t0 + t) * a.hq + w.h * a.group + g] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     };
-    // four columns of a row over the warps that share the row tile
-    auto own = [&](int r, int d) -> State {
-      const int at = ((r >> 4) * kKS * 16) + (r & 15);
-      State s = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+    auto store = [&](int r, int d, const State& s, float inv, bool lse) {
+      const int t = r / a.group, g = r - t * a.group;
+      *reinterpret_cast<uint2*>(a.out + (long long)(q0 + t0 + t) * a.ldo +
+                                (long long)(w.h * a.group + g) * D + d) =
+          make_uint2(pack_bf16(s.v.x * inv, s.v.y * inv), pack_bf16(s.v.z * inv, s.v.w * inv));
+      if (lse && d == 0) store_lse(r, s.m, s.l);
+    };
+    // a row's part of warp k of those that share it
+    auto part_at = [&](int r, int k) { return (r >> 4) * kKS * 16 + (r & 15) + k * 16; };
+    // a row's maximum and sum over its warps, and the warps' factors
+    auto row_state = [&](int r, float* f) -> float2 {
       float2 ml[kKS];
+      float M = -INFINITY, L = 0.f;
 #pragma unroll
       for (int k = 0; k < kKS; ++k) {
-        ml[k] = *reinterpret_cast<const float2*>(sc_ml + (at + k * 16) * 2);
-        s.m = fmaxf(s.m, ml[k].x);
+        ml[k] = *reinterpret_cast<const float2*>(sc_ml + part_at(r, k) * 2);
+        M = fmaxf(M, ml[k].x);
       }
 #pragma unroll
       for (int k = 0; k < kKS; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(scratch + (at + k * 16) * Sh::kLd + d);
-        const float f = s.m == -INFINITY ? 1.f : exp2_approx(ml[k].x - s.m);
-        s.l += f * ml[k].y;
-        s.v.x += f * v.x;
-        s.v.y += f * v.y;
-        s.v.z += f * v.z;
-        s.v.w += f * v.w;
+        f[k] = M == -INFINITY ? 1.f : exp2_approx(ml[k].x - M);
+        L += f[k] * ml[k].y;
+      }
+      return make_float2(M, L);
+    };
+    if (Sh::kFactors) {
+      if (ct < rows) {
+        float f[kKS];
+        const float2 ml = row_state(ct, f);
+#pragma unroll
+        for (int k = 0; k < kKS; ++k) sc_ml[part_at(ct, k) * 2] = f[k];
+        sc_row[ct] = make_float4(ml.x, ml.y, inverse(ml.y), 0.f);
+        if (w.whole && !aborted) store_lse(ct, ml.x, ml.y);
+      }
+      named_bar_sync(1, kCons);
+    }
+    // four columns of a row over the warps that share the row tile
+    auto own = [&](int r, int d) -> State {
+      State s = {make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f};
+      float f[kKS];
+      if (Sh::kFactors) {
+        const float4 row = sc_row[r];
+        s.m = row.x, s.l = row.y;
+#pragma unroll
+        for (int k = 0; k < kKS; ++k) f[k] = sc_ml[part_at(r, k) * 2];
+      } else {
+        const float2 ml = row_state(r, f);
+        s.m = ml.x, s.l = ml.y;
+      }
+#pragma unroll
+      for (int k = 0; k < kKS; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(scratch + part_at(r, k) * Sh::kLd + d);
+        s.v.x += f[k] * v.x;
+        s.v.y += f[k] * v.y;
+        s.v.z += f[k] * v.z;
+        s.v.w += f[k] * v.w;
       }
       return s;
     };
@@ -426,9 +466,9 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
     // see to the same columns, so that the last of them joins these.
     auto slot_of = [&](long long c, bool first) { return a.ws + (c * 2 + (first ? 1 : 0)) * Sh::kSlot; };
     float* mine = slot_of(worker, ut >= u0);
-    auto put = [&](int x, const State& s) {
+    auto put = [&](int x, const State& s, float inv, bool lse) {
       if (w.whole) {
-        if (!aborted) store(x / (D / 4), (x % (D / 4)) * 4, s);
+        if (!aborted) store(x / (D / 4), (x % (D / 4)) * 4, s, inv, lse);
       } else {
         __stcg(reinterpret_cast<float4*>(DG_AT(a.p.status, mine, x * 4, Sh::kSlot - 3)), s.v);
         __stcg(reinterpret_cast<float2*>(mine + Sh::kItems * 4 + x * 2), make_float2(s.m, s.l));
@@ -452,7 +492,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
         const int x = x0 + q * kCons, r = x / (D / 4), d = (x % (D / 4)) * 4;
         if (x >= items) break;
         if (CL == 1) {
-          put(x, s[q]);
+          put(x, s[q], Sh::kFactors ? sc_row[r].z : inverse(s[q].l), !Sh::kFactors);
         } else {
           *reinterpret_cast<float4*>(buf + r * D + d) = s[q].v;
           if (d == 0)
@@ -488,7 +528,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
         const float m2 = __shfl_xor_sync(~0u, s.m, 1), l2 = __shfl_xor_sync(~0u, s.l, 1);
         if (x >= last || (ct & 1)) continue;
         s.add(v2, m2, l2);
-        put(x, s);
+        put(x, s, inverse(s.l), true);
       }
     }
     if (w.whole) {
@@ -508,27 +548,40 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
     }
     named_bar_sync(1, kCons);
     if (s_flag[1] && !aborted) {
-      constexpr int kAhead = 4;  // parts in flight
+      // parts, and items of each, whose loads are in flight together (two items
+      // where the registers last: 11 sequences 31.2 -> 27.8 us)
+      constexpr int kAhead = 4, kItemsAhead = kWarps > 4 ? 1 : 2;
 #pragma unroll 1
-      for (int x = first + ct; x < last; x += kCons) {
-        State s = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+      for (int x0 = first + ct; x0 < last; x0 += kItemsAhead * kCons) {
+        State s[kItemsAhead];
+#pragma unroll
+        for (int i = 0; i < kItemsAhead; ++i) s[i] = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
 #pragma unroll 1
         for (int k0 = 0; k0 < nc; k0 += kAhead) {
-          float4 v[kAhead];
-          float2 ml[kAhead];
+          float4 v[kItemsAhead][kAhead];
+          float2 ml[kItemsAhead][kAhead];
 #pragma unroll
           for (int k = 0; k < kAhead; ++k)
             if (k0 + k < nc) {
               const float* p = slot_of(cf + k0 + k, k0 + k == 0);
-              v[k] = __ldcg(reinterpret_cast<const float4*>(p + x * 4));
-              ml[k] = __ldcg(reinterpret_cast<const float2*>(p + Sh::kItems * 4 + x * 2));
+#pragma unroll
+              for (int i = 0; i < kItemsAhead; ++i) {
+                const int x = x0 + i * kCons < last ? x0 + i * kCons : x0;
+                v[i][k] = __ldcg(reinterpret_cast<const float4*>(p + x * 4));
+                ml[i][k] = __ldcg(reinterpret_cast<const float2*>(p + Sh::kItems * 4 + x * 2));
+              }
             }
 #pragma unroll
           for (int k = 0; k < kAhead; ++k)
-            if (k0 + k < nc) s.add(v[k], ml[k].x, ml[k].y);
+            if (k0 + k < nc)
+#pragma unroll
+              for (int i = 0; i < kItemsAhead; ++i) s[i].add(v[i][k], ml[i][k].x, ml[i][k].y);
         }
-        const int r = x / (D / 4);
-        store(r, (x % (D / 4)) * 4, s);
+#pragma unroll
+        for (int i = 0; i < kItemsAhead; ++i) {
+          const int x = x0 + i * kCons;
+          if (x < last) store(x / (D / 4), (x % (D / 4)) * 4, s[i], inverse(s[i].l), true);
+        }
       }
     }
     named_bar_sync(1, kCons);
