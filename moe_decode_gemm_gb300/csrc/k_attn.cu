@@ -306,12 +306,19 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
 #pragma unroll
         for (int t = 0; t < kBlk / 8; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[t][e] *= a.c;  // before the mask: c may be 0 or negative
-            const int key = key0 + kr + t * 8 + c0 + (e & 1);
-            if (edge && (key > hi[e >> 1] || key < lo[e >> 1])) s[t][e] = -INFINITY;
-            mx[e >> 1] = fmaxf(mx[e >> 1], s[t][e]);
-          }
+          for (int e = 0; e < 4; ++e) s[t][e] *= a.c;  // before the mask: c may be 0 or negative
+        if (edge)
+#pragma unroll
+          for (int t = 0; t < kBlk / 8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + kr + t * 8 + c0 + (e & 1);
+              if (key > hi[e >> 1] || key < lo[e >> 1]) s[t][e] = -INFINITY;
+            }
+#pragma unroll
+        for (int t = 0; t < kBlk / 8; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[t][e]);
         bool grew = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
