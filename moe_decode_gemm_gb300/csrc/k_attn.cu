@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
 
     for (int k = rank; k < w.n; k += CL, ++it) {
       const int st = it % kStages, key0 = (w.j + k) * kKeys;
-      if (!s_flag[0] && !mbar_wait(&full[st], (it / kStages) & 1, a.timeout_ns, a.p.status))
+      if (!mbar_try_wait(&full[st], (it / kStages) & 1) && !s_flag[0] &&
+          !mbar_wait(&full[st], (it / kStages) & 1, a.timeout_ns, a.p.status))
         s_flag[0] = 1;
       const uint32_t kb = smem_u32(smem + st * Sh::kStage), vb = kb + Sh::kKBytes;
       const bool edge = er.in(key0, kKeys);
@@ -291,13 +292,30 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
           // values that no row sees (the unused end of a page may hold
           // anything), and non-finite ones that only some rows see, become 0.
           // Warps of other row tiles may do the same to the same values.
+          auto within = [&](int pos) {
+            const int n = pos - key0;
+            return n < kr ? kr : (n > kr + kBlk ? kr + kBlk : n);
+          };
+          auto at = [&](int x) {  // 8 values: x / (D / 8) positions into the tile
+            const int key = x / (D / 8), ch = x % (D / 8);
+            return reinterpret_cast<uint4*>(smem + st * Sh::kStage + Sh::kKBytes +
+                                            (ch >> 3) * Sh::kHalf + key * 128 +
+                                            (((ch & 7) ^ (key & 7)) << 4));
+          };
+          const int seen0 = within(er.klo), seen1 = within(er.khi);
+          // before and past what is seen; then what not all rows see
 #pragma unroll 1
-          for (int x = lane; x < kBlk * (D / 8); x += 32) {
-            const int key = kr + x / (D / 8), ch = x % (D / 8);
-            uint4* at = reinterpret_cast<uint4*>(smem + st * Sh::kStage + Sh::kKBytes +
-                                                 (ch >> 3) * Sh::kHalf + key * 128 +
-                                                 (((ch & 7) ^ (key & 7)) << 4));
-            found |= clean_edge_value(at, er, key0 + key);
+          for (int side = 0; side < 2; ++side) {
+            const int from = side ? (seen1 > seen0 ? seen1 : seen0) : kr, to = side ? kr + kBlk : seen0;
+#pragma unroll 1
+            for (int x = from * (D / 8) + lane; x < to * (D / 8); x += 32)
+              *at(x) = make_uint4(0, 0, 0, 0);
+            const int some0 =
+                side ? within(er.all_hi > er.all_lo ? er.all_hi : er.all_lo) : seen0;
+            const int some1 = side ? seen1 : within(er.all_lo < er.khi ? er.all_lo : er.khi);
+#pragma unroll 1
+            for (int x = some0 * (D / 8) + lane; x < some1 * (D / 8); x += 32)
+              found |= clean_edge_value(at(x), er, key0 + x / (D / 8));
           }
           fence_async_shared();
           __syncwarp();
