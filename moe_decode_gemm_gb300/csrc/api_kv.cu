@@ -57,13 +57,27 @@ static int attention(const dec_kv_view* kv, const AttnCall& c, void* stream) {
   Ctx cx;
   void* ws;
   int* ctr;
-  // Rows (token, query head) of the longest chunk: up to 32 on mma.sync, in
-  // row tiles of 16 or 32; above that tcgen05. 8 sequences of 4 tokens (56 rows)
-  // over 512 / 2048 / 8192 positions: 30 / 39 / 73 us in mma.sync row tiles of 64,
-  // 18 / 21 / 43 on tcgen05; of 2 tokens (28 rows) over 64 / 2048: 9.4 / 24
-  // against 13 / 21.
-  const int64_t rows = (int64_t)(kv->max_q > 0 ? kv->max_q : c.tokens) * group;
+  // Rows (token, query head) of the longest chunk. Up to 32: mma.sync, a row tile
+  // of 16 or 32. Above, mma.sync reads the keys once for every 32 rows where
+  // tcgen05 reads them once, but starts and joins sooner: it stays while the
+  // reading does not count. us of mma.sync / tcgen05 over 64, 512, 2048 and 8192
+  // positions:
+  //   28 rows, 8 sequences of 4 key heads of 128   9/13  14/18  20/28  33/39
+  //   56 rows, the same                            9/13  14/18  21/28  42/39
+  //   56 rows, 40 sequences                       15/13  25/23  62/48 187/120
+  //   64 rows, 8 sequences of 8 key heads of 64    8/9   11/13  21/22  45/42
+  //   64 rows, 40 sequences                       20/25  32/34  68/71 196/210
+  //   126 rows, 1 sequence of 4 key heads of 128   9/12  14/17  20/26  30/27
+  //   128 rows, 1 sequence of 8 key heads of 64    8/10  10/14  16/21  22/26
+  //   128 rows, 8 sequences of them               13/9   19/13  30/22  70/42
+  const int64_t longest = kv->max_q > 0 ? kv->max_q : c.tokens, rows = longest * group;
   bool tc = rows > 32;
+  if (tc && group <= 32 && rows <= 128) {
+    const int tq = 32 / group;
+    const int64_t tiles = (longest + tq - 1) / tq * v.batch * v.hkv;
+    if (rows <= 64) tc = v.dim == 128 && tiles * 2 > sms;
+    else tc = tiles * v.dim > 17 * sms;
+  }
   const char* force = std::getenv("DEC_FORCE");
   if (force && !std::strcmp(force, "mma") && group <= 32) tc = false;
   if (force && !std::strcmp(force, "tc")) tc = true;

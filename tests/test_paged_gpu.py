@@ -512,6 +512,21 @@ def test_regimes_and_forced_regimes(monkeypatch):
             assert dg.last_attention() == (force or ("mma" if max_q == 1 else "tc"))
 
 
+@pytest.mark.parametrize("force", ["", "mma", "tc"])
+@pytest.mark.parametrize("dim,hq,hkv,page,new,total,window", [
+    (128, 14, 1, 16, [3, 4, 1, 0], [3, 300, 129, 40], 0),
+    (128, 24, 8, 64, [12, 20, 7], [500, 20, 135], 40),
+    (64, 8, 2, 32, [8, 16, 31, 1], [130, 16, 700, 257], 100),
+    (64, 17, 1, 128, [2, 5, 7], [128, 1000, 7], 0),
+    (64, 4, 4, 256, [100, 33], [100, 290], 9)])
+def test_some_tens_of_rows(monkeypatch, force, dim, hq, hkv, page, new, total, window):
+    # where either kernel may be chosen, and each when it is forced
+    monkeypatch.setenv("DEC_FORCE", force)
+    bt = pg.Batch(new, total, hq, hkv, dim, page, seed=54)
+    pg.check_attention(bt, *run(bt, window, max_q=max(new)), window)
+    assert dg.last_attention() in ([force] if force else ["mma", "tc"])
+
+
 # ------------------------------------------------------------------ the rest
 def test_index_checks_find_nothing():
     """The index-checking build of the library over shapes that split and join."""
