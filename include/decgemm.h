@@ -20,10 +20,12 @@
  *    reported as DEC_ETIMEOUT by dec_sync_check or by the next call.
  *  - The library owns a per-device workspace (split-K partials, arrival
  *    counters, routing tables, MoE intermediates), one side stream for the
- *    shared expert, and events. They are created on first use, grown when a
- *    larger shape arrives, and released by dec_shutdown. Calls that may
+ *    shared expert, and events. They are created on first use; a larger shape
+ *    gets a larger one, and all are released by dec_shutdown only, so that a
+ *    captured graph stays valid until then. Calls that may
  *    allocate must not be the first ones issued inside a CUDA graph capture:
- *    make one call of each shape outside capture first. Calls that share the
+ *    make one call of each shape outside capture first (of the paged-cache
+ *    calls, one that uses the workspace). Calls that share the
  *    workspace must be ordered on one stream (the library orders its own
  *    side stream).
  *
@@ -456,6 +458,7 @@ typedef struct dec_kv_pool {
  * Pages that a call gives back are free from the next call on. kv_resize, kv_fork
  * and kv_compact use the library's workspace, as kv_attention does: order such
  * calls on one stream, and make a first one before capturing them in a graph.
+ * The workspace has one size, whatever the calls (about 50 MB).
  */
 int kv_resize(const dec_kv_pool* pool, const int32_t* seqs, const int32_t* lens, int n, void* stream);
 int kv_free(const dec_kv_pool* pool, const int32_t* seqs, int n, void* stream);

@@ -115,6 +115,9 @@ struct DevState {
   Buf ws_main, ctr_main, ws_side, ctr_side;
   Buf kv, ctr_kv;                         // paged cache: partial tiles and page lists; counters
   Buf moe;                                // routing tables + intermediates
+  // Buffers that larger ones have taken the place of, and those of their words
+  // that are zero at rest: a captured graph may hold their addresses.
+  std::vector<Buf> old, old_zero;
   int moe_M = 0, moe_E = 0, moe_k = 0, moe_I = 0, moe_H = 0, moe_L = 0;
   MoeBufs mb = {};
 };
@@ -171,19 +174,25 @@ static int get_dev(DevState** out) {
   return DEC_OK;
 }
 
-// Grow a zero-initialised device buffer. Growing synchronises the device.
-static int ensure(Buf& b, size_t bytes, cudaStream_t st) {
+// Replace a device buffer by a larger one, zero-initialised. The smaller one is
+// kept until dec_shutdown: kernels hold its address in their arguments, and
+// those of a captured graph are launched again long after this call. (With a
+// quarter to spare each time, all the buffers kept are at most four times the
+// last one.) counters: the buffer is zero at rest.
+static int ensure(DevState* s, Buf& b, size_t bytes, cudaStream_t st, bool counters = false) {
   if (b.bytes >= bytes) return DEC_OK;
-  if (b.p) {
-    cudaDeviceSynchronize();
-    cudaFree(b.p);
-    b.p = nullptr;
-    b.bytes = 0;
+  Buf fresh;
+  fresh.bytes = bytes + bytes / 4;
+  if (cudaMalloc(&fresh.p, fresh.bytes) != cudaSuccess) return DEC_ENOMEM;
+  if (cudaMemsetAsync(fresh.p, 0, fresh.bytes, st) != cudaSuccess) {
+    cudaFree(fresh.p);
+    return DEC_ECUDA;
   }
-  size_t want = bytes + bytes / 4;
-  if (cudaMalloc(&b.p, want) != cudaSuccess) return DEC_ENOMEM;
-  if (cudaMemsetAsync(b.p, 0, want, st) != cudaSuccess) return DEC_ECUDA;
-  b.bytes = want;
+  if (b.p) {
+    s->old.push_back(b);
+    if (counters) s->old_zero.push_back(b);
+  }
+  b = fresh;
   return DEC_OK;
 }
 
@@ -367,8 +376,8 @@ static int linear_impl(const void* x, const void* W, const void* res, void* y, i
   }
   if (grid > T) grid = T;
   const size_t slot_rows = wide ? 256 : 128;
-  if ((rc = ensure(s->ws_main, (size_t)grid * 2 * slot_rows * xr * sizeof(float), st))) return rc;
-  if ((rc = ensure(s->ctr_main, (size_t)tiles * sizeof(int), st))) return rc;
+  if ((rc = ensure(s, s->ws_main, (size_t)grid * 2 * slot_rows * xr * sizeof(float), st))) return rc;
+  if ((rc = ensure(s, s->ctr_main, (size_t)tiles * sizeof(int), st, true))) return rc;
   Ctx cx = make_ctx(s, st);
   cx.ldx = ldx;
   cx.ws_len = (long long)(s->ws_main.bytes / sizeof(float));
@@ -424,13 +433,17 @@ static int moe_bufs(DevState* s, int M, int H, int E, int k, int I, int L, cudaS
   size_t o_rctr = off; off += al(4);
   size_t o_z = off; off += al((size_t)Mx * (Lx > 0 ? Lx : 1) * 2);
   size_t o_u = off; off += al((size_t)Mx * Hx * 4);
-  int rc = ensure(s->moe, off, st);
+  // A new buffer, even where the slack of the present one would hold the larger
+  // shapes: a graph captured with the present layout goes on using it, and
+  // expects its arrival counter to be zero at rest.
+  Buf fresh;
+  int rc = ensure(s, fresh, off, st);
   if (rc) return rc;
-  // The layout has changed even when the buffer did not have to grow (its
-  // slack held the larger shapes): the arrival counters that must be zero at
-  // rest now sit on bytes of the old layout. Clear it, on the stream that
-  // orders every earlier use of the buffer.
-  if (cudaMemsetAsync(s->moe.p, 0, off, st) != cudaSuccess) return DEC_ECUDA;
+  if (s->moe.p) {
+    s->old.push_back(s->moe);
+    s->old_zero.push_back(Buf{s->mb.route_ctr, sizeof(int)});
+  }
+  s->moe = fresh;
   uint8_t* b = (uint8_t*)s->moe.p;
   s->mb.logits = (float*)(b + o_logits);
   s->mb.nact = (int*)(b + o_nact);
@@ -487,12 +500,12 @@ static int moe_impl(const void* x, const void* Wr, const void* W13, const void* 
   // at most E + M*topk/16 groups, each with its own tile counters
   const int max_groups = E + (M * topk + 15) / 16;
   const size_t ctr_bytes = (size_t)(max_groups * (size_t)maxt + 64) * sizeof(int);
-  if ((rc = ensure(s->ws_main, ws_bytes, st))) return rc;
-  if ((rc = ensure(s->ctr_main, ctr_bytes, st))) return rc;
+  if ((rc = ensure(s, s->ws_main, ws_bytes, st))) return rc;
+  if ((rc = ensure(s, s->ctr_main, ctr_bytes, st, true))) return rc;
   const bool shared = Ws13 != nullptr;
   if (shared) {
-    if ((rc = ensure(s->ws_side, ws_bytes, st))) return rc;
-    if ((rc = ensure(s->ctr_side, (size_t)(maxt + 64) * sizeof(int), st))) return rc;
+    if ((rc = ensure(s, s->ws_side, ws_bytes, st))) return rc;
+    if ((rc = ensure(s, s->ctr_side, (size_t)(maxt + 64) * sizeof(int), st, true))) return rc;
   }
   Ctx cx = make_ctx(s, st);
   cx.ws_len = (long long)(s->ws_main.bytes / sizeof(float));
@@ -599,8 +612,17 @@ int kv_context(void* stream, size_t bytes, size_t ctrs, Ctx* cx, void** ws, int*
   int rc = get_dev(&s);
   if (rc) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (bytes && (rc = ensure(s->kv, bytes, st))) return rc;
-  if (ctrs && (rc = ensure(s->ctr_kv, ctrs * sizeof(int), st))) return rc;
+  // What the largest of the paged-cache calls takes (40 MB on 152 SMs), from
+  // the first of them on: a decode step, a chunk and a compaction take turns,
+  // and none of them is the first to allocate inside a capture.
+  size_t most = attn_tc_ws(128, s->sms);
+  const size_t lists = ((size_t)3 * kMaxPages + 2) * sizeof(int);
+  if (most < attn_mma_ws(128, 2, s->sms)) most = attn_mma_ws(128, 2, s->sms);
+  if (most < lists) most = lists;
+  if (bytes && (rc = ensure(s, s->kv, bytes < most ? most : bytes, st))) return rc;
+  const size_t ctr_most = attn_tc_ctrs(s->sms);
+  if (ctrs && (rc = ensure(s, s->ctr_kv, (ctrs < ctr_most ? ctr_most : ctrs) * sizeof(int), st, true)))
+    return rc;
   *cx = make_ctx(s, st);
   cx->ws_len = (long long)(s->kv.bytes / sizeof(float));
   cx->ctr_len = (long long)(s->ctr_kv.bytes / sizeof(int));
@@ -750,6 +772,7 @@ int dec_sync_check(void* stream) {
     if (s->ctr_side.p) cudaMemset(s->ctr_side.p, 0, s->ctr_side.bytes);
     if (s->ctr_kv.p) cudaMemset(s->ctr_kv.p, 0, s->ctr_kv.bytes);
     if (s->mb.route_ctr) cudaMemset(s->mb.route_ctr, 0, sizeof(int));
+    for (const Buf& b : s->old_zero) cudaMemset(b.p, 0, b.bytes);
     cudaMemset(s->status, 0, sizeof(words));
     cudaDeviceSynchronize();
     return (st & kStatusBoundsBit) ? DEC_EBOUNDS : DEC_ETIMEOUT;
@@ -832,6 +855,7 @@ void dec_shutdown(void) {
     b->p = nullptr;
     b->bytes = 0;
   }
+  for (const Buf& b : s.old) cudaFree(b.p);
   if (s.status) cudaFree(s.status);
   if (s.side) cudaStreamDestroy(s.side);
   if (s.ev_fork) cudaEventDestroy(s.ev_fork);

@@ -82,7 +82,7 @@ static int attention(const dec_kv_view* kv, const AttnCall& c, void* stream) {
   if (force && !std::strcmp(force, "mma") && group <= 32) tc = false;
   if (force && !std::strcmp(force, "tc")) tc = true;
   if (tc) {
-    if ((rc = kv_context(stream, attn_tc_ws(v.dim, sms), 32 * sms + 1, &cx, &ws, &ctr))) return rc;
+    if ((rc = kv_context(stream, attn_tc_ws(v.dim, sms), attn_tc_ctrs(sms), &cx, &ws, &ctr))) return rc;
     t_last_attention = DEC_REGIME_TC;
     int kernels = 0;
     const cudaError_t e = launch_attn_tc(cx, v, c, static_cast<float*>(ws), ctr, &kernels);
@@ -106,7 +106,7 @@ static int pool_of(const dec_kv_pool* pool, KvPool* p) {
   if (!al(pool->data, 16) || !al(pool->refs, 4) || !al(pool->table, 4) || !al(pool->lens, 4) ||
       !al(pool->info, 4))
     return DEC_EINVAL;
-  if (pool->pages > (1 << 19) || (int64_t)pool->width * pool->page_size > INT32_MAX)
+  if (pool->pages > kMaxPages || (int64_t)pool->width * pool->page_size > INT32_MAX)
     return DEC_EUNSUPPORTED;
   int shift = 0;
   while ((1 << shift) < pool->page_size) ++shift;

@@ -198,9 +198,10 @@ cudaError_t launch_attn_mma(const Ctx& cx, const KvView& v, int rt, const AttnCa
 bool make_tmap_heads(CUtensorMap* map, const void* q, int tokens, int heads, int dim, long long ld,
                      int box_heads, int box_tokens);
 
-// Attention for longer chunks on tcgen05; ws of attn_tc_ws bytes, ctr of 32 zero
-// ints per SM; *kernels: how many it launched.
+// Attention for longer chunks on tcgen05; ws of attn_tc_ws bytes, ctr of
+// attn_tc_ctrs zero ints; *kernels: how many it launched.
 size_t attn_tc_ws(int dim, int sms);
+constexpr size_t attn_tc_ctrs(int sms) { return 32 * (size_t)sms + 1; }
 cudaError_t launch_attn_tc(const Ctx& cx, const KvView& v, const AttnCall& c, float* ws, int* ctr,
                            int* kernels);
 
@@ -217,6 +218,8 @@ struct AppendCall {
   float eps;
 };
 cudaError_t launch_append(const Ctx& cx, const KvView& v, const AppendCall& c);
+
+constexpr int kMaxPages = 1 << 19;  // of a pool
 
 // The pages of a cache of several layers and the state of its sequences
 // (dec_kv_pool); strides and page_bytes in bytes.
@@ -245,8 +248,8 @@ cudaError_t launch_kv_copy(const Ctx& cx, const KvPool& p, const int32_t* src, c
 cudaError_t launch_kv_compact(const Ctx& cx, const KvPool& p, int* ws);
 
 // What the library keeps for the current device: its context and, for the
-// paged-cache calls, `bytes` of workspace and `ctrs` ints that are zero at
-// rest. DEC_* codes.
+// paged-cache calls, at least `bytes` of workspace and `ctrs` ints that are zero
+// at rest (0: none). DEC_* codes.
 int kv_sms();                  // SMs of the current device; 0 if it is not usable
 void count_launches(int n);    // for dec_launch_count
 int kv_context(void* stream, size_t bytes, size_t ctrs, Ctx* cx, void** ws, int** ctr);
