@@ -193,20 +193,21 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   uint64_t* q_full = o_full + 2;
   uint64_t* q_empty = q_full + 1;
   uint64_t* mma_done = q_empty + 1;
-  uint64_t* seg_full = mma_done + 1;    // [4] a drawn pair written to s_seg
+  uint64_t* seg_full = mma_done + 1;    // [4] a segment begun; a drawn pair is in s_seg
+  uint64_t* seg_empty = seg_full + 4;   // [4] a segment left by all warps but the TMA warp
   volatile int* s_flag = reinterpret_cast<volatile int*>(full + 3 * kSlots + 24);  // [0] abort
   volatile int* s_poison = s_flag + 4;  // [4] segment number + 1 with a non-finite edge value
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(const_cast<int*>(s_flag) + 8);
   int4* s_seg = reinterpret_cast<int4*>(const_cast<int*>(s_flag) + 16);  // [4] drawn pairs
-  // (four segments' worth of both: no warp is more than two segments ahead of
-  // another, as the TMA warp waits with Q for the segment before)
+  // (four segments' worth of both: the TMA warp begins a segment when all others
+  // have left the one four before, and they follow it into it)
   const SplitTables tab(s_seg + 4, a.p.batch);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);  // the MMAs done, and warp 10 past the slot
       mbar_init(&v_clean[i], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -217,7 +218,10 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(mma_done, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&seg_full[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 10);  // warps 0-7, 8 and 10
+    }
     s_flag[0] = 0;
     for (int i = 0; i < 4; ++i) s_poison[i] = 0;
     fence_mbar_init();
@@ -257,17 +261,22 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   };
 
   int drawn = 0;  // segments so far
-  // To the next segment; false once a wait has run out.
+  // To the next segment, once the TMA warp has begun it; false if a wait has run out.
   auto next = [&]() -> bool {
-    if (!draws) {
-      if (drawn++) w.next();
-      return true;
-    }
     const int k = drawn++;
     if (!wait(&seg_full[k & 3], k >> 2)) return false;
-    const int4 e = s_seg[k & 3];
-    w.jump(e.x, e.y, e.z);
+    if (draws) {
+      const int4 e = s_seg[k & 3];
+      w.jump(e.x, e.y, e.z);
+    } else if (k) {
+      w.next();
+    }
     return true;
+  };
+  // This warp is done with segment k: its entries of s_seg and s_poison are free.
+  auto leave = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[k & 3]);
   };
 
   if (warp < 8) {
@@ -281,7 +290,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     uint32_t sn = 0, on = 0;
     int seg = 0;
     bool ok = next();
-    for (; ok && w.more(); ok = ok && next(), ++seg) {
+    for (; ok && w.more(); leave(seg++), ok = ok && next()) {
       if (x == 1 && !has_b()) continue;
       const EdgeRange er = edges();
       const int qn = tab.qn[w.b];
@@ -602,16 +611,18 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       }
       const int r = k - base, up = r / a.s.hkv;
       w.jump(seq, r - up * a.s.hkv, last - up);
-      if (lane == 0) {
-        s_seg[drawn & 3] = make_int4(seq, r - up * a.s.hkv, last - up, 0);
-        mbar_arrive(&seg_full[drawn & 3]);
-      }
-      ++drawn;
-      __syncwarp();
+      if (lane == 0) s_seg[drawn & 3] = make_int4(seq, r - up * a.s.hkv, last - up, 0);
     };
     auto advance = [&] {
+      if (drawn >= 4 && !wait(&seg_empty[drawn & 3], (drawn >> 2) + 1)) {
+        ok = false;
+        return;
+      }
       if (draws) draw();
-      else next();
+      else if (drawn) w.next();
+      if (lane == 0) mbar_arrive(&seg_full[drawn & 3]);
+      ++drawn;
+      __syncwarp();
     };
     for (advance(); w.more() && ok; advance()) {
       const bool two = has_b();
@@ -699,7 +710,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
     uint32_t pa = 0, pb = 0, clean = 0;  // phases: P of A and B; edge tiles of each slot
     bool ok = next() && w.more() && wait(&full[0], 0);
 #pragma unroll 1
-    for (; ok; ok = ok && next(), ++seg) {
+    for (; ok; leave(seg++), ok = ok && next()) {
       // the segment's first Q·Kᵀ, while the output of the one before is read
       ok = w.more() && wait(q_full, seg);
       if (!ok) break;
@@ -760,16 +771,23 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
   } else if (warp == 10) {
     // ---------------------------------------------------------------- edge values
     int i = 0, seg = 0;
-    bool ok = next();
-    for (; ok && w.more(); ok = ok && next(), ++seg) {
+    // the first slot's first use has no values, but its phase has to pass too:
+    // fills may land out of order, and the slot's second would be taken for it
+    bool ok = next() && w.more() && wait(&full[0], 0);
+    if (ok && lane == 0) mbar_arrive(&empty[0]);
+    for (; ok && w.more(); leave(seg++), ok = ok && next()) {
       const EdgeRange er = edges();
       for (int k = 0; k < w.n && ok; ++k) {
         ++i;
         const int key0 = (w.j + k) * kTcKeys, st = i % kSlots;
-        // every tile is waited for, edge or not: a phase cannot be told from
-        // the one two later
+        // every tile is waited for and left, edge or not: a phase cannot be told
+        // from the one two later, so the slot must not be filled again before
         ok = wait(&full[st], i / kSlots);
-        if (!ok || !er.in(key0, kTcKeys)) continue;
+        if (!ok) break;
+        if (!er.in(key0, kTcKeys)) {
+          if (lane == 0) mbar_arrive(&empty[st]);
+          continue;
+        }
         uint8_t* v = ring + st * 2 * Sh::kTile;
         int k0, k1;
         edge_steps(er, key0, k0, k1);
@@ -814,7 +832,10 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
         if (__any_sync(~0u, found) && lane == 0) s_poison[seg & 3] = seg + 1;
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_clean[st]);
+        if (lane == 0) {
+          mbar_arrive(&v_clean[st]);
+          mbar_arrive(&empty[st]);
+        }
       }
     }
   }
