@@ -308,6 +308,8 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   const int mask = (1 << p.page_shift) - 1;
   if (tid == 0) s_mine = 0;
   griddep_launch_dependents();
+  __syncwarp();
+  cluster_arrive_all();  // this CTA's shared memory may be written by the others
   griddep_wait();
 
   auto blocks = [&](int n) { return (int)(((long long)n + mask) >> p.page_shift); };
@@ -380,6 +382,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   if (tid < a.n) s_start[tid] = start;
   block_scan(cow, s_warp, copies);
   const int before = block_scan(__popcll(run.bits), s_warp, mine);
+  cluster_wait_all();  // all CTAs of the cluster have started
   if (tid < kPoolCtas) st_dsmem_s32(&s_cnt[rank], tid, mine);
   cluster_sync_all();  // every CTA has read refs, lengths and the entries above
 
@@ -498,6 +501,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   __shared__ int s_warp[32], s_cnt[kPoolCtas];
   const uint32_t rank = cluster_rank();
   griddep_launch_dependents();
+  cluster_arrive_all();  // this CTA's shared memory may be written by the others
   griddep_wait();
   int* holes = ws + 2;
   int* movers = holes + p.pages;
@@ -505,6 +509,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   const PageRun run(p, rank, false);
   int mine;
   int before = block_scan(__popcll(run.bits), s_warp, mine);
+  cluster_wait_all();  // all CTAs of the cluster have started
   if (threadIdx.x < kPoolCtas) st_dsmem_s32(&s_cnt[rank], threadIdx.x, mine);
   cluster_sync_all();
   int n = 0;
