@@ -410,7 +410,9 @@ int kv_append(const dec_kv_view* kv, const void* qkv, int64_t ldqkv, const void*
  * Scores, maximum, sum and output are fp32; the weights enter the product with
  * the values as bf16; out is rounded once. A token that sees nothing (its
  * position is negative: kv_len below its chunk) gets out = 0, lse = -inf. What
- * lies past a sequence's end in its last page is never used, whatever it is.
+ * lies past a sequence's end in its last page is never used, whatever it is, and
+ * with a window neither are the table's entries of pages before the first token's
+ * window (a cache may have dropped them).
  * The result is the same from run to run. Rows of tokens past cu_q[batch] are
  * left alone. Uses the library's workspace: order such calls on one stream.
  */

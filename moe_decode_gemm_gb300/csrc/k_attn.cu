@@ -186,8 +186,9 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
       const int row = paged_row(a.p, w.b);
       const int32_t* trow = a.p.table + (long long)(row < 0 ? 0 : row) * a.p.table_stride;
       auto page_at = [&](int j) -> int {
+        // (pages that no row sees are not looked up: a window may have left them)
         const int pos = j * kKeys + piece * rows;
-        if (piece >= pieces || pos >= w.tr.khi) return -1;
+        if (piece >= pieces || pos >= w.tr.khi || pos + rows <= w.tr.klo) return -1;
         const int pg = __ldg(trow + (pos >> a.p.page_shift));
         // a page that does not exist reads as zeros
         if ((pg < 0 || pg >= a.p.pages) && a.p.status) atomicOr(a.p.status, kStatusBounds);

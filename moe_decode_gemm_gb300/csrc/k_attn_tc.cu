@@ -629,7 +629,11 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       const int row = paged_row(a.p, w.b);
       const int32_t* trow = a.p.table + (long long)(row < 0 ? 0 : row) * a.p.table_stride;
       // this lane's piece of tile j: its entry of the page table, then its page
-      auto has = [&](int j) { return piece < pieces && j * kTcKeys + piece * rows < w.tr.khi; };
+      // (none for a page that no row sees: a window may have left it)
+      auto has = [&](int j) {
+        const int pos = j * kTcKeys + piece * rows;
+        return piece < pieces && pos < w.tr.khi && pos + rows > w.tr.klo;
+      };
       auto entry = [&](int j) -> int {
         return has(j) ? __ldg(trow + ((j * kTcKeys + piece * rows) >> a.p.page_shift)) : -1;
       };
