@@ -241,9 +241,11 @@ const char* dec_strerror(int code);
  * dec_sync_check -- synchronise `stream` (and the library's side stream),
  * then read and clear the device status words that kernels set when a bounded
  * wait gives up: the library's own and the one in dec_linear_noalloc's fixed
- * array. Returns DEC_OK, DEC_ETIMEOUT, or DEC_ECUDA if the synchronisation
- * itself failed (DEC_EBOUNDS as described there). Allocates nothing: in a process that has only called
- * dec_linear_noalloc it sets up no workspace, stream or event.
+ * array. Returns DEC_OK, DEC_ETIMEOUT, DEC_EBOUNDS as described there, or
+ * DEC_ECUDA if the synchronisation itself failed. Where a wait gave up and a
+ * check failed it returns DEC_ETIMEOUT, and the next call DEC_EBOUNDS.
+ * Allocates nothing: in a process that has only called dec_linear_noalloc it
+ * sets up no workspace, stream or event.
  */
 int dec_sync_check(void* stream);
 

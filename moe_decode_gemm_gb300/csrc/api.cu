@@ -759,25 +759,29 @@ int dec_sync_check(void* stream) {
   if (cudaMemcpy(words, s->status, sizeof(words), cudaMemcpyDeviceToHost) != cudaSuccess)
     return DEC_ECUDA;
   const int st = words[0];
-  if (st == 0 && nst != 0) return DEC_ETIMEOUT;
+  const bool bounds = (st & kStatusBoundsBit) != 0, timeout = nst != 0 || (st & ~kStatusBoundsBit) != 0;
   if (st != 0) {
-    if (st & kStatusBoundsBit) {
+    if (bounds) {
       g_check_line = words[1];
       g_check_index = (long long)(unsigned)words[2] | ((long long)words[3] << 32);
     }
-    // Reset the status word and every arrival counter a timed-out kernel may
-    // have left behind.
-    cudaMemset(s->status, 0, sizeof(int));
-    if (s->ctr_main.p) cudaMemset(s->ctr_main.p, 0, s->ctr_main.bytes);
-    if (s->ctr_side.p) cudaMemset(s->ctr_side.p, 0, s->ctr_side.bytes);
-    if (s->ctr_kv.p) cudaMemset(s->ctr_kv.p, 0, s->ctr_kv.bytes);
-    if (s->mb.route_ctr) cudaMemset(s->mb.route_ctr, 0, sizeof(int));
-    for (const Buf& b : s->old_zero) cudaMemset(b.p, 0, b.bytes);
+    // Reset the status words, and every arrival counter that a timed-out kernel
+    // (or a failed check of a DEC_DEBUG build) may have left behind. Both a
+    // time-out and a check: the time-out is reported first, as results are
+    // missing, and the check by the next call.
+    const int left[4] = {bounds && timeout ? kStatusBoundsBit : 0, words[1], words[2], words[3]};
+    if (timeout || words[1]) {
+      if (s->ctr_main.p) cudaMemset(s->ctr_main.p, 0, s->ctr_main.bytes);
+      if (s->ctr_side.p) cudaMemset(s->ctr_side.p, 0, s->ctr_side.bytes);
+      if (s->ctr_kv.p) cudaMemset(s->ctr_kv.p, 0, s->ctr_kv.bytes);
+      if (s->mb.route_ctr) cudaMemset(s->mb.route_ctr, 0, sizeof(int));
+      for (const Buf& b : s->old_zero) cudaMemset(b.p, 0, b.bytes);
+    }
     cudaMemset(s->status, 0, sizeof(words));
+    if (left[0]) cudaMemcpy(s->status, left, sizeof(left), cudaMemcpyHostToDevice);
     cudaDeviceSynchronize();
-    return (st & kStatusBoundsBit) ? DEC_EBOUNDS : DEC_ETIMEOUT;
   }
-  return DEC_OK;
+  return timeout ? DEC_ETIMEOUT : (bounds ? DEC_EBOUNDS : DEC_OK);
 }
 
 int dec_debug_check_site(int* line, long long* index) {
