@@ -70,7 +70,7 @@ def _rows(what, h, t, dtype):
             ld, one = t.stride()
             if one == 1:
                 # a single row's stride says nothing
-                return n, width, (ld if n > 1 or ld > width else width)
+                return n, width, (ld if n > 1 else width)
     except (AttributeError, ValueError):
         pass
     _same(what, h.device, t, dtype, dims=2, row_stride=True)
