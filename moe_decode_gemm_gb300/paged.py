@@ -15,6 +15,7 @@ tables -- change from step to step on the device.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 from . import REGIME_NAMES, _check, lib
 
@@ -102,6 +103,14 @@ class _Handle:
         return self._current(self._index) if stream is None else stream.cuda_stream
 
 
+def _int32(what, n):
+    """An integer that the C ABI's 32 bits hold (ctypes would cut it to them)."""
+    n = operator.index(n)
+    if not -(1 << 31) <= n < 1 << 31:
+        raise ValueError("%s: %d does not fit 32 bits" % (what, n))
+    return n
+
+
 def _row_stride(t):
     """Elements between rows (a single row's stride says nothing)."""
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
@@ -147,7 +156,7 @@ class PagedKV(_Handle):
             cache.data_ptr(), cache.stride(0) if pages > 1 else page, pages, self.heads,
             self.page_size, self.dim, table.data_ptr(), _row_stride(table), table.shape[1],
             table.shape[0], None if rows is None else rows.data_ptr(), cu_q.data_ptr(),
-            kv_len.data_ptr(), cu_q.shape[0] - 1, int(max_q))
+            kv_len.data_ptr(), cu_q.shape[0] - 1, _int32("max_q", int(max_q)))
         self._ref = ctypes.byref(self._view)
 
     @property
@@ -156,7 +165,7 @@ class PagedKV(_Handle):
 
     @max_q.setter
     def max_q(self, n):
-        self._view.max_q = int(n)
+        self._view.max_q = _int32("max_q", int(n))
 
 
 class KVPool(_Handle):
@@ -198,7 +207,7 @@ class KVPool(_Handle):
         self._pool = _Pool(
             data.data_ptr(), data.stride(0) * size if layers > 1 else page,
             data.stride(1) * size if pages > 1 else page, page, layers, pages,
-            int(data.shape[-2] if page_size is None else page_size), refs.data_ptr(),
+            _int32("page_size", int(data.shape[-2] if page_size is None else page_size)), refs.data_ptr(),
             table.data_ptr(), _row_stride(table), table.shape[1], lens.data_ptr(), table.shape[0],
             None if info is None else info.data_ptr())
         self._ref = ctypes.byref(self._pool)
@@ -279,7 +288,8 @@ def kv_attention(q, kv, out=None, lse=None, scale=None, window=0, stream=None):
         lsep = lse.data_ptr()
     if T:
         rc = lib().kv_attention(kv._ref, q.data_ptr(), ldq, out.data_ptr(), ldo, lsep, T, hq,
-                                dim ** -0.5 if scale is None else scale, window,
+                                dim ** -0.5 if scale is None else scale,
+                                window and _int32("window", window),
                                 kv._stream(stream))
         if rc:
             _check(rc, "kv_attention")
