@@ -362,7 +362,7 @@ typedef struct dec_kv_view {
   int32_t page_size, dim;  /* 16, 32, 64, 128 or 256 positions; 64 or 128 elements of a head */
   const int32_t* table;    /* device [table_rows][table_stride] */
   int64_t table_stride;    /* elements from one row to the next */
-  int32_t width;           /* entries of a row */
+  int32_t width;           /* entries of a row; width * page_size at most 2^31 - 256 */
   int32_t table_rows;      /* rows of table, and entries of kv_len */
   const int32_t* rows;     /* device [batch]: the row (and kv_len entry) of each sequence of the
                               batch; NULL: sequence b has row b */

@@ -9,6 +9,9 @@
 
 namespace dg {
 
+// Positions of a table row: the end of a key tile past the last is still 32 bits.
+constexpr int64_t kMaxPositions = INT32_MAX - 255;
+
 static thread_local int t_last_attention = DEC_REGIME_NONE;
 
 static bool al(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -34,7 +37,7 @@ static int view_of(const dec_kv_view* kv, KvView* v) {
     return DEC_EINVAL;
   if (kv->page_size & (kv->page_size - 1)) return DEC_EINVAL;
   if (kv->page_size < 16 || kv->page_size > 256 || (kv->dim != 64 && kv->dim != 128) ||
-      kv->batch > 1024 || (int64_t)kv->width * kv->page_size > INT32_MAX)
+      kv->batch > 1024 || (int64_t)kv->width * kv->page_size > kMaxPositions)
     return DEC_EUNSUPPORTED;
   *v = {kv->cache, kv->page_stride, kv->pages,  kv->heads,      kv->page_size, kv->dim, kv->table,
         kv->table_stride, kv->width, kv->table_rows, kv->rows, kv->cu_q, kv->kv_len, kv->batch};

@@ -112,7 +112,7 @@ __device__ __noinline__ void add_edge_values(const PagedArgs& p, int window, int
                                              const EdgeRange& er, int pos, int j, int n, int rank,
                                              int step, int r, int d, float* scratch) {
   for (int k = rank; k < n; k += step)
-    edge_values<D>(p, paged_row(p, b), h, er, window > 0 ? pos - window + 1 : 0, pos, (j + k) * KEYS,
+    edge_values<D>(p, paged_row(p, b), h, er, first_seen(window, pos), pos, (j + k) * KEYS,
                    (j + k + 1) * KEYS, d, [&](const uint16_t* e, int key) {
                      const int row = ((r >> 4) * KS + key % KEYS / BLK) * 16 + (r & 15);
                      float* o = scratch + row * (D + 8) + d;
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT, CL>::kThreads, 1)
       const uint16_t* src = a.q + (long long)(q0 + t0 + t) * a.ldq +
                             (long long)(w.h * a.group + (live ? r - t * a.group : 0)) * D;
       hi[e] = live ? pos0 + t : -1;
-      lo[e] = live && a.s.window > 0 ? pos0 + t - a.s.window + 1 : 0;
+      lo[e] = live ? first_seen(a.s.window, pos0 + t) : 0;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         qf[kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + c0)) : 0u;

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kTcAttnThreads, 1)
       const bool live = t < nt;
       const int pos = tab.kv[w.b] - qn + t0 + t;
       const int hi = live ? pos : -1;
-      const int lo = live && a.s.window > 0 ? pos - a.s.window + 1 : 0;
+      const int lo = live ? first_seen(a.s.window, pos) : 0;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < w.n; ++k) {
         const int key0 = (w.j + k) * kTcKeys;

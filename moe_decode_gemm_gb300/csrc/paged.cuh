@@ -87,6 +87,12 @@ __device__ __forceinline__ int paged_first(const PagedArgs& p, int b) {
   return a < 0 ? 0 : (a > p.tokens ? p.tokens : a);
 }
 
+// First position that a token at position pos sees. (pos may be negative, and
+// window anything up to 2^31 - 1.)
+__device__ __forceinline__ int first_seen(int window, int pos) {
+  return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+
 // ------------------------------------------------------------------ the split
 struct SplitShape {
   int tq;        // tokens of a row tile
@@ -109,11 +115,7 @@ __device__ __forceinline__ TileRange tile_range(const SplitShape& s, int qn, int
   const int t1 = t0 + s.tq < qn ? t0 + s.tq : qn;
   r.khi = kv - qn + t1;
   if (r.khi < 0) r.khi = 0;
-  r.klo = 0;
-  if (s.window > 0) {
-    const int lo = kv - qn + t0 - s.window + 1;
-    if (lo > 0) r.klo = lo;
-  }
+  r.klo = first_seen(s.window, kv - qn + t0);
   r.j0 = r.klo >> s.bn_shift;
   r.n = ((r.khi + (1 << s.bn_shift) - 1) >> s.bn_shift) - r.j0;
   if (r.n < 1) r.n = 1;
@@ -130,7 +132,7 @@ struct EdgeRange {
 // pos0: position of the tile's first of nt tokens
 __device__ __forceinline__ EdgeRange edge_range(const SplitShape& s, const TileRange& r, int pos0,
                                                 int nt) {
-  return EdgeRange{r.klo, r.khi, s.window > 0 ? pos0 + nt - s.window : 0, pos0 + 1};
+  return EdgeRange{r.klo, r.khi, first_seen(s.window, pos0 + nt - 1), pos0 + 1};
 }
 
 // A value of a key tile at the edge must not reach the sums of rows that do
