@@ -56,7 +56,8 @@ extern "C" {
 /* Error codes. */
 #define DEC_OK            0
 #define DEC_EINVAL       -1  /* NULL required pointer, bad size, misaligned pointer, K % 8 != 0 */
-#define DEC_EUNSUPPORTED -2  /* outside the decode envelope: M > 64, topk > 32 or > E, E > 1024 */
+#define DEC_EUNSUPPORTED -2  /* outside the decode envelope: M > 64, topk > 32 or > E, E > 1024 (the
+                                paged cache's limits: see dec_kv_view and its calls) */
 #define DEC_ECUDA        -3  /* a CUDA runtime call or a launch failed */
 #define DEC_ETIMEOUT     -4  /* a bounded device-side wait gave up */
 #define DEC_ENOMEM       -5  /* the workspace could not be allocated */
@@ -370,7 +371,8 @@ typedef struct dec_kv_view {
   const int32_t* kv_len;   /* device [table_rows]: positions, the new tokens included */
   int32_t batch;           /* 1 .. 1024 sequences; some may have no new token */
   int32_t max_q;           /* the most new tokens of one sequence, as far as the caller knows: it
-                              chooses the kernel, not the result. 0: unknown */
+                              chooses the kernel, not the result. 0: unknown, taken as all of
+                              the call's tokens (slower for a batch of short steps) */
 } dec_kv_view;
 
 /*

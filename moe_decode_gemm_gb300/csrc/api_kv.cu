@@ -73,6 +73,10 @@ static int attention(const dec_kv_view* kv, const AttnCall& c, void* stream) {
   //   126 rows, 1 sequence of 4 key heads of 128   9/12  14/17  20/26  30/27
   //   128 rows, 1 sequence of 8 key heads of 64    8/10  10/14  16/21  22/26
   //   128 rows, 8 sequences of them               13/9   19/13  30/22  70/42
+  //   120 rows, 1 sequence of 8 key heads of 128  10/13  14/18  21/27  35/28
+  // From 65 rows on that is up to about 20 row tiles of 128 columns, or 40 of 64,
+  // a little more than the clusters take. (The last line has 32 and goes to
+  // tcgen05: slower below some 4096 positions, faster above.)
   const int64_t longest = kv->max_q > 0 ? kv->max_q : c.tokens, rows = longest * group;
   bool tc = rows > 32;
   if (tc && group <= 32 && rows <= 128) {

@@ -26,13 +26,20 @@
 // that the others' weight 0 would turn into NaN: both become 0 in shared
 // memory, and the rows that do see a non-finite value get it added at the end.
 //
+// Every ring has a way back: a slot is filled again when the MMAs that read it
+// are done and warp 10 is past it, a segment begins when all warps have left the
+// one four before, and all follow the TMA warp into it. So no role, however
+// late, can take a barrier's phase for the one two before.
+//
 // The work is split into equal ranges of (row tile pair, key tile) units, or
 // drawn pair by pair where there are many, see paged.cuh.
 //
 // Measured (56 query and 4 key heads of 128): a chunk of 512 tokens over 32k
-// positions 290 us, 1.65 PFLOP/s or 87% of what a large matrix product reaches; a
-// key tile of a pair takes 1.4 us, the two halves' softmax (1.1 us each) and
-// products (0.6 us each) in turn. Four ragged prompts of up to 2047 tokens 148 us,
+// positions 291 us, 1.64 PFLOP/s or 87% of what a large matrix product reaches
+// (in a graph, at the highest clock; called in a row for long, under the power
+// cap, 313 to 318 us, 1.5 PFLOP/s or 80%); a key tile of a pair takes 1.4 us,
+// the two halves' softmax (1.1 us each) and products (0.6 us each) in turn.
+// Four ragged prompts of up to 2047 tokens 148 us,
 // 1.13 PFLOP/s: pairs of 1 to 16 key tiles, each with 2.5 us for its edge, its
 // output and the first scores of the next. Calls of a few pairs 15 to 18 us,
 // latency: 3 us until the work is split, 2.5 until the first scores, then the

@@ -25,9 +25,12 @@ namespace dg {
 // and angles, took twice the instructions and were bound by them: 80 us for
 // 7.9k tokens of 64 heads of 128.)
 //
-// Measured: those 7.9k tokens, half of each head rotated, 262 MB in 48 us =
-// 5.5 TB/s, 81% of a copy's rate, instructions and memory about even; one token
-// 2.5 us, 64 tokens 3.2 us.
+// Measured: those 7.9k tokens, half of each head rotated, 262 MB in 49 us =
+// 5.3 TB/s, 79% of a copy's rate, instructions and memory about even; one token
+// 2.5 us, 64 tokens 3.3 us. Four loads in flight to a lane need 64 heads of 128
+// (128 of 64) to a token; with fewer a CTA's lanes are that much emptier: 24 + 16
+// heads of 128, 2793 tokens, 14.9 us (8.5 at a copy's rate), 32 + 16 of 64, 7153
+// tokens, 28.7 (13.0).
 constexpr int kAppendThreads = 256;
 
 struct AppendArgs {
@@ -465,7 +468,9 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   // A cut sequence's copies of pages that others hold are few, mostly none:
   // this cluster makes them itself, where a second kernel would cost every
   // call 2 us and its launch. A fork copies a page for most of its sequences:
-  // that takes the whole device.
+  // that takes the whole device. Measured, pages of 128 KB a layer, us beyond a
+  // call without copies (and what their bytes take): 1 / 8 / 64 pages of 4 layers
+  // 3 / 14 / 90 (0.2 / 1.2 / 10), of 60 layers 23 / 166 / 1285 (2.3 / 18 / 148).
   if (!FORK && copies && !lacking) {
     cluster_sync_all();
     copy_pages<kPoolThreads>(p, a.n, [&](int i, int& s, int& d) {

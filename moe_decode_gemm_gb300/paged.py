@@ -123,8 +123,11 @@ class PagedKV(_Handle):
     than their size); table [rows, width] int32; cu_q [batch+1] int32; kv_len
     [rows] int32, the new tokens included; rows: optional [batch] int32, the
     table row of each sequence of the batch (default: row b for sequence b).
-    max_q: the most new tokens of one sequence as far as the caller knows (it
-    chooses the kernel); it may be set anew between calls.
+    max_q: the most new tokens of one sequence as far as the caller knows; it may
+    be set anew between calls. It chooses the kernel, not the result: give 1 for
+    a step of one token a sequence, as 0 (unknown) is taken as all of the call's
+    tokens and sends such a step to the kernel for chunks (8 sequences over 2000
+    positions 28 us instead of 14, 64 over 4000 102 instead of 86).
     """
 
     def __init__(self, cache, table, cu_q, kv_len, rows=None, max_q=0):
