@@ -478,6 +478,81 @@ int kv_copy(const dec_kv_pool* pool, const int32_t* src, const int32_t* dst, int
  * past n go, in order, to the free places before n; table and refs follow. */
 int kv_compact(const dec_kv_pool* pool, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The norm of the residual stream, and projections with 4-bit weights: the
+ * library's own calls, as the paged cache's are. Numbers in 4 and 8 bits come in
+ * blocks of 32 with a shared power of two (the OCP microscaling formats MXFP4 and
+ * MXFP8): a scale byte b stands for 2^(b - 127), 255 for NaN.
+ *
+ * dec_rmsnorm -- y = h * rsqrt(mean(h^2) + eps) * w over each row, with
+ * h = bf16(x + res), or h = x when res is NULL.
+ *
+ *   x, res, h, y : [rows, H] bf16, rows ldx, ldres, ldh, ldy elements apart (each at
+ *          least H and a multiple of 8); h is written with res only
+ *   w    : [H] bf16;  H a multiple of 8, at most 65536;  eps >= 0
+ *
+ * The sum of squares is that of the rounded h, in fp32; y is fp32 rounded once.
+ * h may be x or res, and y may be x or res, with the same row stride (y not h).
+ * Otherwise outputs overlap nothing. Errors: DEC_EINVAL, DEC_EUNSUPPORTED (H),
+ * DEC_ECUDA.
+ *
+ * dec_rmsnorm_mx -- the same y in 8 bits: q [rows, H] e4m3 (rows ldq apart, a
+ * multiple of 16) and scales [rows, H/32] bytes (rows ldscales apart); H a multiple
+ * of 32. For each 32 values with largest magnitude a the scale is 2^e with
+ * e = ceil(log2(a / 448)), at least -127 (for a = 0 too), and q = e4m3(y / 2^e), to
+ * nearest even. A group with a value that is not finite: scale 255, q NaN.
+ */
+int dec_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, float eps,
+                void* h, int64_t ldh, void* y, int64_t ldy, int rows, int H, void* stream);
+int dec_rmsnorm_mx(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, float eps,
+                   void* h, int64_t ldh, void* q, int64_t ldq, void* scales, int64_t ldscales, int rows,
+                   int H, void* stream);
+
+/*
+ * 4-bit weights [N, K]: W[n][k] = v(code) * 2^(b - 127), b the scale byte of k's 32
+ * (aligned) k; a code has its sign in bit 3 and v = 0, .5, 1, 1.5, 2, 3, 4, 6 by
+ * its low bits. They lie in units of 128 rows x 128 k:
+ *   q      : [ceil(N/128)][ceil(K/128)][128 rows][64 bytes], 128-byte aligned; element
+ *            2i of a row's 128 k in the low half of byte i
+ *   scales : [ceil(N/128)][ceil(K/128)][32][4][4], 16-byte aligned: row n, group g of
+ *            the unit's four at [n % 32][n % 128 / 32][g]
+ * Codes past K are 0. What lies past N is read and has no effect.
+ *
+ * dec_quant_w4 -- bf16 weights W [N, K] (rows ldw elements apart, a multiple of 8;
+ * K a multiple of 8) in that form, what lies past N and K included (codes 0). For
+ * each 32 with largest magnitude a: 2^e with e = ceil(log2(a / 6)), at least -127 (for
+ * a = 0 too), codes to nearest, ties to the even code. A group with a value that is
+ * not finite: scale 255, codes 0.
+ */
+int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K, void* stream);
+
+/*
+ * dec_linear_w4 -- y = bf16(x·Wᵀ), or bf16(res + x·Wᵀ) when res is not NULL.
+ *
+ *   x    : [M, K] bf16, rows ldx elements apart (at least K, a multiple of 8);
+ *          1 <= M <= 64, K a multiple of 8
+ *   res, y : [M, N] bf16; y may be res
+ *
+ * The tensor cores take 4-bit weights with 8-bit tokens. A bf16 token value enters
+ * as the sum of two e4m3 numbers, each with a scale for 32 k: exact down to 2^-15
+ * of the largest magnitude of its 32, off by at most 2^-22 of that magnitude below.
+ * Products are exact, sums fp32, in an order that does not change from run to
+ * run; y is rounded once. A token with a value that is not finite gives NaN in
+ * all its outputs. W is read before the previous kernel of the stream has finished:
+ * as with dec_linear, that kernel must not be one of this library's that writes it
+ * (dec_quant_w4 is safe: nothing starts before it has ended).
+ * Errors: DEC_EINVAL, DEC_EUNSUPPORTED (M > 64, or 2^24 units or more), DEC_ECUDA.
+ *
+ * dec_linear_w4_mx -- the same for tokens in 8 bits: x [M, K] e4m3, rows ldx bytes
+ * apart (a multiple of 16), xscales [M, K/32] bytes, rows ldxscales apart; K a
+ * multiple of 32. The tokens' values are taken as they are.
+ */
+int dec_linear_w4(const void* x, int64_t ldx, const void* wq, const void* wscales, const void* res,
+                  void* y, int M, int N, int K, void* stream);
+int dec_linear_w4_mx(const void* x, int64_t ldx, const void* xscales, int64_t ldxscales, const void* wq,
+                     const void* wscales, const void* res, void* y, int M, int N, int K, void* stream);
+
 /* dec_shutdown -- free the workspace, side stream and events of the current device. */
 void dec_shutdown(void);
 

@@ -36,7 +36,7 @@ EXPORTS = [
     "dec_launch_count", "dec_probe_begin", "dec_probe_end", "dec_shutdown", "dec_version",
     "dec_linear_noalloc", "dec_debug_build", "dec_debug_check_site",
     "kv_append", "kv_attention", "kv_last_attention", "kv_resize", "kv_free", "kv_fork", "kv_copy",
-    "kv_compact",
+    "kv_compact", "dec_rmsnorm", "dec_rmsnorm_mx", "dec_linear_w4", "dec_linear_w4_mx", "dec_quant_w4",
 ]
 
 _lib = None
@@ -110,6 +110,11 @@ def _configure(L):
         "kv_fork": (I, [P, P, P, I, P]),
         "kv_copy": (I, [P, P, P, I, P]),
         "kv_compact": (I, [P, P]),
+        "dec_rmsnorm": (I, [P, LL, P, LL, P, F, P, LL, P, LL, I, I, P]),
+        "dec_rmsnorm_mx": (I, [P, LL, P, LL, P, F, P, LL, P, LL, P, LL, I, I, P]),
+        "dec_linear_w4": (I, [P, LL, P, P, P, P, I, I, I, P]),
+        "dec_linear_w4_mx": (I, [P, LL, P, LL, P, P, P, P, I, I, I, P]),
+        "dec_quant_w4": (I, [P, LL, P, P, I, I, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -430,3 +435,4 @@ PROBE_EXPERT_W13, PROBE_EXPERT_W2, PROBE_LINEAR, PROBE_ROUTER, PROBE_COMBINE = 0
 
 from .paged import (KVPool, PagedKV, kv_append, kv_attention, kv_compact, kv_copy,  # noqa: E402
                     kv_fork, kv_free, kv_resize, last_attention)
+from .w4 import (MX8, W4, dec_linear_w4, dec_quant_w4, dec_rmsnorm, dec_rmsnorm_mx)  # noqa: E402

@@ -24,7 +24,7 @@ DEBUG_LIB = os.path.join(HERE, "libdecgemm_debug.so")
 ROOT = os.path.dirname(HERE)
 
 SOURCES = ["api.cu", "api_kv.cu", "k_linear.cu", "k_moe.cu", "k_tc.cu", "k_gemv.cu", "k_noalloc.cu",
-           "k_kv.cu", "k_attn.cu", "k_attn_tc.cu"]
+           "k_kv.cu", "k_attn.cu", "k_attn_tc.cu", "api_w4.cu", "k_w4.cu", "k_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

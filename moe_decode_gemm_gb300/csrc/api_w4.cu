@@ -1,0 +1,85 @@
+// api_w4.cu -- the C ABI of the norm and of the projections with 4-bit weights:
+// argument checks.
+#include <cmath>
+
+#include "../../include/decgemm.h"
+#include "launch.h"
+
+namespace dg {
+
+static bool al(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+static int result(cudaError_t e) {
+  if (e != cudaSuccess) return DEC_ECUDA;
+  count_launches(1);
+  return DEC_OK;
+}
+
+static int norm(NormCall c, void* stream) {
+  if (!c.x || !c.w || (!c.y && !c.q) || (c.res && !c.h)) return DEC_EINVAL;
+  if (c.rows < 1 || c.H < 8 || c.H % (c.q ? 32 : 8) || !std::isfinite(c.eps) || c.eps < 0.f)
+    return DEC_EINVAL;
+  const void* ptrs[] = {c.x, c.res, c.w, c.h, c.y, c.q};
+  for (const void* p : ptrs)
+    if (!al(p, 16)) return DEC_EINVAL;
+  if (c.ldx < c.H || c.ldx % 8 || (c.res && (c.ldres < c.H || c.ldres % 8 || c.ldh < c.H || c.ldh % 8)))
+    return DEC_EINVAL;
+  if (c.y && (c.ldy < c.H || c.ldy % 8 || c.y == c.h)) return DEC_EINVAL;
+  if (c.q && (!c.sc || c.ldq < c.H || c.ldq % 16 || c.ldsc < c.H / 32)) return DEC_EINVAL;
+  if (c.H > kNormMaxWidth) return DEC_EUNSUPPORTED;
+  Ctx cx;
+  if (int rc = kv_context(stream, 0, 0, &cx, nullptr, nullptr)) return rc;
+  return result(launch_norm(cx, c));
+}
+
+static int linear(const W4Call& c, void* stream) {
+  if (!c.x || !c.wq || !c.ws || !c.y) return DEC_EINVAL;
+  if (c.M < 1 || c.N < 1 || c.K < 8 || c.K % (c.xs ? 32 : 8)) return DEC_EINVAL;
+  if (c.ldx < c.K || c.ldx % (c.xs ? 16 : 8) || (c.xs && c.ldxs < c.K / 32)) return DEC_EINVAL;
+  if (!al(c.x, 16) || !al(c.wq, 128) || !al(c.ws, 16) || !al(c.res, 16) || !al(c.y, 16)) return DEC_EINVAL;
+  if (c.M > 64 || !w4_fits(c.N, c.K)) return DEC_EUNSUPPORTED;
+  Ctx cx;
+  if (int rc = kv_context(stream, 0, 0, &cx, nullptr, nullptr)) return rc;
+  return result(launch_w4_linear(cx, c));
+}
+
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+int dec_rmsnorm(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, float eps,
+                void* h, int64_t ldh, void* y, int64_t ldy, int rows, int H, void* stream) {
+  if (!y) return DEC_EINVAL;
+  return norm({x, res, w, h, y, nullptr, nullptr, ldx, ldres, ldh, ldy, 0, 0, rows, H, eps}, stream);
+}
+
+int dec_rmsnorm_mx(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w, float eps,
+                   void* h, int64_t ldh, void* q, int64_t ldq, void* scales, int64_t ldscales, int rows,
+                   int H, void* stream) {
+  if (!q) return DEC_EINVAL;
+  return norm({x, res, w, h, nullptr, q, scales, ldx, ldres, ldh, 0, ldq, ldscales, rows, H, eps}, stream);
+}
+
+int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K, void* stream) {
+  if (!W || !q || !scales || N < 1 || K < 8 || K % 8 || ldw < K || ldw % 8) return DEC_EINVAL;
+  if (!al(W, 16) || !al(q, 128) || !al(scales, 16)) return DEC_EINVAL;
+  if (!w4_fits(N, K)) return DEC_EUNSUPPORTED;
+  Ctx cx;
+  if (int rc = kv_context(stream, 0, 0, &cx, nullptr, nullptr)) return rc;
+  return result(launch_w4_quant(cx, W, ldw, q, scales, N, K));
+}
+
+int dec_linear_w4(const void* x, int64_t ldx, const void* wq, const void* wscales, const void* res,
+                  void* y, int M, int N, int K, void* stream) {
+  return linear({x, nullptr, wq, wscales, res, y, ldx, 0, M, N, K}, stream);
+}
+
+int dec_linear_w4_mx(const void* x, int64_t ldx, const void* xscales, int64_t ldxscales, const void* wq,
+                     const void* wscales, const void* res, void* y, int M, int N, int K, void* stream) {
+  if (!xscales) return DEC_EINVAL;
+  return linear({x, xscales, wq, wscales, res, y, ldx, ldxscales, M, N, K}, stream);
+}
+
+}  // extern "C"

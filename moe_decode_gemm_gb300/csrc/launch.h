@@ -247,6 +247,40 @@ cudaError_t launch_kv_copy(const Ctx& cx, const KvPool& p, const int32_t* src, c
 // ws: 3 * pages + 2 ints.
 cudaError_t launch_kv_compact(const Ctx& cx, const KvPool& p, int* ws);
 
+// ------------------------------------------------------------------ 4-bit weights
+// Tensor map of packed 4-bit weights, units of 128 rows of 128 (64 bytes each) one
+// after the other, read in boxes of a unit; 16 numbers of 8 bytes land in each 16
+// bytes of shared memory, 128-byte swizzle. Returns false on failure.
+bool make_tmap_w4(CUtensorMap* map, const void* q, uint64_t rows);
+
+// Whether the units of N x K weights can be named by 32 bits.
+inline bool w4_fits(int N, int K) {
+  return ((int64_t)N + 127) / 128 * (((int64_t)K + 127) / 128) <= (INT32_MAX / 128);
+}
+
+struct W4Call {
+  const void* x;            // bf16 tokens, or e4m3 ones where xs is given
+  const void* xs;
+  const void* wq;
+  const void* ws;
+  const void* res;
+  void* y;
+  long long ldx, ldxs;
+  int M, N, K;
+};
+cudaError_t launch_w4_linear(const Ctx& cx, const W4Call& c);
+cudaError_t launch_w4_quant(const Ctx& cx, const void* W, long long ldw, void* q, void* s, int N, int K);
+
+constexpr int kNormMaxWidth = 65536;
+struct NormCall {
+  const void *x, *res, *w;
+  void *h, *y, *q, *sc;     // y, or q and sc
+  long long ldx, ldres, ldh, ldy, ldq, ldsc;
+  int rows, H;
+  float eps;
+};
+cudaError_t launch_norm(const Ctx& cx, const NormCall& c);
+
 // What the library keeps for the current device: its context and, for the
 // paged-cache calls, at least `bytes` of workspace and `ctrs` ints that are zero
 // at rest (0: none). DEC_* codes.
