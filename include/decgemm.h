@@ -549,7 +549,8 @@ int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K
  * multiple of 32. The tokens' values are taken as they are.
  */
 int dec_linear_w4(const void* x, int64_t ldx, const void* wq, const void* wscales, const void* res,
-                  void* y, int M, int N, int K, void* stream);
+                  void* y, int M, int N, int K, void* work, void* stream);
+size_t dec_linear_w4_work(int M, int K);
 int dec_linear_w4_mx(const void* x, int64_t ldx, const void* xscales, int64_t ldxscales, const void* wq,
                      const void* wscales, const void* res, void* y, int M, int N, int K, void* stream);
 

@@ -36,7 +36,7 @@ EXPORTS = [
     "dec_launch_count", "dec_probe_begin", "dec_probe_end", "dec_shutdown", "dec_version",
     "dec_linear_noalloc", "dec_debug_build", "dec_debug_check_site",
     "kv_append", "kv_attention", "kv_last_attention", "kv_resize", "kv_free", "kv_fork", "kv_copy",
-    "kv_compact", "dec_rmsnorm", "dec_rmsnorm_mx", "dec_linear_w4", "dec_linear_w4_mx", "dec_quant_w4",
+    "kv_compact", "dec_rmsnorm", "dec_rmsnorm_mx", "dec_linear_w4", "dec_linear_w4_work", "dec_linear_w4_mx", "dec_quant_w4",
 ]
 
 _lib = None
@@ -112,7 +112,8 @@ def _configure(L):
         "kv_compact": (I, [P, P]),
         "dec_rmsnorm": (I, [P, LL, P, LL, P, F, P, LL, P, LL, I, I, P]),
         "dec_rmsnorm_mx": (I, [P, LL, P, LL, P, F, P, LL, P, LL, P, LL, I, I, P]),
-        "dec_linear_w4": (I, [P, LL, P, P, P, P, I, I, I, P]),
+        "dec_linear_w4": (I, [P, LL, P, P, P, P, I, I, I, P, P]),
+        "dec_linear_w4_work": (SZ, [I, I]),
         "dec_linear_w4_mx": (I, [P, LL, P, LL, P, P, P, P, I, I, I, P]),
         "dec_quant_w4": (I, [P, LL, P, P, I, I, P]),
     }

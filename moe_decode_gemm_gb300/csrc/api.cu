@@ -98,15 +98,28 @@ bool make_tmap_heads(CUtensorMap* map, const void* q, int tokens, int heads, int
   return r == CUDA_SUCCESS;
 }
 
-bool make_tmap_w4(CUtensorMap* map, const void* q, uint64_t rows) {
+bool make_tmap_w4(CUtensorMap* map, const void* q, uint64_t rows, uint32_t box_rows) {
   if (!load_encode() || rows == 0) return false;
   cuuint64_t dims[2] = {128, rows};
   cuuint64_t strides[1] = {64};
-  cuuint32_t box[2] = {128, 128};
+  cuuint32_t box[2] = {128, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(q), dims, strides,
                         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_bytes(CUtensorMap* map, const void* x, uint64_t rows, uint64_t cols, uint64_t ld,
+                     uint32_t box_rows) {
+  if (!load_encode() || rows == 0 || cols == 0) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(x), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -9,9 +9,9 @@ namespace dg {
 
 static bool al(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-static int result(cudaError_t e) {
+static int result(cudaError_t e, int launches = 1) {
   if (e != cudaSuccess) return DEC_ECUDA;
-  count_launches(1);
+  count_launches(launches);
   return DEC_OK;
 }
 
@@ -38,9 +38,11 @@ static int linear(const W4Call& c, void* stream) {
   if (c.ldx < c.K || c.ldx % (c.xs ? 16 : 8) || (c.xs && c.ldxs < c.K / 32)) return DEC_EINVAL;
   if (!al(c.x, 16) || !al(c.wq, 128) || !al(c.ws, 16) || !al(c.res, 16) || !al(c.y, 16)) return DEC_EINVAL;
   if (c.M > 64 || !w4_fits(c.N, c.K)) return DEC_EUNSUPPORTED;
+  const bool work = !c.xs && w4_work_bytes(c.M, c.K) > 0;
+  if (work && (!c.work || !al(c.work, 16))) return DEC_EINVAL;
   Ctx cx;
   if (int rc = kv_context(stream, 0, 0, &cx, nullptr, nullptr)) return rc;
-  return result(launch_w4_linear(cx, c));
+  return result(launch_w4_linear(cx, c), work ? 2 : 1);
 }
 
 }  // namespace dg
@@ -71,15 +73,17 @@ int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K
   return result(launch_w4_quant(cx, W, ldw, q, scales, N, K));
 }
 
+size_t dec_linear_w4_work(int M, int K) { return M < 1 || M > 64 || K < 1 ? 0 : w4_work_bytes(M, K); }
+
 int dec_linear_w4(const void* x, int64_t ldx, const void* wq, const void* wscales, const void* res,
-                  void* y, int M, int N, int K, void* stream) {
-  return linear({x, nullptr, wq, wscales, res, y, ldx, 0, M, N, K}, stream);
+                  void* y, int M, int N, int K, void* work, void* stream) {
+  return linear({x, nullptr, wq, wscales, res, y, ldx, 0, M, N, K, work}, stream);
 }
 
 int dec_linear_w4_mx(const void* x, int64_t ldx, const void* xscales, int64_t ldxscales, const void* wq,
                      const void* wscales, const void* res, void* y, int M, int N, int K, void* stream) {
   if (!xscales) return DEC_EINVAL;
-  return linear({x, xscales, wq, wscales, res, y, ldx, ldxscales, M, N, K}, stream);
+  return linear({x, xscales, wq, wscales, res, y, ldx, ldxscales, M, N, K, nullptr}, stream);
 }
 
 }  // extern "C"

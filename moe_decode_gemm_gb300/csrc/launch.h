@@ -251,7 +251,13 @@ cudaError_t launch_kv_compact(const Ctx& cx, const KvPool& p, int* ws);
 // Tensor map of packed 4-bit weights, units of 128 rows of 128 (64 bytes each) one
 // after the other, read in boxes of a unit; 16 numbers of 8 bytes land in each 16
 // bytes of shared memory, 128-byte swizzle. Returns false on failure.
-bool make_tmap_w4(CUtensorMap* map, const void* q, uint64_t rows);
+bool make_tmap_w4(CUtensorMap* map, const void* q, uint64_t rows, uint32_t box_rows);
+
+// Tensor map of 8-bit numbers [rows, cols], rows ld bytes apart (a multiple of 16),
+// read in boxes of 128 columns x box_rows rows, 128-byte swizzle; what lies outside
+// reads as 0. Returns false on failure.
+bool make_tmap_bytes(CUtensorMap* map, const void* x, uint64_t rows, uint64_t cols, uint64_t ld,
+                     uint32_t box_rows);
 
 // Whether the units of N x K weights can be named by 32 bits.
 inline bool w4_fits(int N, int K) {
@@ -267,7 +273,9 @@ struct W4Call {
   void* y;
   long long ldx, ldxs;
   int M, N, K;
+  void* work;               // w4_work_bytes(M, K) bytes for bf16 tokens
 };
+size_t w4_work_bytes(int M, int K);
 cudaError_t launch_w4_linear(const Ctx& cx, const W4Call& c);
 cudaError_t launch_w4_quant(const Ctx& cx, const void* W, long long ldw, void* q, void* s, int N, int K);
 

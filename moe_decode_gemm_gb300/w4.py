@@ -29,7 +29,7 @@ def _bound(index):
 
         h = _Handle()
         h._bind(torch.device("cuda", index))
-        h._f8, h._e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+        h._f8, h._e8, h._u8 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8
         h._getdev, h._guard = torch._C._cuda_getDevice, torch.cuda.device
         _handles[index] = h
     return h
@@ -328,8 +328,16 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
             _call(b, "dec_linear_w4", lib().dec_linear_w4_mx,
                   (*x._args, *W._args, rp, y.data_ptr(), M, N, K), stream)
         else:
-            _call(b, "dec_linear_w4", lib().dec_linear_w4,
-                  (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K), stream)
+            L, wp = lib(), None
+            if M > 16:
+                n = L.dec_linear_w4_work(M, K)
+                if n:
+                    work = b._empty(n, dtype=b._u8, device=b.device)
+                    if stream is not None:
+                        work.record_stream(stream)
+                    wp = work.data_ptr()
+            _call(b, "dec_linear_w4", L.dec_linear_w4,
+                  (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K, wp), stream)
     return y
 
 

@@ -176,12 +176,12 @@ def test_norm_output_is_not_the_stream(L):
 
 
 def _linear(L, mx=False, **kw):
-    a = dict(x=A, ldx=64, xs=A, ldxs=2, q=A, s=A, res=None, y=A, M=2, N=16, K=64)
+    a = dict(x=A, ldx=64, xs=A, ldxs=2, q=A, s=A, res=None, y=A, M=2, N=16, K=64, work=A)
     a.update(kw)
     if mx:
         return L.dec_linear_w4_mx(a["x"], a["ldx"], a["xs"], a["ldxs"], a["q"], a["s"], a["res"], a["y"], a["M"],
                                   a["N"], a["K"], None)
-    return L.dec_linear_w4(a["x"], a["ldx"], a["q"], a["s"], a["res"], a["y"], a["M"], a["N"], a["K"], None)
+    return L.dec_linear_w4(a["x"], a["ldx"], a["q"], a["s"], a["res"], a["y"], a["M"], a["N"], a["K"], a["work"], None)
 
 
 @pytest.mark.parametrize("mx", [False, True])
@@ -200,6 +200,14 @@ def test_linear_codes(L, mx, kw, code):
 @pytest.mark.parametrize("kw", [dict(K=40), dict(ldx=72), dict(ldxs=1), dict(xs=None)])
 def test_linear_mx_codes(L, kw):
     assert _linear(L, True, **kw) == dg.DEC_EINVAL
+
+
+def test_linear_work(L):
+    """A few tokens need no work space; more have to be given it, 16-byte aligned."""
+    assert L.dec_linear_w4_work(1, 4096) == 0 and L.dec_linear_w4_work(64, 4096) > 2 * 64 * 4096
+    assert L.dec_linear_w4_work(0, 4096) == 0 and L.dec_linear_w4_work(65, 4096) == 0
+    for work in (None, MIS):
+        assert _linear(L, M=64, work=work) == dg.DEC_EINVAL
 
 
 @pytest.mark.parametrize("args,code", [
