@@ -30,20 +30,16 @@ def _bound(index):
         h = _Handle()
         h._bind(torch.device("cuda", index))
         h._f8, h._e8, h._u8 = torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8
+        h._like = torch.empty_like
         h._getdev, h._guard = torch._C._cuda_getDevice, torch.cuda.device
         _handles[index] = h
     return h
 
 
-def _call(h, what, fn, args, stream):
-    """One C call on h's device, whichever is current."""
-    if h._getdev() == h._index:
-        rc = fn(*args, h._stream(stream))
-    else:
-        with h._guard(h._index):
-            rc = fn(*args, h._stream(stream))
-    if rc:
-        _check(rc, what)
+def _elsewhere(h, fn, args, stream):
+    """One C call on a device that is not the current one."""
+    with h._guard(h._index):
+        return fn(*args, h._stream(stream))
 
 
 def _is_matrix(t, dtype, index, rows, width):
@@ -116,15 +112,10 @@ class MX8:
         _explain("s", s, e8, (T, H // 32), 1)
         if q.device != s.device:
             raise ValueError("s: on %s, the other operands on %s" % (s.device, q.device))
-        self._set(q, s)
-
-    def _set(self, q, s):
         self.q, self.s = q, s
         self.shape, self._index = q.shape, q.get_device()
-        T, H = q.shape
         self._args = (q.data_ptr(), q.stride(0) if T > 1 else H, s.data_ptr(),
                       s.stride(0) if T > 1 else H // 32)
-        return self
 
 
 class W4:
@@ -151,9 +142,13 @@ class W4:
                 raise ValueError("%s: must be contiguous" % what)
         if q.device != s.device:
             raise ValueError("s: on %s, the other operands on %s" % (s.device, q.device))
+        self._set(q, s, n, k)
+
+    def _set(self, q, s, n, k):
         self.q, self.s, self.n, self.k = q, s, n, k
         self._index = q.get_device()
         self._args = (q.data_ptr(), s.data_ptr())
+        return self
 
     @staticmethod
     def empty(n, k, device="cuda"):
@@ -184,27 +179,26 @@ class W4:
 
 
 # ---------------------------------------------------------------- the calls
+# (The calls of a decode step are short: what they pass is looked over in few steps,
+# and _wrong says what is the matter.)
 def _norm(what, mx, x, w, residual, h, out, eps, stream):
     try:
         T, H = x.shape
         index = x.get_device()
-        ok = index >= 0 and w.shape == (H,)
-    except (AttributeError, ValueError):
-        ok = False
-    if ok:
-        b = _bound(index)
+        b = _handles.get(index) or _bound(index) if index >= 0 else None
         bf = b._bf16
         ldx = _is_matrix(x, bf, index, T, H)
-        ok = ldx and ldx % 8 == 0 and w.dtype is bf and w.get_device() == index and w.is_contiguous()
-    if ok and T == 0:
-        ldx = H
-    ldr = ldh = 0
+        ok = (ldx and ldx % 8 == 0 and w.shape == (H,) and w.dtype is bf and w.get_device() == index
+              and w.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    ldr = ldh = ldo = 0
     rp = hp = None
     if residual is not None:
         if ok:
             ldr = _is_matrix(residual, bf, index, T, H)
             if h is None:
-                h = b._empty((T, H), dtype=bf, device=b.device)
+                h = b._like(x) if ldx == H else b._empty((T, H), dtype=bf, device=b.device)
                 ldh = H
             else:
                 ldh = _is_matrix(h, bf, index, T, H)
@@ -215,7 +209,7 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         raise ValueError("h: given without a residual")
     if ok and out is not None:
         if mx:
-            if not isinstance(out, MX8):
+            if type(out) is not MX8:
                 raise TypeError("out: expected an MX8, got %s" % type(out).__name__)
             if out._index != index or out.shape != (T, H):
                 raise ValueError("out: expected shape %s on %s, got %s on %s"
@@ -231,23 +225,28 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         _wrong(x.device, ("x", x, bf, (None, None), 8), ("w", w, bf, (x.shape[1],), 1),
                ("residual", residual, bf, tuple(x.shape), 8), ("h", h, bf, tuple(x.shape), 8),
                ("y", None if mx else out, bf, tuple(x.shape), 8))
-    L = lib()
     if mx:
         if H % 32 or not H:
             raise ValueError("x: an 8-bit output needs a width that is a multiple of 32, got %d" % H)
         if out is None:
-            out = MX8.__new__(MX8)._set(b._empty((T, H), dtype=b._f8, device=b.device),
-                                        b._empty((T, H // 32), dtype=b._e8, device=b.device))
-        if T:
-            _call(b, what, L.dec_rmsnorm_mx, (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh,
-                                              *out._args, T, H), stream)
+            q = b._empty((T, H), dtype=b._f8, device=b.device)
+            s = b._empty((T, H // 32), dtype=b._e8, device=b.device)
+            out = MX8.__new__(MX8)
+            out.q, out.s, out.shape, out._index = q, s, x.shape, index
+            out._args = (q.data_ptr(), H, s.data_ptr(), H // 32)
+        fn = lib().dec_rmsnorm_mx
+        args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, *out._args, T, H)
     else:
         if out is None:
-            out = b._empty((T, H), dtype=bf, device=b.device)
+            out = b._like(x) if ldx == H else b._empty((T, H), dtype=bf, device=b.device)
             ldo = H
-        if T:
-            _call(b, what, L.dec_rmsnorm, (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh,
-                                           out.data_ptr(), ldo, T, H), stream)
+        fn = lib().dec_rmsnorm
+        args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, out.data_ptr(), ldo, T, H)
+    if T:
+        rc = (fn(*args, b._stream(stream)) if b._getdev() == index else
+              _elsewhere(b, fn, args, stream))
+        if rc:
+            _check(rc, what)
     return out if residual is None else (out, h)
 
 
@@ -286,11 +285,11 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
     mx = type(x) is MX8
     ok = index >= 0
     if ok:
-        b = _bound(index)
+        b = _handles.get(index) or _bound(index)
         bf = b._bf16
         if mx:
-            M = x.shape[0]
-            ok = x._index == index and x.shape[1] == K
+            M, k = x.shape
+            ok = x._index == index and k == K
         else:
             try:
                 M = x.shape[0]
@@ -309,10 +308,11 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
         if mx:
             if x.shape[1] != K:
                 raise ValueError("x: expected shape [any, %d], got %s" % (K, tuple(x.shape)))
-            shape, xt, dt, al = (x.shape[0], N), x.q, torch.float8_e4m3fn, 16
+            xt, dt, al = x.q, torch.float8_e4m3fn, 16
         else:
             _explain("x", x, bf, (None, K), 8)
-            shape, xt, dt, al = (x.shape[0], N), x, bf, 8
+            xt, dt, al = x, bf, 8
+        shape = (x.shape[0], N)
         for what, t in (("y", y), ("residual", residual)):
             if t is not None:
                 _explain(what, t, bf, shape, 1)
@@ -323,12 +323,12 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
     if y is None:
         y = b._empty((M, N), dtype=bf, device=b.device)
     if M:
+        L = lib()
         rp = None if residual is None else residual.data_ptr()
         if mx:
-            _call(b, "dec_linear_w4", lib().dec_linear_w4_mx,
-                  (*x._args, *W._args, rp, y.data_ptr(), M, N, K), stream)
+            fn, args = L.dec_linear_w4_mx, (*x._args, *W._args, rp, y.data_ptr(), M, N, K)
         else:
-            L, wp = lib(), None
+            wp = None
             if M > 16:
                 n = L.dec_linear_w4_work(M, K)
                 if n:
@@ -336,8 +336,11 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
                     if stream is not None:
                         work.record_stream(stream)
                     wp = work.data_ptr()
-            _call(b, "dec_linear_w4", L.dec_linear_w4,
-                  (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K, wp), stream)
+            fn, args = L.dec_linear_w4, (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K, wp)
+        rc = (fn(*args, b._stream(stream)) if b._getdev() == index else
+              _elsewhere(b, fn, args, stream))
+        if rc:
+            _check(rc, "dec_linear_w4")
     return y
 
 
@@ -348,24 +351,35 @@ def dec_quant_w4(W, out=None, stream=None):
     least power of two that brings the largest to 6 or less; codes are the nearest,
     ties to the even one. A group with a value that is not finite gets the scale NaN.
     """
-    import torch
+    try:
+        N, K = W.shape
+        index = W.get_device()
+        b = _handles.get(index) or _bound(index) if index >= 0 else None
+        ld = _is_matrix(W, b._bf16, index, N, K)
+        ok = ld and ld % 8 == 0 and N >= 1 and K >= 8 and K % 8 == 0
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        import torch
 
-    _explain("W", W, torch.bfloat16, (None, None), 8)
-    N, K = W.shape
-    if N < 1 or K < 8 or K % 8:
-        raise ValueError("W: expected [N, K] with K a multiple of 8, got shape %s" % (tuple(W.shape),))
-    if out is not None:
-        if not isinstance(out, W4):
-            raise TypeError("out: expected a W4, got %s" % type(out).__name__)
-        if (out.n, out.k) != (N, K):
-            raise ValueError("out: expected a W4 of %d x %d, got %d x %d" % (N, K, out.n, out.k))
-    if W.device.type != "cuda":
-        raise ValueError("W: expected a CUDA tensor, got one on %s" % W.device)
+        _explain("W", W, torch.bfloat16, (None, None), 8)
+        N, K = W.shape
+        if N < 1 or K < 8 or K % 8:
+            raise ValueError("W: expected [N, K] with K a multiple of 8, got shape %s" % (tuple(W.shape),))
+        _wrong(None, ("W", W, torch.bfloat16, (None, None), 8))
     if out is None:
-        out = W4.empty(N, K, W.device)
-    elif out.q.device != W.device:
+        nt, kc = -(-N // 128), -(-K // 128)
+        out = W4.__new__(W4)._set(b._empty((nt, kc, 128, 64), dtype=b._u8, device=b.device),
+                                  b._empty((nt, kc, 32, 4, 4), dtype=b._u8, device=b.device), N, K)
+    elif type(out) is not W4:
+        raise TypeError("out: expected a W4, got %s" % type(out).__name__)
+    elif (out.n, out.k) != (N, K):
+        raise ValueError("out: expected a W4 of %d x %d, got %d x %d" % (N, K, out.n, out.k))
+    elif out._index != index:
         raise ValueError("out: on %s, the other operands on %s" % (out.q.device, W.device))
-    b = _bound(W.get_device())
-    _call(b, "dec_quant_w4", lib().dec_quant_w4,
-          (W.data_ptr(), W.stride(0) if N > 1 else K, *out._args, N, K), stream)
+    fn, args = lib().dec_quant_w4, (W.data_ptr(), ld, *out._args, N, K)
+    rc = (fn(*args, b._stream(stream)) if b._getdev() == index else
+          _elsewhere(b, fn, args, stream))
+    if rc:
+        _check(rc, "dec_quant_w4")
     return out
