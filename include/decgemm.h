@@ -517,7 +517,8 @@ int dec_rmsnorm_mx(const void* x, int64_t ldx, const void* res, int64_t ldres, c
  *            2i of a row's 128 k in the low half of byte i
  *   scales : [ceil(N/128)][ceil(K/128)][32][4][4], 16-byte aligned: row n, group g of
  *            the unit's four at [n % 32][n % 128 / 32][g]
- * Codes past K are 0. What lies past N is read and has no effect.
+ * What lies past N is read and has no effect; past K, where the tokens read as 0,
+ * neither has what is not a scale of 255.
  *
  * dec_quant_w4 -- bf16 weights W [N, K] (rows ldw elements apart, a multiple of 8;
  * K a multiple of 8) in that form, what lies past N and K included (codes 0). For
@@ -533,16 +534,19 @@ int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K
  *   x    : [M, K] bf16, rows ldx elements apart (at least K, a multiple of 8);
  *          1 <= M <= 64, K a multiple of 8
  *   res, y : [M, N] bf16; y may be res
+ *   work : dec_linear_w4_work(M, K) bytes of device memory, 16-byte aligned, that the
+ *          call may write until its kernels end; NULL where that is 0 (M <= 16). The
+ *          library's own workspace is not used: calls with work spaces of their own
+ *          may run at once.
  *
  * The tensor cores take 4-bit weights with 8-bit tokens. A bf16 token value enters
  * as the sum of two e4m3 numbers, each with a scale for 32 k: exact down to 2^-15
  * of the largest magnitude of its 32, off by at most 2^-22 of that magnitude below.
  * Products are exact, sums fp32, in an order that does not change from run to
  * run; y is rounded once. A token with a value that is not finite gives NaN in
- * all its outputs. W is read before the previous kernel of the stream has finished:
- * as with dec_linear, that kernel must not be one of this library's that writes it
- * (dec_quant_w4 is safe: nothing starts before it has ended).
- * Errors: DEC_EINVAL, DEC_EUNSUPPORTED (M > 64, or 2^24 units or more), DEC_ECUDA.
+ * all its outputs. W is read while the previous kernel of the stream may still run, as
+ * by dec_linear; dec_quant_w4 lets nothing start before it has ended.
+ * Errors: DEC_EINVAL, DEC_EUNSUPPORTED (M > 64, K > 2^29, 2^24 units or more), DEC_ECUDA.
  *
  * dec_linear_w4_mx -- the same for tokens in 8 bits: x [M, K] e4m3, rows ldx bytes
  * apart (a multiple of 16), xscales [M, K/32] bytes, rows ldxscales apart; K a

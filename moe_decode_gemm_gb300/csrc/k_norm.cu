@@ -114,13 +114,11 @@ __global__ void __launch_bounds__(WARP ? kNormWarps * 32 : 1024) norm_kernel(con
   const long long row = WARP ? (long long)blockIdx.x * kNormWarps + warp : blockIdx.x;
   const int nv = a.H / 8;
   griddep_launch_dependents();
-  uint4 w[VPT];
-  if (VPT == 1) {  // few rows: the weights come while the kernel before ends
-    w[0] = t < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + t) : make_uint4(0u, 0u, 0u, 0u);
-  }
   griddep_wait();
   if (WARP && row >= a.rows) return;
-  uint4 h[VPT];
+  uint4 h[VPT], w[VPT];
+  if (VPT == 1)  // few rows: the weights' way is the same as the row's
+    w[0] = t < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + t) : make_uint4(0u, 0u, 0u, 0u);
   float sum = 0.f;
   float2 sq_hi = make_float2(0.f, 0.f), sq_lo = sq_hi;  // of even and odd columns
 #pragma unroll

@@ -266,9 +266,12 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
     // ---------------------------------------------------------------- weights
     if (lane == 0) {
       const uint64_t pol = policy_evict_first();
-      int i = 0, rt = 0, s = 0, ph = 1;  // the first pass over the ring finds it empty
+      int i = 0, rt = 0, s = 0, ph = 1;
       for (int kc = 0; kc < nk; ++i) {
-        if (!mbar_wait(&wempty[s], ph, a.timeout_ns, a.status)) {
+        // The first pass over the ring finds it empty, and the kernel before perhaps
+        // running; from then on the wait is for this kernel alone.
+        if (i == WS) griddep_wait();
+        if (i >= WS && !mbar_wait(&wempty[s], ph, a.timeout_ns, a.status)) {
           s_flags[0] = 1;
           break;
         }
@@ -354,8 +357,9 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
         xp ^= 1;
       }
     }
-    umma_commit_elect(leader, tfull);
     if (!ok) s_flags[0] = 1;
+    __syncwarp();
+    umma_commit_elect(leader, tfull);
     mbar_wait(tfull, 0, drain_ns(a.timeout_ns), nullptr);
   } else {
     // ---------------------------------------------------------------- tokens
@@ -391,11 +395,10 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
               xp ^= 1;
             }
           }
-          // A give-up: the copies in flight land before the shared memory is used anew
-          // (their barriers may lack arrivals, so the wait may take its whole bound).
-          if (!ok)
-            for (int q = 0; q < XS && q < issued; ++q)
-              mbar_wait(&xfull[q], ((issued - q + XS - 1) / XS - 1) & 1, drain_ns(a.timeout_ns), nullptr);
+          // Every issued copy has landed before the shared memory is used anew (after a
+          // give-up a barrier may lack arrivals, and the wait take its whole bound).
+          for (int q = 0; q < XS && q < issued; ++q)
+            mbar_wait(&xfull[q], ((issued - q + XS - 1) / XS - 1) & 1, drain_ns(a.timeout_ns), nullptr);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       } else if (MODE == W4_MX && warp < 3 + (MT + 31) / 32) {

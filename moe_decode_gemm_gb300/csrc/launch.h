@@ -259,9 +259,9 @@ bool make_tmap_w4(CUtensorMap* map, const void* q, uint64_t rows, uint32_t box_r
 bool make_tmap_bytes(CUtensorMap* map, const void* x, uint64_t rows, uint64_t cols, uint64_t ld,
                      uint32_t box_rows);
 
-// Whether the units of N x K weights can be named by 32 bits.
+// Whether the rows of the units of N x K weights, and places along K, fit 32 bits.
 inline bool w4_fits(int N, int K) {
-  return ((int64_t)N + 127) / 128 * (((int64_t)K + 127) / 128) <= (INT32_MAX / 128);
+  return K <= (1 << 29) && ((int64_t)N + 127) / 128 * (((int64_t)K + 127) / 128) <= (INT32_MAX / 128);
 }
 
 struct W4Call {

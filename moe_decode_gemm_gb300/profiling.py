@@ -17,6 +17,9 @@
     python -m moe_decode_gemm_gb300.profiling case shared TOKENS [CALLS]
     python -m moe_decode_gemm_gb300.profiling case prefetch M ON [CALLS]
     python -m moe_decode_gemm_gb300.profiling case attention BATCH TOKENS LENGTH [CALLS]
+    python -m moe_decode_gemm_gb300.profiling case w4 M N K MX [CALLS]
+    python -m moe_decode_gemm_gb300.profiling case norm ROWS WIDTH MX [CALLS]
+    python -m moe_decode_gemm_gb300.profiling case quant N K [CALLS]
         A small case to run under `ncu --set full` (needs a GPU): CALLS
         (default 3) MoE blocks of TOKENS tokens over a bank of EXPERTS routed
         experts (hidden 7168, intermediate 2048, top-8, no shared expert),
@@ -30,7 +33,10 @@
         rate of the projection under `ncu --cache-control none`), or CALLS
         appends and attentions of BATCH sequences with TOKENS new tokens each
         over LENGTH positions in pages of 64 (56 query and 4 key/value heads of
-        128), between two layers' caches in turn. Inputs are
+        128), between two layers' caches in turn, or CALLS projections with 4-bit
+        weights of M bf16 (MX = 0) or 8-bit tokens over eight weight matrices in
+        turn, or CALLS norms with residual of ROWS rows with bf16 or 8-bit output,
+        or CALLS quantisations of an N x K matrix. Inputs are
         seeded and synthetic; each expert is 88 MB, so a bank of 32 (2.8 GB)
         is far larger than L2 and its DRAM counters mean what they say.
 
@@ -89,13 +95,25 @@ def kernel_label(name):
         if m.group(3) in _TRUE:
             return "router + top-k [tcgen05 cluster%s]" % stage
         return "projection [tcgen05 %s cluster%s]" % (_EPI.get(m.group(1), m.group(1)), stage)
+    # <tokens, tiles a CTA, source of the tokens, warps>
+    m = re.search(r"w4_linear_kernel<(\d+),\s*(\d+),\s*(\d+)", name)
+    if m:
+        return "4-bit projection [%s tokens, %s tile%s, %s]" % (
+            m.group(1), m.group(2), "" if m.group(2) == "1" else "s",
+            {"0": "converted", "1": "8-bit", "2": "converted ahead"}.get(m.group(3), m.group(3)))
+    m = re.search(r"norm_kernel<(\d+),\s*(\w+),\s*(\w+)>", name)
+    if m:
+        return "norm [%s, %s, %s vector%s a thread]" % (
+            "8-bit" if m.group(2) in _TRUE else "bf16", "warp a row" if m.group(3) in _TRUE else "CTA a row",
+            m.group(1), "" if m.group(1) == "1" else "s")
     for k, lab in (("schedule_gather_kernel", "schedule + gather"),
                    ("combine_kernel", "combine"), ("add_kernel", "residual add"),
                    ("prefetch_kernel", "l2_prefetch"), ("append_kernel", "append"),
                    ("attn_tc_kernel", "attention [tcgen05]"), ("attn_join_kernel", "attention join"),
                    ("attn_mma_kernel", "attention [mma.sync]"), ("kv_change_kernel", "page state"),
                    ("kv_copy_kernel", "page copies"), ("kv_rank_kernel", "compact: ranks"),
-                   ("kv_move_kernel", "compact: moves")):
+                   ("kv_move_kernel", "compact: moves"), ("w4_tokens_kernel", "4-bit projection: tokens"),
+                   ("w4_quant_kernel", "quantisation to 4 bits")):
         if k in name:
             return lab
     return name[:60]
@@ -251,6 +269,37 @@ def case(kind, *args):
         torch.cuda.synchronize()
         print("attention batch=%d tokens=%d length=%d regime=%s calls=%d"
               % (B, T, N, dg.last_attention(), calls))
+    elif kind == "w4":
+        M, N, K, mx = (int(v) for v in args[:4])
+        calls = int(args[4]) if len(args) > 4 else 9
+        W = normal_bf16_cuda((N, K), WEIGHT_STD, "profile", "W4")
+        Ws = [dg.dec_quant_w4(W) for _ in range(8)]
+        x = normal_bf16_cuda((M, K), 1.0, "profile", "x4", M)
+        y = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        if mx:
+            x = dg.dec_rmsnorm_mx(x, torch.ones(K, dtype=torch.bfloat16, device="cuda"))
+        torch.cuda.synchronize()
+        for i in range(calls):
+            dg.dec_linear_w4(x, Ws[i % 8], y)
+        torch.cuda.synchronize()
+        print("w4 M=%d N=%d K=%d mx=%d calls=%d" % (M, N, K, mx, calls))
+    elif kind == "norm":
+        T, H, mx = (int(v) for v in args[:3])
+        calls = int(args[3]) if len(args) > 3 else 3
+        xs = [normal_bf16_cuda((T, H), 1.0, "profile", "xn", i) for i in range(4)]
+        w = normal_bf16_cuda((H,), 1.0, "profile", "wn")
+        for i in range(calls):
+            (dg.dec_rmsnorm_mx if mx else dg.dec_rmsnorm)(xs[i % 2], w, xs[2 + i % 2])
+        torch.cuda.synchronize()
+        print("norm rows=%d width=%d mx=%d calls=%d" % (T, H, mx, calls))
+    elif kind == "quant":
+        N, K = int(args[0]), int(args[1])
+        calls = int(args[2]) if len(args) > 2 else 3
+        Ws = [normal_bf16_cuda((N, K), WEIGHT_STD, "profile", "Wq4", i) for i in range(2)]
+        for i in range(calls):
+            dg.dec_quant_w4(Ws[i % 2])
+        torch.cuda.synchronize()
+        print("quant N=%d K=%d calls=%d" % (N, K, calls))
     else:
         sys.exit(__doc__)
     if dg.sync_check() != 0:

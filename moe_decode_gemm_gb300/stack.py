@@ -10,7 +10,8 @@ and, on a side stream, an L2 prefetch of the next layer's weights. The o
 projection consuming q stands in for the attention output; kv is computed and
 not consumed. The benchmark and the full-size parity tests both run this
 function, so what is timed is what is checked. attention_layer is the same
-layer with its attention over a paged cache.
+layer with its attention over a paged cache, w4_layer that one with its norms
+and with 4-bit weights in its projections.
 
 Sources: "vLLM 如何用智能体辅助优化 Kimi K3 解码性能", Part 1 §1 (projections),
 §3 (MoE block, shared expert on its own stream) and §4 (prefetch of upcoming
@@ -19,7 +20,8 @@ weights on a side stream); "vLLM 宣布 Kimi K3 在 GB300 NVL72 上实现 batch 
 """
 from __future__ import annotations
 
-from . import dec_linear, kv_append, kv_attention, l2_prefetch, moe_decode
+from . import (dec_linear, dec_linear_w4, dec_rmsnorm, dec_rmsnorm_mx, kv_append, kv_attention,
+               l2_prefetch, moe_decode)
 
 
 def decode_layer(L, x, qkv, r, out, topk, idx=None, stream=None, prefetch=None):
@@ -72,5 +74,33 @@ def attention_layer(L, x, kv, rope, qkv, o, r, out, topk, wq=None, wk=None, wind
         side.wait_event(ev)
         l2_prefetch(ptr, nbytes, stream=side)
     moe_decode(r, L.Wr, L.W13, L.W2, L.Ws13, L.Ws2, topk, out=out, topk_idx=idx, stream=stream,
+               residual=r)
+    return out
+
+
+def w4_layer(L, x, kv, rope, qkv, o, a, r, out, topk, wq=None, wk=None, window=0, idx=None, stream=None,
+             interleaved=False, mx=True, eps=1e-6):
+    """One decode layer with its norms, attention and 4-bit projections; returns ``out``.
+
+      n           = norm(x)·w1          in 8 bits with scales (dec_rmsnorm_mx), or with
+                                        mx=False in bf16 (dec_rmsnorm)
+      [q | k | v] = n·Wqkvᵀ             4-bit weights (dec_linear_w4)
+      o           = attention, as attention_layer
+      a           = o·Woᵀ               4-bit weights
+      r           = bf16(x + a),  n = norm(r)·w2      (dec_rmsnorm, one pass)
+      x'          = bf16(r + MoE(n))    (moe_decode, bf16 weights)
+
+    L: weights with Wqkv [q width + 2*kv.heads*kv.dim, H] and Wo [H, q width] as W4
+    (dec_quant_w4), w1 and w2 [H] bf16, Wr, W13, W2, Ws13, Ws2 as decode_layer's.
+    x [M, H] bf16, M <= 64; qkv, o, r, out: buffers as attention_layer's, a [M, H]
+    bf16. out may be x. The other arguments as there; H a multiple of 32 for mx.
+    """
+    norm = dec_rmsnorm_mx if mx else dec_rmsnorm
+    dec_linear_w4(norm(x, L.w1, eps=eps, stream=stream), L.Wqkv, qkv, stream=stream)
+    q = kv_append(qkv, kv, rope, wq, wk, q=qkv[:, :L.Wo.k], stream=stream, interleaved=interleaved)
+    kv_attention(q, kv, out=o, window=window, stream=stream)
+    dec_linear_w4(o, L.Wo, a, stream=stream)
+    n, _ = dec_rmsnorm(a, L.w2, x, h=r, eps=eps, stream=stream)
+    moe_decode(n, L.Wr, L.W13, L.W2, L.Ws13, L.Ws2, topk, out=out, topk_idx=idx, stream=stream,
                residual=r)
     return out

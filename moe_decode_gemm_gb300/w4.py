@@ -125,8 +125,9 @@ class W4:
     sign in bit 3 and stands for 0, .5, 1, 1.5, 2, 3, 4 or 6.
     q [ceil(N/128), ceil(K/128), 128, 64] uint8: row n % 128, element 2i of its 128
     k in the low half of byte i. s [ceil(N/128), ceil(K/128), 32, 4, 4] uint8: scale
-    of row n at [n % 32, n % 128 // 32, k % 128 // 32]. Codes past N or K are 0 (those
-    past K must be). dec_quant_w4 makes them from bf16 weights, `pack` from codes.
+    of row n at [n % 32, n % 128 // 32, k % 128 // 32]. What lies past N has no effect,
+    past K only a scale of 255. dec_quant_w4 makes them from bf16 weights, `pack` from
+    codes.
     """
 
     def __init__(self, q, s, n, k):
@@ -277,7 +278,8 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
     not x. fp32 sums, one rounding. bf16 tokens are taken as two 8-bit numbers
     each: exact for values down to 2^-15 of the largest of their 32 (aligned) k,
     off by at most 2^-22 of the largest below. A token with a value that is not
-    finite gives NaN in all its outputs.
+    finite gives NaN in all its outputs. More than 16 bf16 tokens take a work space
+    from torch's allocator for the call.
     """
     if not isinstance(W, W4):
         raise TypeError("W: expected a W4, got %s" % type(W).__name__)

@@ -321,3 +321,59 @@ def test_on_another_stream():
     for i in range(2):
         for y in got[i]:
             assert torch.equal(y, want[i])
+
+
+# ------------------------------------------------------------------ the index-checking build
+def test_index_checks():
+    """Every kind of call through the build that checks its indexes."""
+    dbg = dg._load(dg.DEBUG_LIB_PATH)
+    old = dg.use_library(dbg)
+    try:
+        for M, N, K in ((1, 130, 264), (7, 2048, 1024), (16, 1001, 520), (30, 300, 1000), (64, 257, 512)):
+            W = ref.normal(N, N, K, std=0.05)
+            w4 = dg.dec_quant_w4(W.cuda())
+            x, res = ref.activations(M, M, K), ref.normal(M + 1, M, N)
+            y = dg.dec_linear_w4(x.cuda(), w4, residual=res.cuda())
+            want, a, spread = ref.linear(x, ref.weights(*ref.unpack(w4.q, w4.s, N, K)), res)
+            _check(y, want, ref.linear_bound(want, a, spread, K, False))
+        for rows, H in ((1, 40), (5, 7168), (700, 96), (700, 2048), (330, 8200)):
+            x, w, res = ref.activations(H, rows, H), ref.normal(1, H), ref.normal(2, rows, H)
+            h, want = ref.norm(x, w, res)
+            y, hh = dg.dec_rmsnorm(_strided(x, 8), w.cuda(), res.cuda())
+            _check(y, want, (ref.HALF_BF + 48 * 2.0 ** -24) * want.abs() + 1e-38)
+            if H % 32 == 0:
+                _check_mx(dg.dec_rmsnorm_mx(x.cuda(), w.cuda(), res.cuda())[0], want)
+        x, values = _mx8(3, 33, 1024)
+        codes, scales = ref.random_codes(3, 300, 1024)
+        y = dg.dec_linear_w4(x, dg.W4.pack(codes.cuda(), scales.cuda()))
+        want, a, spread = ref.linear(values, ref.weights(codes, scales))
+        _check(y, want, ref.linear_bound(want, a, spread, 1024, True))
+    finally:
+        torch.cuda.synchronize()
+        dg.use_library(old)
+
+
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("M,N,K,mx", [(1, 2048, 4096, False), (12, 8192, 4096, False), (40, 1024, 4096, False),
+                                      (64, 1024, 4096, True)])
+def test_waits_that_run_out(M, N, K, mx):
+    """With no time to wait the kernel gives up, says so and ends; the next call is right."""
+    codes, scales = ref.random_codes(1, N, K)
+    W = dg.W4.pack(codes.cuda(), scales.cuda())
+    if mx:
+        x, values = _mx8(M, M, K)
+    else:
+        values = ref.activations(M, M, K)
+        x = values.cuda()
+    first = dg.dec_linear_w4(x, W)
+    assert dg.sync_check() == dg.DEC_OK
+    old = dg.set_wait_timeout_ns(0)
+    try:
+        dg.dec_linear_w4(x, W)
+        assert dg.sync_check() in (dg.DEC_OK, dg.DEC_ETIMEOUT)
+    finally:
+        dg.set_wait_timeout_ns(old)
+    assert torch.equal(dg.dec_linear_w4(x, W), first)
+    assert dg.sync_check() == dg.DEC_OK
+    want, a, spread = ref.linear(values, ref.weights(codes, scales))
+    _check(first, want, ref.linear_bound(want, a, spread, K, mx))
