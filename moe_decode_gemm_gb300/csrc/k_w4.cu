@@ -193,6 +193,34 @@ __device__ __forceinline__ void bulk_copy_s2cluster(void* local, const void* src
                : "memory");
 }
 
+// A thread's next outputs: a token's four rows each, threads side by side along the
+// rows that the CTA owns.
+template <int THREADS>
+struct W4Outputs {
+  static constexpr int U = 2;  // under way at once
+  int quads, items, n0;        // fours of rows of a token; of all tokens; the first row
+  int e;                       // the item after these
+  int tok[U], quad[U];         // tok < 0: none
+  uint2 res[U];
+  __device__ bool any() const { return tok[0] >= 0; }
+  __device__ void find(const W4Args& a, int first) {
+    e = first;
+#pragma unroll
+    for (int u = 0; u < U; ++u, e += THREADS) {
+      tok[u] = -1;
+      quad[u] = 0;
+      res[u] = make_uint2(0u, 0u);
+      if (e >= items) continue;
+      tok[u] = e / quads;
+      quad[u] = e - tok[u] * quads;
+      const int n = n0 + 4 * quad[u];
+      if (a.res && (a.N & 3) == 0 && n < a.N)
+        res[u] = *reinterpret_cast<const uint2*>(
+            DG_AT(a.status, a.res, (long long)tok[u] * a.N + n, (long long)a.M * a.N - 3));
+    }
+  }
+};
+
 template <int MT, int RT, int MODE, int CW>
 __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
     w4_linear_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap1,
@@ -228,6 +256,11 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
   const int R4 = ((rows + cs - 1) / cs + 3) / 4 * 4;
   const int r0 = cr * R4 < rows ? cr * R4 : rows;
   const int RR = (r0 + R4 < rows ? r0 + R4 : rows) - r0;
+
+  W4Outputs<CONV> next;
+  next.quads = RR / 4;
+  next.items = next.quads * a.M;
+  next.n0 = tile0 * kW4Tile + r0;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -515,6 +548,7 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
       }
     }
     if (!ok) s_flags[0] = 1;
+    next.find(a, threadIdx.x - 64);  // the first outputs' places, and their residual, meanwhile
     if (!s_flags[0]) {
       if (!mbar_wait(tfull, 0, a.timeout_ns, a.status)) s_flags[0] = 1;
     }
@@ -576,44 +610,19 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
     if (cs > 1) cluster_arrive_all();  // what this CTA was sent has landed
   }
   if (warp >= 2 && whole && !s_flags[0]) {
-    // an item is a token's four rows; two under way per thread
-    constexpr int U = 2;
-    const int quads = RR / 4, items = quads * a.M;
-    const bool vec = (a.N & 3) == 0;
-    const int n0 = tile0 * kW4Tile + r0;
-    int e = threadIdx.x - 64, tok = quads ? e / quads : 0, rq = e - tok * quads;
-    const int dtok = quads ? CONV / quads : 0, drq = CONV - dtok * quads;
-    while (e < items) {
-      float4 sum[U];
-      int toks[U], rqs[U];
-      bool in[U];
-      uint2 rv[U];
+    while (next.any()) {
+      W4Outputs<CONV> now = next;
+      next.find(a, now.e);
+      float4 sum[now.U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        in[u] = e < items;
-        toks[u] = tok;
-        rqs[u] = rq;
-        e += CONV;
-        tok += dtok;
-        rq += drq;
-        if (rq >= quads) {
-          rq -= quads;
-          ++tok;
-        }
-        sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        rv[u] = make_uint2(0u, 0u);
-        const int n = n0 + 4 * rqs[u];
-        if (a.res && vec && in[u] && n < a.N)
-          rv[u] = *reinterpret_cast<const uint2*>(
-              DG_AT(a.status, a.res, (long long)toks[u] * a.N + n, (long long)a.M * a.N - 3));
-      }
+      for (int u = 0; u < now.U; ++u) sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int src = 0; src < cs; ++src) {
         const float* p = (!Sh::kRecvApart && src == cr ? own : recv) + (size_t)src * a.M * R4;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (in[u]) {
-            const float4 v = *reinterpret_cast<const float4*>(p + toks[u] * R4 + 4 * rqs[u]);
+        for (int u = 0; u < now.U; ++u)
+          if (now.tok[u] >= 0) {
+            const float4 v = *reinterpret_cast<const float4*>(p + now.tok[u] * R4 + 4 * now.quad[u]);
             sum[u].x += v.x;
             sum[u].y += v.y;
             sum[u].z += v.z;
@@ -621,24 +630,22 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
           }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int n = n0 + 4 * rqs[u];
-        if (!in[u] || n >= a.N) continue;
-        const long long o = (long long)toks[u] * a.N + n;
+      for (int u = 0; u < now.U; ++u) {
+        const int n = now.n0 + 4 * now.quad[u];
+        if (now.tok[u] < 0 || n >= a.N) continue;
+        const long long o = (long long)now.tok[u] * a.N + n;
         const float4 v = sum[u];
-        if (vec) {  // four outputs lie in 8 aligned bytes
-          float4 f = v;
-          if (a.res)
-            f = make_float4(bf16lo(rv[u].x) + v.x, bf16hi(rv[u].x) + v.y, bf16lo(rv[u].y) + v.z,
-                            bf16hi(rv[u].y) + v.w);
+        if ((a.N & 3) == 0) {  // four outputs lie in 8 aligned bytes
+          const uint2 r = now.res[u];
           *reinterpret_cast<uint2*>(DG_AT(a.status, a.y, o, (long long)a.M * a.N - 3)) =
-              make_uint2(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w));
+              a.res ? make_uint2(pack_bf16(bf16lo(r.x) + v.x, bf16hi(r.x) + v.y),
+                                 pack_bf16(bf16lo(r.y) + v.z, bf16hi(r.y) + v.w))
+                    : make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         } else {
-          const float out[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll 1
           for (int j = 0; j < 4; ++j)
             if (n + j < a.N) {
-              const float f = j == 0 ? out[0] : j == 1 ? out[1] : j == 2 ? out[2] : out[3];
+              const float f = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
               const float r = a.res ? bf_bits2f(*DG_AT(a.status, a.res, o + j, (long long)a.M * a.N)) + f : f;
               *DG_AT(a.status, a.y, o + j, (long long)a.M * a.N) = f2bf_bits(r);
             }

@@ -184,20 +184,26 @@ class W4:
 # and _wrong says what is the matter.)
 def _norm(what, mx, x, w, residual, h, out, eps, stream):
     try:
-        T, H = x.shape
+        T, H = shape = x.shape
+        ldx, one = x.stride()
         index = x.get_device()
         b = _handles.get(index) or _bound(index) if index >= 0 else None
         bf = b._bf16
-        ldx = _is_matrix(x, bf, index, T, H)
-        ok = (ldx and ldx % 8 == 0 and w.shape == (H,) and w.dtype is bf and w.get_device() == index
-              and w.is_contiguous())
-    except (AttributeError, ValueError):
+        if T < 2:
+            ldx = H  # a single row's stride says nothing
+        ok = (x.dtype is bf and one == 1 and ldx % 8 == 0 and ldx >= H and w.dtype is bf
+              and w.get_device() == index and w.shape == (H,) and w.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
         ok = False
     ldr = ldh = ldo = 0
     rp = hp = None
     if residual is not None:
         if ok:
-            ldr = _is_matrix(residual, bf, index, T, H)
+            if residual.shape == shape and residual.dtype is bf and residual.get_device() == index \
+                    and residual.is_contiguous():
+                ldr = H
+            else:
+                ldr = _is_matrix(residual, bf, index, T, H)
             if h is None:
                 h = b._like(x) if ldx == H else b._empty((T, H), dtype=bf, device=b.device)
                 ldh = H
@@ -212,7 +218,7 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         if mx:
             if type(out) is not MX8:
                 raise TypeError("out: expected an MX8, got %s" % type(out).__name__)
-            if out._index != index or out.shape != (T, H):
+            if out._index != index or out.shape != shape:
                 raise ValueError("out: expected shape %s on %s, got %s on %s"
                                  % ((T, H), x.device, tuple(out.shape), out.q.device))
         else:
@@ -244,8 +250,10 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         fn = lib().dec_rmsnorm
         args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, out.data_ptr(), ldo, T, H)
     if T:
-        rc = (fn(*args, b._stream(stream)) if b._getdev() == index else
-              _elsewhere(b, fn, args, stream))
+        if b._getdev() == index:
+            rc = fn(*args, b._current(index) if stream is None else stream.cuda_stream)
+        else:
+            rc = _elsewhere(b, fn, args, stream)
         if rc:
             _check(rc, what)
     return out if residual is None else (out, h)
@@ -294,10 +302,13 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
             ok = x._index == index and k == K
         else:
             try:
-                M = x.shape[0]
-                ld = _is_matrix(x, bf, index, M, K)
-                ok = ld and ld % 8 == 0
-            except (AttributeError, IndexError):
+                M, k = x.shape
+                ld, one = x.stride()
+                if M < 2:
+                    ld = K  # a single row's stride says nothing
+                ok = (k == K and x.dtype is bf and x.get_device() == index and one == 1 and ld % 8 == 0
+                      and ld >= K)
+            except (AttributeError, ValueError):
                 ok = False
     if ok and y is not None:
         ok = _is_matrix(y, bf, index, M, N) and y.is_contiguous()
@@ -339,8 +350,10 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
                         work.record_stream(stream)
                     wp = work.data_ptr()
             fn, args = L.dec_linear_w4, (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K, wp)
-        rc = (fn(*args, b._stream(stream)) if b._getdev() == index else
-              _elsewhere(b, fn, args, stream))
+        if b._getdev() == index:
+            rc = fn(*args, b._current(index) if stream is None else stream.cuda_stream)
+        else:
+            rc = _elsewhere(b, fn, args, stream)
         if rc:
             _check(rc, "dec_linear_w4")
     return y
