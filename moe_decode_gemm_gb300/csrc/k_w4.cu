@@ -28,11 +28,11 @@
 // into their ring (bf16 ones converted, e4m3 ones by TMA) and then drain the
 // accumulators.
 //
-// GB300, us on the GPU (of the weights' bytes at the measured copy rate): 7168 x 7168
-// with 1 / 16 / 64 tokens 7.8 / 8.5 / 13.4 (4.0), 16384 x 7168 12.2 / 13.6 / 19.6 (9.2),
-// 64 tokens in 8 bits 10.1 and 14.8. About 3.5 us are start and end (first copies,
-// conversion, exchange, output); 64 bf16 tokens are bound by what an SM takes in, 34 KB
-// of tokens for 17 KB of weights.
+// GB300, us on the GPU (in brackets the weights' bytes at the measured copy rate):
+// 7168 x 7168 with 1 / 16 / 64 tokens 7.7 / 8.4 / 12.8 (4.0), 16384 x 7168 12.1 / 13.4 /
+// 19.3 (9.2), 64 tokens in 8 bits 9.4 and 15.3. About 3.5 us are start and end (first
+// copies, conversion, exchange, output); 64 bf16 tokens with one tile are bound by
+// the 64 bytes a clock that an SM takes in, 34 KB of tokens for 17 KB of weights.
 #include <atomic>
 
 #include "launch.h"
@@ -60,14 +60,13 @@ struct W4Shape {
   static constexpr int kRows = MODE == W4_MX ? MT : 2 * MT;   // token rows: hi, then lo
   static constexpr int kXChunk = kRows * 128;                 // token rows of 128 k
   static constexpr int kXSlot = kPair * kXChunk + 1024;       // and their scales
-  static constexpr int kXS = kRows <= 16 ? 4 : 3;      // ring slots of tokens
+  static constexpr int kXS = kRows <= 16 ? 4 : RT * kRows <= 128 ? 3 : 2;  // ring slots of tokens
   // A slot of weights is a pair of units: what a slot costs the copying and the
   // multiplying warp, 430 and 250 clocks, is more than half of the copies' own time.
   static constexpr int kWSlot = kPair * kW4Spread + 1024;     // and their scales
-  // What a CTA receives from the others of its cluster: RT * 128 rows and 4 to
-  // spare from each, MT tokens. Up to 16 tokens it has a place of its own and is
-  // stored into directly; beyond, bulk copies out of a layout by owner where the
-  // rings were.
+  // The sums of the rows that a CTA owns, from every rank: RT * 128 rows and 4 to spare
+  // from each, MT tokens. Up to 16 tokens they have a place of their own, and no CTA
+  // waits for another's rings before it sends; beyond, they take the rings' place.
   static constexpr int kSums = (RT * kW4Tile + 32) * MT * 4;
   static constexpr bool kRecvApart = MT <= 16;
   static constexpr int kFixed = 1024 + 512 + (kRecvApart ? kSums : 0);
@@ -81,8 +80,8 @@ struct W4Shape {
   static_assert(kWS >= 2 && kTmemUsed <= 512, "ring depth, tensor memory");
   static_assert(MODE != W4_CONVERT || kSlots <= kXS, "a turn takes no slot of the ring twice");
   static_assert(kSmem <= kMaxDynSmem, "shared memory");
-  static_assert(8 * (2 * kWS + 2 * kXS + 2) + 16 <= 512, "barriers and flags");
-  static_assert(kRecvApart || 2 * kSums <= kRings, "own sums and received ones fit in the rings");
+  static_assert(8 * (2 * kWS + 2 * kXS + 1) + 16 <= 512, "barriers and flags");
+  static_assert(kRecvApart || kSums <= kRings, "the sums fit in the rings");
   static_assert(CW % 4 == 0, "every quarter of the tensor-memory lanes is drained");
 };
 
@@ -179,20 +178,6 @@ __global__ void __launch_bounds__(kReadyThreads) w4_tokens_kernel(const uint16_t
   put_token<MT>(out + (long long)slot * (kPair * 2 * MT * 128 + 1024), tok, lane, hi, lo, b);
 }
 
-// Bulk copy of `bytes` (a multiple of 16) from this CTA's shared memory to the
-// place that `local` has in CTA `rank` of the cluster, completing on that CTA's
-// barrier where this one has `bar`.
-__device__ __forceinline__ void bulk_copy_s2cluster(void* local, const void* src, uint32_t bytes, uint64_t* bar,
-                                                    uint32_t rank) {
-  uint32_t dst, rbar;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rbar) : "r"(smem_u32(bar)), "r"(rank));
-  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   dst),
-               "r"(smem_u32(src)), "r"(bytes), "r"(rbar)
-               : "memory");
-}
-
 // A thread's next outputs: a token's four rows each, threads side by side along the
 // rows that the CTA owns.
 template <int THREADS>
@@ -231,15 +216,13 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* xring = smem + WS * Sh::kWSlot;
-  float* own = reinterpret_cast<float*>(smem);  // [owner][token][row], when the rings are done with
-  float* recv = reinterpret_cast<float*>(smem + (Sh::kRecvApart ? Sh::kRings : Sh::kSums));  // [source][token][row]
+  float* recv = reinterpret_cast<float*>(smem + (Sh::kRecvApart ? Sh::kRings : 0));  // [source][token][row]
   uint64_t* wfull = reinterpret_cast<uint64_t*>(smem + Sh::kSmem - 1024 - 512);
   uint64_t* wempty = wfull + WS;
   uint64_t* xfull = wempty + WS;
   uint64_t* xempty = xfull + XS;
   uint64_t* tfull = xempty + XS;
-  uint64_t* rfull = tfull + 1;
-  volatile int* s_flags = reinterpret_cast<volatile int*>(rfull + 1);  // [0] abort
+  volatile int* s_flags = reinterpret_cast<volatile int*>(tfull + 1);  // [0] abort
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(const_cast<int*>(s_flags) + 1);
   auto wslot = [&](int s) { return smem + s * Sh::kWSlot; };
   auto xslot = [&](int s) { return xring + s * Sh::kXSlot; };
@@ -273,11 +256,8 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
       mbar_init(&xempty[s], 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(rfull, 1);
     s_flags[0] = 0;
     fence_mbar_init();
-    // the sums that the other ranks will send, whenever they do
-    if (!Sh::kRecvApart && cs > 1) mbar_arrive_expect_tx(rfull, RR > 0 ? (cs - 1) * a.M * R4 * 4 : 0);
   }
   if (warp == 1) {
     tmem_alloc(s_taddr, Sh::kTmem);
@@ -563,14 +543,13 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
     if (!Sh::kRecvApart) cluster_arrive_all();
     cluster_wait_all();  // every rank can be sent to
   }
-  bool whole = true;
   if (warp >= 2 && !s_flags[0]) {
     constexpr int PARTS = CW / 4;  // warps that share a quarter of the lanes
     const uint32_t lanes = taddr + ((uint32_t)((warp & 3) * 32) << 16);
 #pragma unroll 1
     for (int rt = 0; rt < nrt; ++rt) {
       const int r = rt * kW4Tile + (warp & 3) * 32 + lane, q = r / R4;
-      float* dst = (Sh::kRecvApart ? recv + (size_t)cr * a.M * R4 : own + (size_t)q * a.M * R4) + (r - q * R4);
+      float* dst = recv + (size_t)cr * a.M * R4 + (r - q * R4);
 #pragma unroll 1
       for (int c = 16 * ((warp - 2) >> 2); c < a.M; c += 16 * PARTS) {
         uint32_t v[16], w[16];
@@ -583,33 +562,15 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
         for (int j = 0; j < 16; ++j) {
           float f = __uint_as_float(v[j]);
           if constexpr (MODE != W4_MX) f += __uint_as_float(w[j]);
-          if (c + j < a.M) {
-            if (Sh::kRecvApart) st_dsmem_f32(dst + (c + j) * R4, (uint32_t)q, f);
-            else dst[(c + j) * R4] = f;
-          }
+          if (c + j < a.M) st_dsmem_f32(dst + (c + j) * R4, (uint32_t)q, f);
         }
       }
     }
     tc_fence_before();
   }
-  if (Sh::kRecvApart) {
-    __syncwarp();
-    cluster_sync_all();
-  } else {
-    if (warp >= 2 && cs > 1) {
-      fence_async_shared();
-      named_bar_sync(1, CONV);
-      // (a CTA that has given up sends nothing: its peers' waits run out as well)
-      if (warp == 2 && lane < cs && lane != cr && lane * R4 < rows && !s_flags[0])
-        bulk_copy_s2cluster(recv + (size_t)cr * a.M * R4, own + (size_t)lane * a.M * R4, a.M * R4 * 4, rfull, lane);
-      whole = mbar_wait_cluster(rfull, 0, s_flags[0] ? drain_ns(a.timeout_ns) : a.timeout_ns, a.status);
-    } else if (warp >= 2) {
-      named_bar_sync(1, CONV);
-    }
-    __syncwarp();
-    if (cs > 1) cluster_arrive_all();  // what this CTA was sent has landed
-  }
-  if (warp >= 2 && whole && !s_flags[0]) {
+  __syncwarp();
+  cluster_sync_all();
+  if (warp >= 2 && !s_flags[0]) {
     while (next.any()) {
       W4Outputs<CONV> now = next;
       next.find(a, now.e);
@@ -618,7 +579,7 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
       for (int u = 0; u < now.U; ++u) sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int src = 0; src < cs; ++src) {
-        const float* p = (!Sh::kRecvApart && src == cr ? own : recv) + (size_t)src * a.M * R4;
+        const float* p = recv + (size_t)src * a.M * R4;
 #pragma unroll
         for (int u = 0; u < now.U; ++u)
           if (now.tok[u] >= 0) {
@@ -653,8 +614,6 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
       }
     }
   }
-  __syncwarp();
-  if (!Sh::kRecvApart && cs > 1) cluster_wait_all();  // and what it has sent: its memory may go
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -766,41 +725,50 @@ size_t w4_work_bytes(int M, int K) {
   return (size_t)pairs * (kPair * 2 * mt * 128 + 1024);
 }
 
-// Ring slots of tokens that a CTA converts, with RT tiles a CTA.
-template <int MT, int RT, int CW>
-static cudaError_t w4_slots(const Ctx& cx, const W4Call& c, int* slots) {
+// Ring slots of tokens that an SM goes through, with RT tiles a CTA.
+template <int MT, int RT, int MODE, int CW>
+static cudaError_t w4_slots(const Ctx& cx, const W4Call& c, long long* slots) {
   const int tiles = (c.N + kW4Tile - 1) / kW4Tile, pairs = ((c.K + kW4Tile - 1) / kW4Tile + kPair - 1) / kPair;
+  const int sets = (tiles + RT - 1) / RT;
   int split = 1;
-  const cudaError_t e = w4_split<MT, RT, W4_CONVERT, CW>((tiles + RT - 1) / RT, pairs, cx.sms, &split);
-  *slots = (pairs + split - 1) / split;
+  const cudaError_t e = w4_split<MT, RT, MODE, CW>(sets, pairs, cx.sms, &split);
+  *slots = (long long)((pairs + split - 1) / split) * ((sets * (long long)split + cx.sms - 1) / cx.sms);
   return e;
 }
 
-// One or two tiles a CTA. With more than a few tokens the conversion of a slot (700
-// clocks) takes longer than its pair of units; two tiles share it, with half of the
-// sums' exchange more. us (GPU) of one / two tiles: 16 tokens of 16384 x 7168 20.0 /
-// 13.6 (28 slots a CTA / 14), 8192 x 7168 11.7 / 8.7 (14 / 7), 2048 x 16384 9.8 / 8.7
-// (11 / 8), 2048 x 7168 6.15 / 6.07 (5 / 4), 4096 x 4096 5.72 / 5.73 (4 / 3), 1001 x
-// 1992 4.10 / 4.35 (1 / 1); 8 tokens of 16384 x 7168 14.4 / 13.2.
-template <int MT, int CW>
-static cudaError_t w4_convert(const Ctx& cx, const W4Call& c) {
-  int one = 0, two = 0;
-  if (cudaError_t e = w4_slots<MT, 1, CW>(cx, c, &one); e != cudaSuccess) return e;
-  if (cudaError_t e = w4_slots<MT, 2, CW>(cx, c, &two); e != cudaSuccess) return e;
-  return one - two >= 2 ? run_w4<MT, 2, W4_CONVERT, CW>(cx, c) : run_w4<MT, 1, W4_CONVERT, CW>(cx, c);
+// One or two tiles a CTA: two where that leaves each SM at least `least` slots fewer, or
+// any where there are more tiles than SMs (20000 x 4096, 157 tiles, 1 token: 15.4 us
+// of one, 32 slots, 12.2 of two, 16; 64 in 8 bits 20.9 and 16.1).
+// Two tiles share a slot's tokens, with twice the sums to exchange. Converting them
+// takes 700 clocks a slot, longer than a pair of units; from 33 tokens on they are
+// twice a pair's bytes, more than an SM takes in. us (GPU) of one / two tiles, slots
+// in brackets:
+//   16 tokens  16384 x 7168 20.0 (28) / 13.6 (14), 8192 x 7168 11.7 (14) / 8.7 (7),
+//              2048 x 16384 9.8 (11) / 8.7 (8), 2048 x 7168 6.15 (5) / 6.07 (4), 4096 x
+//              4096 5.72 (4) / 5.73 (3), 1001 x 1992 4.10 (1) / 4.35 (1)
+//    8 tokens  16384 x 7168 14.4 / 13.2, 8192 x 7168 9.3 / 8.5, 2048 x 16384 8.2 / 8.2
+//   64 tokens  16384 x 7168 20.1 / 19.3, 8192 x 7168 13.0 / 13.3, 2048 x 16384 11.7 / 13.1
+template <int MT, int MODE, int CW>
+static cudaError_t w4_tiles(const Ctx& cx, const W4Call& c, int least) {
+  long long one = 0, two = 0;
+  if (cudaError_t e = w4_slots<MT, 1, MODE, CW>(cx, c, &one); e != cudaSuccess) return e;
+  if (cudaError_t e = w4_slots<MT, 2, MODE, CW>(cx, c, &two); e != cudaSuccess) return e;
+  if ((c.N + kW4Tile - 1) / kW4Tile > cx.sms) least = 1;
+  return one - two >= least ? run_w4<MT, 2, MODE, CW>(cx, c) : run_w4<MT, 1, MODE, CW>(cx, c);
 }
 
 cudaError_t launch_w4_linear(const Ctx& cx, const W4Call& c) {
+  constexpr int kNever = INT32_MAX;
   if (c.xs) {
-    if (c.M <= 16) return run_w4<16, 1, W4_MX, 4>(cx, c);
-    if (c.M <= 32) return run_w4<32, 1, W4_MX, 4>(cx, c);
-    return run_w4<64, 1, W4_MX, 8>(cx, c);
+    if (c.M <= 16) return w4_tiles<16, W4_MX, 4>(cx, c, kNever);
+    if (c.M <= 32) return w4_tiles<32, W4_MX, 4>(cx, c, kNever);
+    return w4_tiles<64, W4_MX, 8>(cx, c, kNever);
   }
-  if (c.M <= 4) return run_w4<8, 1, W4_CONVERT, 8>(cx, c);  // few warps have a token: groups of them hide it
-  if (c.M <= 8) return w4_convert<8, 8>(cx, c);
-  if (c.M <= kW4Convert) return w4_convert<16, 8>(cx, c);
-  if (c.M <= 32) return run_w4<32, 1, W4_READY, 4>(cx, c);
-  return run_w4<64, 1, W4_READY, 8>(cx, c);
+  if (c.M <= 4) return w4_tiles<8, W4_CONVERT, 8>(cx, c, kNever);  // groups of warps hide the conversion
+  if (c.M <= 8) return w4_tiles<8, W4_CONVERT, 8>(cx, c, 2);
+  if (c.M <= kW4Convert) return w4_tiles<16, W4_CONVERT, 8>(cx, c, 2);
+  if (c.M <= 32) return w4_tiles<32, W4_READY, 4>(cx, c, kNever);
+  return w4_tiles<64, W4_READY, 8>(cx, c, 12);
 }
 
 // ------------------------------------------------------------------ quantisation

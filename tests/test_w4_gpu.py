@@ -89,6 +89,19 @@ def test_linear_large(M):
         assert torch.equal(dg.dec_linear_w4(x.cuda(), W), y)  # the same bits from run to run
 
 
+@pytest.mark.parametrize("M,mx", [(1, False), (6, False), (16, False), (32, False), (64, False), (11, True),
+                                  (25, True), (64, True)])
+def test_linear_of_more_tiles_than_sms(M, mx):
+    """153 tiles of 128 outputs, an odd number, the last of 44."""
+    N, K = 152 * 128 + 44, 640
+    codes, scales = ref.random_codes(10, N, K)
+    W = dg.W4.pack(codes.cuda(), scales.cuda())
+    x = _mx8(M, M, K) if mx else (ref.activations(M, M, K),) * 2
+    y = dg.dec_linear_w4(x[0] if mx else x[0].cuda(), W)
+    want, a, spread = ref.linear(x[1], ref.weights(codes, scales))
+    _check(y, want, ref.linear_bound(want, a, spread, K, mx))
+
+
 def test_linear_of_tokens_with_a_far_larger_value():
     """Elements down to 2^-15 of the largest of their 32 are taken exactly: with
     a weight of 0 under the largest, only fp32 sums and the output round."""
