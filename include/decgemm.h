@@ -546,6 +546,7 @@ int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K
  * run; y is rounded once. A token with a value that is not finite gives NaN in
  * all its outputs. W is read while the previous kernel of the stream may still run, as
  * by dec_linear; dec_quant_w4 lets nothing start before it has ended.
+ * dec_last_choice, dec_last_grid and the probe say nothing of these calls.
  * Errors: DEC_EINVAL, DEC_EUNSUPPORTED (M > 64, K > 2^29, 2^24 units or more), DEC_ECUDA.
  *
  * dec_linear_w4_mx -- the same for tokens in 8 bits: x [M, K] e4m3, rows ldx bytes

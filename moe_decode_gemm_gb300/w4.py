@@ -55,6 +55,14 @@ def _is_matrix(t, dtype, index, rows, width):
     return ld if rows > 1 else width  # a single row's stride says nothing
 
 
+def _kept(stream, *tensors):
+    """Tensors made here for a call on ``stream``: their memory is not given out anew
+    before it has passed the call, whichever stream torch made them for."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _explain(what, t, dtype, shape, align):
     """Raise what is wrong with a matrix (its device last)."""
     import torch
@@ -168,6 +176,8 @@ class W4:
 
         _explain("codes", codes, torch.uint8, (None, None), 1)
         n, k = codes.shape
+        if codes.numel() and int(codes.max()) > 15:
+            raise ValueError("codes: expected 0 to 15, got %d" % int(codes.max()))
         _explain("scales", scales, torch.uint8, (n, -(-k // 32)), 1)
         nt, kc = -(-n // 128), -(-k // 128)
         c = codes.new_zeros((nt * 128, kc * 128))
@@ -199,14 +209,11 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
     rp = hp = None
     if residual is not None:
         if ok:
-            if residual.shape == shape and residual.dtype is bf and residual.get_device() == index \
-                    and residual.is_contiguous():
-                ldr = H
-            else:
-                ldr = _is_matrix(residual, bf, index, T, H)
+            ldr = _is_matrix(residual, bf, index, T, H)
             if h is None:
                 h = b._like(x) if ldx == H else b._empty((T, H), dtype=bf, device=b.device)
                 ldh = H
+                _kept(stream, h)
             else:
                 ldh = _is_matrix(h, bf, index, T, H)
             ok = ldr and ldr % 8 == 0 and ldh and ldh % 8 == 0
@@ -239,6 +246,7 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
             q = b._empty((T, H), dtype=b._f8, device=b.device)
             s = b._empty((T, H // 32), dtype=b._e8, device=b.device)
             out = MX8.__new__(MX8)
+            _kept(stream, q, s)
             out.q, out.s, out.shape, out._index = q, s, x.shape, index
             out._args = (q.data_ptr(), H, s.data_ptr(), H // 32)
         fn = lib().dec_rmsnorm_mx
@@ -247,6 +255,7 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         if out is None:
             out = b._like(x) if ldx == H else b._empty((T, H), dtype=bf, device=b.device)
             ldo = H
+            _kept(stream, out)
         fn = lib().dec_rmsnorm
         args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, out.data_ptr(), ldo, T, H)
     if T:
@@ -335,6 +344,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
                ("residual", residual, bf, shape, 1), ("W", W.q, torch.uint8, tuple(W.q.shape), 1))
     if y is None:
         y = b._empty((M, N), dtype=bf, device=b.device)
+        _kept(stream, y)
     if M:
         L = lib()
         rp = None if residual is None else residual.data_ptr()
@@ -346,8 +356,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
                 n = L.dec_linear_w4_work(M, K)
                 if n:
                     work = b._empty(n, dtype=b._u8, device=b.device)
-                    if stream is not None:
-                        work.record_stream(stream)
+                    _kept(stream, work)
                     wp = work.data_ptr()
             fn, args = L.dec_linear_w4, (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K, wp)
         if b._getdev() == index:
@@ -386,6 +395,7 @@ def dec_quant_w4(W, out=None, stream=None):
         nt, kc = -(-N // 128), -(-K // 128)
         out = W4.__new__(W4)._set(b._empty((nt, kc, 128, 64), dtype=b._u8, device=b.device),
                                   b._empty((nt, kc, 32, 4, 4), dtype=b._u8, device=b.device), N, K)
+        _kept(stream, out.q, out.s)
     elif type(out) is not W4:
         raise TypeError("out: expected a W4, got %s" % type(out).__name__)
     elif (out.n, out.k) != (N, K):

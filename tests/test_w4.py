@@ -68,6 +68,8 @@ def test_linear_w4_rejects(kw, exc, msg):
     (dict(w=_t(64, dtype=torch.float32)), TypeError, "w: expected torch.bfloat16"),
     (dict(w=_t(128)[::2]), ValueError, "w: needs unit column stride"),
     (dict(residual=_t(2, 32)), ValueError, "residual: expected shape [2, 64]"),
+    (dict(residual=[1.0]), TypeError, "residual: expected a torch tensor"),
+    (dict(x=_t(1, 64).expand(2, 64)), ValueError, "x: its rows overlap"),
     (dict(residual=_t(2, 64), h=_t(3, 64)), ValueError, "h: expected shape [2, 64]"),
     (dict(h=_t(2, 64)), ValueError, "h: given without a residual"),
     (dict(), ValueError, "x: expected a CUDA tensor"),
@@ -133,6 +135,13 @@ def test_pack_is_the_documented_layout(n, k):
     pad = torch.ones(-(-n // 128) * 128, -(-k // 128) * 128, dtype=torch.bool)
     pad[:n, :k] = False
     assert not ref.unpack(w.q, w.s, *pad.shape)[0][pad].any()
+
+
+def test_pack_rejects_what_is_no_code():
+    codes, scales = ref.random_codes(1, 20, 64)
+    codes[3, 5] = 16
+    with pytest.raises(ValueError, match="expected 0 to 15, got 16"):
+        dg.W4.pack(codes, scales)
 
 
 # ------------------------------------------------------------------ the C ABI

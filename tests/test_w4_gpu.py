@@ -116,6 +116,17 @@ def test_linear_of_tokens_with_a_far_larger_value():
     _check(y, want, ref.linear_bound(want, a, torch.zeros_like(a), K, False))
 
 
+@pytest.mark.parametrize("M", [3, 20])
+def test_linear_of_the_largest_bf16(M):
+    """The weights bring the products back: nothing overflows on the way."""
+    N, K = 100, 256
+    codes, scales = ref.random_codes(8, N, K)
+    x = ref.normal(9, M, K).sign() * 3.3e38
+    y = dg.dec_linear_w4(x.to(BF).cuda(), dg.W4.pack(codes.cuda(), (scales - 20).cuda()))
+    want, a, spread = ref.linear(x.to(BF), ref.weights(codes, scales - 20))
+    _check(y, want, ref.linear_bound(want, a, spread, K, False))
+
+
 @pytest.mark.parametrize("power", [-120, -60, 60, 100])
 def test_linear_of_tokens_near_the_ends_of_bf16(power):
     M, N, K = 5, 200, 512
@@ -230,6 +241,32 @@ def test_norm_in_8_bits(rows, H):
     y, hh = dg.dec_rmsnorm_mx(x.cuda(), w.cuda(), res.cuda())
     _check_mx(y, want)
     assert torch.equal(hh.double().cpu(), h)
+
+
+@pytest.mark.parametrize("rows,H", [(2, 7168), (400, 1024), (1000, 2048), (40, 16384)])
+def test_norm_in_8_bits_is_rounded_once(rows, H):
+    """Every value and scale is the definition's: fp32 alone puts one in a million on
+    the other side of a rounding border."""
+    x, w, res = ref.activations(H, rows, H), ref.normal(2, H), ref.normal(3, rows, H)
+    got, _ = dg.dec_rmsnorm_mx(x.cuda(), w.cuda(), res.cuda())
+    _, want = ref.norm(x, w, res)
+    g = want.reshape(rows, -1, 32)
+    e = ref.least_exponent(g.abs().amax(2), 448.0)
+    v = g / torch.exp2(e)[..., None]
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=1e-30))).clamp(min=-6) - 3)
+    assert torch.equal(got.s.view(torch.uint8).cpu().double() - 127, e)
+    assert torch.equal(got.q.double().cpu(), (torch.round(v / step) * step).reshape(rows, H))
+
+
+def test_norm_of_exact_products():
+    """Where nothing is cut off nothing is marked as cut off: borders and scales of
+    exact values (mean 1, eps 0)."""
+    x = ref.normal(4, 3, 64).sign()
+    w = torch.tensor([1.75, 1.0625, 1.1875, 0.4375, 0.0, 1.0, -1.0625, 0.5] * 8).to(BF)
+    got = dg.dec_rmsnorm_mx(x.cuda(), w.cuda(), eps=0.0)
+    v = x.float() * w.float()
+    assert (got.s.view(torch.uint8) == 127 - 8).all()      # 1.75 = 448 * 2^-8
+    assert torch.equal(got.q.cpu().view(torch.uint8), (v * 256).to(F8).view(torch.uint8))
 
 
 @pytest.mark.parametrize("mx", [False, True])

@@ -60,6 +60,16 @@ def test_steps(mx):
         o, a, r, out = (torch.empty(M, H, dtype=BF, device="cuda") for _ in range(4))
         got = w4_layer(L, x, kv, rope, qkv, o, a, r, out, K, mx=mx)
         assert got is out and dg.sync_check() == dg.DEC_OK
+        # on a stream of its own, its passing tensors' memory wanted at once by another
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        q2, o2, a2, r2, out2 = (torch.empty_like(t) for t in (qkv, o, a, r, out))
+        for _ in range(8):
+            w4_layer(L, x, kv, rope, q2, o2, a2, r2, out2, K, mx=mx, stream=side)
+            torch.full((M, 4 * H), float("nan"), dtype=BF, device="cuda")
+            torch.full((M, H), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out2, out) and torch.equal(a2, a) and dg.sync_check(side) == dg.DEC_OK
         # the norm and the first projection
         n = (dg.dec_rmsnorm_mx if mx else dg.dec_rmsnorm)(x, L.w1)
         values = ref.mx8_values(n.q.cpu(), n.s.cpu()) if mx else n.cpu()
