@@ -241,7 +241,7 @@ cudaError_t launch_norm(const Ctx& cx, const NormCall& c) {
   const int nv = c.H / 8;
   // As few vectors a thread as all rows' threads fit on the SMs at once with, up to four
   // (3001 rows of 2048 in 8 bits: a warp of eight vectors to each 9.9 us, two warps of
-  // four 6.1); short rows by a warp each, as an SM holds no more than 32 CTAs.
+  // four 8.7); short rows by a warp each, as an SM holds no more than 32 CTAs.
   int per = 1;
   while (per < 8 && (long long)c.rows * nv > 2048LL * cx.sms * per) per *= 2;
   if (nv <= 256 && (per == 8 || (nv <= 64 && c.rows > 2 * cx.sms))) {

@@ -716,7 +716,7 @@ static cudaError_t run_w4(const Ctx& cx, const W4Call& c) {
 
 // bf16 tokens are converted by each CTA up to 16 (one launch, no work space); beyond,
 // by a kernel before (about 2 us): in each CTA 64 tokens of 16384 x 7168 took 27 us, so
-// 19.6, 32 tokens 20.3 and 15.5.
+// 19.5, 32 tokens 20.3 and 16.0.
 constexpr int kW4Convert = 16;
 
 size_t w4_work_bytes(int M, int K) {
