@@ -12,8 +12,13 @@
 // The 8-bit output's groups of 32 are 4 lanes. An e4m3 has 4 significant bits, so
 // an error of one fp32 step in y moves about one in a million of them to the
 // other side of a rounding border, where the whole value changes by a sixteenth: for
-// it the sum, the root and the product are carried in two fp32 numbers, and y is
-// rounded once.
+// it the sum and the root are carried in two fp32 numbers, and products near a border
+// are rounded from what is exact.
+//
+// GB300, us (in brackets the bytes at the measured copy rate): 8000 x 7168 with
+// residual 67.4 (67.7), in 8 bits 66.6 (59.5: instructions); 64 x 7168 2.3 and 3.0
+// (latency); 3001 x 2048 5.7 (3.6) and 7.8 (2.8: one wave, load, sum, output one after
+// another). In 8 bits with every product in two numbers 73, 3.5 and 8.9.
 #include "launch.h"
 #include "launch_util.cuh"
 #include "mx_common.cuh"
@@ -26,7 +31,7 @@ struct NormArgs {
   uint8_t *q, *sc;               // 8-bit output
   long long ldx, ldres, ldh, ldy, ldq, ldsc;
   int H;
-  float eps;
+  float eps, inv;  // inv = 1 / H
   int* status;
   int rows;
 };
@@ -51,11 +56,11 @@ __device__ __forceinline__ Two add_two(Two a, Two b) {
   return s;
 }
 
-// 1 / sqrt(sum / n + eps): one Newton step from rsqrtf's value, whose error is taken
-// exactly.
-__device__ __forceinline__ Two root_two(Two sum, float n, float eps) {
-  const float q = __fdiv_rn(sum.hi, n);
-  const Two m = add_two(Two{q, __fdiv_rn(fmaf(-q, n, sum.hi) + sum.lo, n)}, eps);
+// 1 / sqrt(sum / n + eps), inv = 1 / n: one Newton step from rsqrtf's value, whose error
+// is taken exactly, as is the quotient's (n has 17 bits at most).
+__device__ __forceinline__ Two root_two(Two sum, float n, float inv, float eps) {
+  const float q = __fmul_rn(sum.hi, inv);
+  const Two m = add_two(Two{q, (fmaf(-q, n, sum.hi) + sum.lo) * inv}, eps);
   const float f = rsqrtf(m.hi), p = __fmul_rn(f, f), pe = fmaf(f, f, -p);
   const float e = fmaf(-m.hi, p, 1.f) - fmaf(m.hi, pe, m.lo * p);  // 1 - m f^2
   // (a mean that is not finite, or 0: f alone says what the result is)
@@ -76,37 +81,112 @@ DG_F32X2(pair_add, "add.rn.f32x2")
 DG_F32X2(pair_sub, "sub.rn.f32x2")
 DG_F32X2(pair_mul, "mul.rn.f32x2")
 #undef DG_F32X2
-template <bool RZ>
-__device__ __forceinline__ float2 pair_fma(float2 a, float2 b, float2 c) {  // RZ: rounded towards 0
+__device__ __forceinline__ float2 pair_fma(float2 a, float2 b, float2 c) {
   float2 y;
-  if constexpr (RZ)
-    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
-        "fma.rz.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
-        : "=f"(y.x), "=f"(y.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  else
-    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
-        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
-        : "=f"(y.x), "=f"(y.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+      "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return y;
 }
 
-// a * f for two exact a: cut to fp32, the last bit set where something was cut off, so
-// that a later rounding to fewer bits sees on which side of a border the product lies.
-__device__ __forceinline__ float2 times_two(float2 a, Two f) {
-  const float2 hi = make_float2(f.hi, f.hi), c = pair_mul(a, make_float2(f.lo, f.lo));
-  const float2 y = pair_fma<true>(a, hi, c);
-  const float2 r = pair_add(pair_fma<false>(a, hi, make_float2(-y.x, -y.y)), c);
-  return make_float2(__uint_as_float(__float_as_uint(y.x) | (r.x != 0.f ? 1u : 0u)),
-                     __uint_as_float(__float_as_uint(y.y) | (r.y != 0.f ? 1u : 0u)));
+// The largest magnitude of three, NaN if one is.
+__device__ __forceinline__ float most_of(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// The products of eight pairs of bf16 (each exact) with f, to fp32.
+__device__ __forceinline__ void times_root(const uint4& h, const uint4& w, Two f, float2 (&y)[4]) {
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = pair_mul(make_float2(bf16lo(hw[j]), bf16hi(hw[j])), make_float2(bf16lo(ww[j]), bf16hi(ww[j])));
+    y[j] = pair_fma(p, make_float2(f.hi, f.hi), pair_mul(p, make_float2(f.lo, f.lo)));
+  }
+}
+
+// The same product, where it is not exact to the neighbour with an odd last bit, so that
+// a rounding of it to fewer bits sees on which side of a border the product lies. (A rest
+// of 2^-40 is the root's own error: the product is y.)
+__device__ __forceinline__ float to_odd(float y, float x, float g, Two f) {
+  const float p = x * g, r = fmaf(p, f.hi, -y) + p * f.lo;
+  uint32_t b = __float_as_uint(y);
+  if (!(b & 1) && fabsf(r) > fabsf(y) * 0x1p-40f) b += (r > 0.f) == (y > 0.f) ? 1u : ~0u;
+  return __uint_as_float(b);
+}
+__device__ __forceinline__ void to_odd(const uint4& h, const uint4& w, Two f, float2 (&y)[4]) {
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    y[j] = make_float2(to_odd(y[j].x, bf16lo(hw[j]), bf16lo(ww[j]), f),
+                       to_odd(y[j].y, bf16hi(hw[j]), bf16hi(ww[j]), f));
+}
+
+// The largest magnitude (its bits) of the 32 values that four lanes hold.
+__device__ __forceinline__ uint32_t group_most(const float2 (&y)[4]) {
+  const float m3 = most_of(most_of(y[0].x, y[0].y, y[1].x), y[1].y, y[2].x);
+  uint32_t m = __float_as_uint(most_of(most_of(m3, y[2].y, y[3].x), y[3].y, 0.f));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+
+__device__ __forceinline__ int group_exponent(uint32_t most) {
+  const int e = mx_exponent_e4m3(__uint_as_float(most));
+  return e < -127 ? -127 : e;
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const float2 (&y)[4], float s) {
+  const float2 ss = make_float2(s, s);
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 u = pair_mul(y[j], ss);
+    q[j] = pack_e4m3(u.x, u.y);
+  }
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+}
+
+// Eight values of a group of 32 (four lanes) in 8 bits, and the group's scale byte.
+// fp32 products are off by half a step: where 2^-22 more and 2^-22 less are the same
+// e4m3, so is the product. Otherwise (one warp in 700), where the largest is just what
+// a scale can hold, or where products are below 2^-100 and might not be as near as that,
+// the warp rounds them anew from their odd neighbours.
+__device__ __forceinline__ uint2 norm_e4m3(const uint4& h, const uint4& w, Two f, int* byte) {
+  float2 y[4];
+  times_root(h, w, f, y);
+  uint32_t m = group_most(y);
+  uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);  // NaN, as the scale
+  *byte = 255;
+  bool near = false;
+  if (!not_finite(__uint_as_float(m))) {
+    const int e = group_exponent(m);
+    const float s = pow2_f(-e);
+    q = to_e4m3(y, s * (1.f + 0x1p-22f));
+    const uint2 less = to_e4m3(y, s * (1.f - 0x1p-22f));
+    *byte = e + 127;
+    near = q.x != less.x || q.y != less.y || (m & 0x7FFFFFu) == 0x600000u || m - 1u < 27u << 23;
+  }
+  if (__any_sync(0xffffffffu, near)) {
+    to_odd(h, w, f, y);
+    m = group_most(y);
+    if (!not_finite(__uint_as_float(m))) {
+      const int e = group_exponent(m);
+      q = to_e4m3(y, pow2_f(-e));
+      *byte = e + 127;
+    }
+  }
+  return q;
 }
 
 constexpr int kNormWarps = 8;   // rows of a CTA where a warp takes one
 
 // VPT: vectors of 8 values a thread holds; MX: 8-bit output; WARP: a warp to a row.
+// 48 registers: an SM holds 20 CTAs of 64 threads, 3001 rows of 2048 run at once (in
+// 8 bits 8.0 us with 57 registers, so 7.8; 8000 x 7168 69.0 and 66.6).
 template <int VPT, bool MX, bool WARP>
-__global__ void __launch_bounds__(WARP ? kNormWarps * 32 : 1024) norm_kernel(const NormArgs a) {
+__global__ void __maxnreg__(WARP ? 80 : VPT > 4 ? 64 : 48) norm_kernel(const NormArgs a) {
   constexpr int BATCH = VPT < 4 ? VPT : 4;  // vectors loaded at once
   __shared__ float s_hi[32], s_lo[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -117,7 +197,7 @@ __global__ void __launch_bounds__(WARP ? kNormWarps * 32 : 1024) norm_kernel(con
   griddep_wait();
   if (WARP && row >= a.rows) return;
   uint4 h[VPT], w[VPT];
-  if (VPT == 1)  // few rows: the weights' way is the same as the row's
+  if (VPT <= 4)  // on its way with the row (8000 x 7168 in 8 bits 69.7 us, so 69.0)
     w[0] = t < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + t) : make_uint4(0u, 0u, 0u, 0u);
   float sum = 0.f;
   float2 sq_hi = make_float2(0.f, 0.f), sq_lo = sq_hi;  // of even and odd columns
@@ -157,71 +237,47 @@ __global__ void __launch_bounds__(WARP ? kNormWarps * 32 : 1024) norm_kernel(con
   }
   Two sum2 = {sum, 0.f};
   if (MX) sum2 = add_two(Two{sq_hi.x, sq_lo.x}, Two{sq_hi.y, sq_lo.y});
-  auto reduce = [&] {
+  auto reduce = [&](int lanes) {  // of each `lanes` side by side, a power of two
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
+      if (off >= lanes) continue;
       const float o = __shfl_xor_sync(0xffffffffu, sum2.hi, off);
       if (MX) sum2 = add_two(sum2, Two{o, __shfl_xor_sync(0xffffffffu, sum2.lo, off)});
       else sum2.hi += o;
     }
   };
-  reduce();
+  reduce(32);
   if (!WARP) {
     if (lane == 0) {
       s_hi[warp] = sum2.hi;
       s_lo[warp] = sum2.lo;
     }
     __syncthreads();
-    sum2.hi = lane < nt / 32 ? s_hi[lane] : 0.f;
-    sum2.lo = MX && lane < nt / 32 ? s_lo[lane] : 0.f;
-    reduce();
+    const int warps = nt / 32, lanes = warps > 1 ? 2 << (31 - __clz(warps - 1)) : 1, from = lane & (lanes - 1);
+    sum2.hi = from < warps ? s_hi[from] : 0.f;
+    sum2.lo = MX && from < warps ? s_lo[from] : 0.f;
+    reduce(lanes);
   }
-  const Two f = MX ? root_two(sum2, (float)a.H, a.eps) : Two{rsqrtf(sum2.hi / (float)a.H + a.eps), 0.f};
+  const Two f = MX ? root_two(sum2, (float)a.H, a.inv, a.eps) : Two{rsqrtf(sum2.hi / (float)a.H + a.eps), 0.f};
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = t + i * nt;
-    if (VPT > 1) w[i] = v < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + v) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t* hw = reinterpret_cast<const uint32_t*>(&h[i]);
-    const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w[i]);
-    float y[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 x = make_float2(bf16lo(hw[j]), bf16hi(hw[j])), g = make_float2(bf16lo(ww[j]), bf16hi(ww[j]));
-      if (MX) {  // (the product of two bf16 is exact)
-        const float2 p = times_two(pair_mul(x, g), f);
-        y[2 * j] = p.x;
-        y[2 * j + 1] = p.y;
-      } else {
-        y[2 * j] = x.x * f.hi * g.x;
-        y[2 * j + 1] = x.y * f.hi * g.y;
-      }
-    }
+    if (VPT > 4 || i > 0) w[i] = v < nv ? __ldg(reinterpret_cast<const uint4*>(a.w) + v) : make_uint4(0u, 0u, 0u, 0u);
     if constexpr (MX) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      int b = 255;
-      uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);  // NaN, as the scale
-      if (!not_finite(__uint_as_float(m))) {
-        int e = mx_exponent_e4m3(__uint_as_float(m));
-        e = e < -127 ? -127 : e;
-        b = e + 127;
-        const float s = pow2_f(-e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= s;
-        q.x = pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16;
-        q.y = pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16;
-      }
+      int b;
+      const uint2 q = norm_e4m3(h[i], w[i], f, &b);
       if (v < nv) {
         *reinterpret_cast<uint2*>(a.q + norm_at(a, row, a.ldq, v * 8, a.H)) = q;
         if (!(v & 3)) a.sc[norm_at(a, row, a.ldsc, v / 4, a.H / kMxGroup)] = (uint8_t)b;
       }
     } else if (v < nv) {
-      *reinterpret_cast<uint4*>(a.y + norm_at(a, row, a.ldy, v * 8, a.H)) =
-          make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                     pack_bf16(y[6], y[7]));
+      const uint32_t* hw = reinterpret_cast<const uint32_t*>(&h[i]);
+      const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w[i]);
+      uint32_t y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        y[j] = pack_bf16(bf16lo(hw[j]) * f.hi * bf16lo(ww[j]), bf16hi(hw[j]) * f.hi * bf16hi(ww[j]));
+      *reinterpret_cast<uint4*>(a.y + norm_at(a, row, a.ldy, v * 8, a.H)) = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
 }
@@ -237,11 +293,11 @@ cudaError_t launch_norm(const Ctx& cx, const NormCall& c) {
   const NormArgs a = {static_cast<const uint16_t*>(c.x), static_cast<const uint16_t*>(c.res),
                       static_cast<const uint16_t*>(c.w), static_cast<uint16_t*>(c.h),
                       static_cast<uint16_t*>(c.y), static_cast<uint8_t*>(c.q), static_cast<uint8_t*>(c.sc),
-                      c.ldx, c.ldres, c.ldh, c.ldy, c.ldq, c.ldsc, c.H, c.eps, cx.status, c.rows};
+                      c.ldx, c.ldres, c.ldh, c.ldy, c.ldq, c.ldsc, c.H, c.eps, 1.f / (float)c.H, cx.status, c.rows};
   const int nv = c.H / 8;
   // As few vectors a thread as all rows' threads fit on the SMs at once with, up to four
-  // (3001 rows of 2048 in 8 bits: a warp of eight vectors to each 9.9 us, two warps of
-  // four 8.7); short rows by a warp each, as an SM holds no more than 32 CTAs.
+  // (3001 rows of 2048 in 8 bits: a warp of eight vectors to each 8.1 us, two warps of
+  // four 7.8); short rows by a warp each, as an SM holds no more than 32 CTAs.
   int per = 1;
   while (per < 8 && (long long)c.rows * nv > 2048LL * cx.sms * per) per *= 2;
   if (nv <= 256 && (per == 8 || (nv <= 64 && c.rows > 2 * cx.sms))) {

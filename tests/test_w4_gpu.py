@@ -269,6 +269,33 @@ def test_norm_of_exact_products():
     assert torch.equal(got.q.cpu().view(torch.uint8), (v * 256).to(F8).view(torch.uint8))
 
 
+def test_norm_of_rows_of_one_size():
+    """Roots that are rational (rows of +-c, eps 0): products that lie on a border are
+    neither rounded up nor given a larger scale."""
+    c = torch.arange(1, 128, 2).to(BF)[:, None]
+    x = c * ref.normal(5, 64, 96).sign()
+    w = torch.tensor([1.75, 1.0625, 1.1875, 0.4375, 0.0, 1.0, -1.0625, 0.5] * 12).to(BF)
+    got = dg.dec_rmsnorm_mx(x.cuda(), w.cuda(), eps=0.0)
+    v = x.float().sign() * w.float()
+    assert (got.s.view(torch.uint8) == 127 - 8).all()
+    assert torch.equal(got.q.cpu().float(), (v * 256).to(F8).float())
+
+
+def test_norm_of_the_least_products():
+    """Where products are below fp32's normal numbers the 8-bit values still are the
+    definition's, as near as fp32's least step."""
+    x, w = ref.normal(6, 16, 256), (ref.normal(7, 256).float() * 2.0 ** -124).to(BF)
+    x[8:] *= 2.0 ** -4
+    _, want = ref.norm(x, w)
+    got = dg.dec_rmsnorm_mx(x.cuda(), w.cuda())
+    s = got.s.view(torch.uint8).cpu().double() - 127
+    have = got.q.double().cpu().reshape(16, 8, 32) * torch.exp2(s)[..., None]
+    want = want.reshape(16, 8, 32)
+    # half a step of an e4m3 (2^-4 of the value, 2^-10 of the scale below the normal
+    # ones) and a step of fp32's least numbers
+    assert ((have - want).abs() <= 2.0 ** -4 * want.abs() + 2.0 ** -10 * torch.exp2(s)[..., None] + 2.0 ** -148).all()
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_norm_in_place(mx):
     """h over the residual or x, y over x; rows behind the last are left alone."""
