@@ -280,6 +280,16 @@ int dec_selftest_timeout(long long ns, void* stream);
 int dec_debug_build(void);
 int dec_debug_check_site(int* line, long long* index);
 
+/*
+ * dec_debug_stall -- of the index-checking build: with on != 0 the calls of
+ * dec_linear_w4 and dec_linear_w4_mx from then on wait in vain for one more arrival
+ * on their tokens, give up after the wait bound, and end without a result;
+ * dec_sync_check then returns DEC_ETIMEOUT. Exercises their way out without
+ * faulting or hanging the GPU. Returns what was set before (0 or 1), or
+ * DEC_EUNSUPPORTED from the other build.
+ */
+int dec_debug_stall(int on);
+
 /* dec_launch_count -- kernels launched by this library since load (all threads). */
 long long dec_launch_count(void);
 

@@ -35,6 +35,7 @@ EXPORTS = [
     "dec_strerror", "dec_sync_check", "dec_set_wait_timeout_ns", "dec_selftest_timeout",
     "dec_launch_count", "dec_probe_begin", "dec_probe_end", "dec_shutdown", "dec_version",
     "dec_linear_noalloc", "dec_debug_build", "dec_debug_check_site",
+    "dec_debug_stall",
     "kv_append", "kv_attention", "kv_last_attention", "kv_resize", "kv_free", "kv_fork", "kv_copy",
     "kv_compact", "dec_rmsnorm", "dec_rmsnorm_mx", "dec_linear_w4", "dec_linear_w4_work", "dec_linear_w4_mx", "dec_quant_w4",
 ]
@@ -102,6 +103,7 @@ def _configure(L):
         "dec_debug_build": (I, []),
         "dec_debug_check_site": (I, [ctypes.POINTER(ctypes.c_int),
                                      ctypes.POINTER(ctypes.c_longlong)]),
+        "dec_debug_stall": (I, [I]),
         "kv_append": (I, [P, P, LL, P, P, F, P, I, I, I, P, P, LL, I, I, P]),
         "kv_attention": (I, [P, P, LL, P, LL, P, I, I, F, I, P]),
         "kv_last_attention": (I, []),

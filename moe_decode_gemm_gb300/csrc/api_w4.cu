@@ -86,4 +86,9 @@ int dec_linear_w4_mx(const void* x, int64_t ldx, const void* xscales, int64_t ld
   return linear({x, xscales, wq, wscales, res, y, ldx, ldxscales, M, N, K, nullptr}, stream);
 }
 
+int dec_debug_stall(int on) {
+  const int old = w4_stall(on);
+  return old < 0 ? DEC_EUNSUPPORTED : old;
+}
+
 }  // extern "C"

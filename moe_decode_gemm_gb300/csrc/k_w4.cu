@@ -326,36 +326,36 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
     const uint32_t xa = __shfl_sync(~0u, (uint32_t)desc + (smem_u32(xring) >> 4), 0);
     const uint32_t idesc = umma_idesc_mx(Sh::kRows, 0);
     int ws = 0, wp = 0, xs = 0, xp = 0;
+    // A wait that runs out ends both loops: a slot that was not read is not given back,
+    // or its next copy would be issued beside the one still on its way.
     bool ok = true, ready = false;
     for (int kx = 0; kx < nx; ++kx) {
       const bool two = (kx + 1) * kPair <= nk;
-      if (ok) ok = mbar_wait(&xfull[xs], xp, a.timeout_ns, a.status);
+      ok = mbar_wait(&xfull[xs], xp, a.timeout_ns, a.status);
+      if (!ok) break;
       const uint32_t xd = xa + xs * (Sh::kXSlot >> 4), sx = sfx + 4 * kPair * xs;
       tc_fence_after();
-      if (ok) {
+#pragma unroll
+      for (int h = 0; h < kPair; ++h)
+        tmem_copy_scales_elect(leader, sx + 4 * h, xd + ((kPair * Sh::kXChunk + h * kW4Scales) >> 4));
+      for (int rt = 0; rt < nrt; ++rt) {
+        if (!ready) ok = mbar_wait(&wfull[ws], wp, a.timeout_ns, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t wd = wa + ws * (Sh::kWSlot >> 4), sw = sfw + 4 * kPair * ws, d = tm + rt * Sh::kRows;
 #pragma unroll
         for (int h = 0; h < kPair; ++h)
-          tmem_copy_scales_elect(leader, sx + 4 * h, xd + ((kPair * Sh::kXChunk + h * kW4Scales) >> 4));
-      }
-      for (int rt = 0; rt < nrt; ++rt) {
-        if (ok && !ready) ok = mbar_wait(&wfull[ws], wp, a.timeout_ns, a.status);
-        tc_fence_after();
-        if (ok) {
-          const uint32_t wd = wa + ws * (Sh::kWSlot >> 4), sw = sfw + 4 * kPair * ws, d = tm + rt * Sh::kRows;
+          if (h == 0 || two)
+            tmem_copy_scales_elect(leader, sw + 4 * h, wd + ((kPair * kW4Spread + h * kW4Scales) >> 4));
 #pragma unroll
-          for (int h = 0; h < kPair; ++h)
-            if (h == 0 || two)
-              tmem_copy_scales_elect(leader, sw + 4 * h, wd + ((kPair * kW4Spread + h * kW4Scales) >> 4));
+        for (int h = 0; h < kPair; ++h)
+          if (h == 0 || two) {
+            const uint32_t wh = wd + (h * kW4Spread >> 4), xh = xd + (h * Sh::kXChunk >> 4);
 #pragma unroll
-          for (int h = 0; h < kPair; ++h)
-            if (h == 0 || two) {
-              const uint32_t wh = wd + (h * kW4Spread >> 4), xh = xd + (h * Sh::kXChunk >> 4);
-#pragma unroll
-              for (int g = 0; g < 4; ++g)
-                umma_mx_elect(leader, d, wh + 2 * g, d_hi, xh + 2 * g, d_hi, idesc | umma_mx_group(g), sw + 4 * h,
-                              sx + 4 * h, (g > 0 || h > 0 || kx > 0) ? 1u : 0u);
-            }
-        }
+            for (int g = 0; g < 4; ++g)
+              umma_mx_elect(leader, d, wh + 2 * g, d_hi, xh + 2 * g, d_hi, idesc | umma_mx_group(g), sw + 4 * h,
+                            sx + 4 * h, (g > 0 || h > 0 || kx > 0) ? 1u : 0u);
+          }
         uint64_t* done = &wempty[ws];
         if (++ws == WS) {
           ws = 0;
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
         ready = mbar_test_wait(&wfull[ws], wp);
         umma_commit_elect(leader, done);
       }
+      if (!ok) break;
       umma_commit_elect(leader, &xempty[xs]);
       if (++xs == XS) {
         xs = 0;
@@ -622,6 +623,13 @@ __global__ void __launch_bounds__(W4Shape<MT, RT, MODE, CW>::kThreads, 1)
   }
 }
 
+#ifdef DEC_DEBUG
+static std::atomic<int> g_w4_stall{0};  // arrivals that slots of tokens wait for in vain
+int w4_stall(int on) { return g_w4_stall.exchange(on ? 1 : 0); }
+#else
+int w4_stall(int) { return -1; }
+#endif
+
 // CTAs that share a set of tiles: the most, up to 8 (the portable cluster size)
 // and one per pair of units, for which every cluster runs at once. (A GPU's SMs come
 // in groups that a cluster cannot cross: of 152 SMs, 15 clusters of 8 CTAs hold at
@@ -692,6 +700,9 @@ static cudaError_t run_w4(const Ctx& cx, const W4Call& c) {
   } else {
     a.xarrivals = MODE == W4_MX ? 1 + (MT + 31) / 32 : 1;
   }
+#ifdef DEC_DEBUG
+  a.xarrivals += g_w4_stall.load(std::memory_order_relaxed);
+#endif
   a.status = cx.status;
   a.timeout_ns = cx.timeout_ns;
   CUtensorMap wmap, wmap1, xmap;

@@ -276,6 +276,7 @@ struct W4Call {
   void* work;               // w4_work_bytes(M, K) bytes for bf16 tokens
 };
 size_t w4_work_bytes(int M, int K);
+int w4_stall(int on);       // dec_debug_stall; -1 where the build has none
 cudaError_t launch_w4_linear(const Ctx& cx, const W4Call& c);
 cudaError_t launch_w4_quant(const Ctx& cx, const void* W, long long ldw, void* q, void* s, int N, int K);
 
