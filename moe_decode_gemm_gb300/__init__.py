@@ -188,6 +188,26 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made(stream, device, make, *args, seen=True, **kw):
+    """``make(*args, device=device, **kw)``, a tensor that a call on ``stream`` writes.
+
+    It is made on that stream: a block that was freed on the current one may still be
+    read or written there. Where the caller gets to see it, its memory is not given out
+    anew either before the current stream has passed what was done with it there."""
+    if stream is None or device.type != "cuda":
+        return make(*args, device=device, **kw)
+    import torch
+
+    now = torch.cuda.current_stream(device)
+    if stream.cuda_stream == now.cuda_stream:
+        return make(*args, device=device, **kw)
+    with torch.cuda.stream(stream):
+        t = make(*args, device=device, **kw)
+    if seen:
+        t.record_stream(now)
+    return t
+
+
 # ---------------------------------------------------------------- the hot path
 def dec_linear(x, W, y=None, stream=None, residual=None):
     """y = x·Wᵀ (bf16), or y = residual + x·Wᵀ when ``residual`` is given.

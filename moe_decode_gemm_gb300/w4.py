@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _check, lib
+from . import _check, _made, lib
 from .paged import _Handle
 
 _handles = {}
@@ -53,14 +53,6 @@ def _is_matrix(t, dtype, index, rows, width):
     if one != 1 and width > 1:
         return 0
     return ld if rows > 1 else width  # a single row's stride says nothing
-
-
-def _kept(stream, *tensors):
-    """Tensors made here for a call on ``stream``: their memory is not given out anew
-    before it has passed the call, whichever stream torch made them for."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
 
 
 def _explain(what, t, dtype, shape, align):
@@ -192,6 +184,18 @@ class W4:
 # ---------------------------------------------------------------- the calls
 # (The calls of a decode step are short: what they pass is looked over in few steps,
 # and _wrong says what is the matter.)
+def _new(b, shape, dtype, stream, seen=True):
+    """A tensor for a call on ``stream``."""
+    if stream is None:
+        return b._empty(shape, dtype=dtype, device=b.device)
+    return _made(stream, b.device, b._empty, shape, dtype=dtype, seen=seen)
+
+
+def _rows_of(b, x, ldx, stream):
+    """A matrix of x's shape for a call on ``stream``."""
+    return b._like(x) if stream is None and ldx == x.shape[1] else _new(b, x.shape, b._bf16, stream)
+
+
 def _norm(what, mx, x, w, residual, h, out, eps, stream):
     try:
         T, H = shape = x.shape
@@ -211,9 +215,8 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         if ok:
             ldr = _is_matrix(residual, bf, index, T, H)
             if h is None:
-                h = b._like(x) if ldx == H else b._empty((T, H), dtype=bf, device=b.device)
+                h = _rows_of(b, x, ldx, stream)
                 ldh = H
-                _kept(stream, h)
             else:
                 ldh = _is_matrix(h, bf, index, T, H)
             ok = ldr and ldr % 8 == 0 and ldh and ldh % 8 == 0
@@ -243,19 +246,17 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         if H % 32 or not H:
             raise ValueError("x: an 8-bit output needs a width that is a multiple of 32, got %d" % H)
         if out is None:
-            q = b._empty((T, H), dtype=b._f8, device=b.device)
-            s = b._empty((T, H // 32), dtype=b._e8, device=b.device)
+            q = _new(b, (T, H), b._f8, stream)
+            s = _new(b, (T, H // 32), b._e8, stream)
             out = MX8.__new__(MX8)
-            _kept(stream, q, s)
             out.q, out.s, out.shape, out._index = q, s, x.shape, index
             out._args = (q.data_ptr(), H, s.data_ptr(), H // 32)
         fn = lib().dec_rmsnorm_mx
         args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, *out._args, T, H)
     else:
         if out is None:
-            out = b._like(x) if ldx == H else b._empty((T, H), dtype=bf, device=b.device)
+            out = _rows_of(b, x, ldx, stream)
             ldo = H
-            _kept(stream, out)
         fn = lib().dec_rmsnorm
         args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, out.data_ptr(), ldo, T, H)
     if T:
@@ -343,8 +344,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
         _wrong(W.q.device, ("x", xt, dt, (None, K), al), ("y", y, bf, shape, 1),
                ("residual", residual, bf, shape, 1), ("W", W.q, torch.uint8, tuple(W.q.shape), 1))
     if y is None:
-        y = b._empty((M, N), dtype=bf, device=b.device)
-        _kept(stream, y)
+        y = _new(b, (M, N), bf, stream)
     if M:
         L = lib()
         rp = None if residual is None else residual.data_ptr()
@@ -355,8 +355,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
             if M > 16:
                 n = L.dec_linear_w4_work(M, K)
                 if n:
-                    work = b._empty(n, dtype=b._u8, device=b.device)
-                    _kept(stream, work)
+                    work = _new(b, n, b._u8, stream, seen=False)
                     wp = work.data_ptr()
             fn, args = L.dec_linear_w4, (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K, wp)
         if b._getdev() == index:
@@ -393,9 +392,8 @@ def dec_quant_w4(W, out=None, stream=None):
         _wrong(None, ("W", W, torch.bfloat16, (None, None), 8))
     if out is None:
         nt, kc = -(-N // 128), -(-K // 128)
-        out = W4.__new__(W4)._set(b._empty((nt, kc, 128, 64), dtype=b._u8, device=b.device),
-                                  b._empty((nt, kc, 32, 4, 4), dtype=b._u8, device=b.device), N, K)
-        _kept(stream, out.q, out.s)
+        out = W4.__new__(W4)._set(_new(b, (nt, kc, 128, 64), b._u8, stream),
+                                  _new(b, (nt, kc, 32, 4, 4), b._u8, stream), N, K)
     elif type(out) is not W4:
         raise TypeError("out: expected a W4, got %s" % type(out).__name__)
     elif (out.n, out.k) != (N, K):
