@@ -227,7 +227,7 @@ def dec_linear(x, W, y=None, stream=None, residual=None):
         raise ValueError("W: expected [N, %d], got shape %s" % (K, tuple(W.shape)))
     N = W.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _made(stream, x.device, torch.empty, (M, N), dtype=torch.bfloat16)
     _need(y, "y", shape=(M, N))
     if residual is not None:
         _need(residual, "residual", shape=(M, N))
@@ -275,7 +275,7 @@ def dec_linear_splitk(x, W, S, y=None, stream=None):
         raise ValueError("W: expected [N, %d], got shape %s" % (K, tuple(W.shape)))
     N = W.shape[0]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _made(stream, x.device, torch.empty, (M, N), dtype=torch.bfloat16)
     _need(y, "y", shape=(M, N))
     _on_one_gpu(x=x, W=W, y=y)
     _check(lib().dec_linear_splitk(_ptr(x), _ptr(W), _ptr(y), M, N, K, int(S), _stream(stream)),
@@ -309,7 +309,7 @@ def moe_decode(x, Wr, W13, W2, Ws13, Ws2, topk, out=None, topk_idx=None, topk_w=
         _need(Ws13, "Ws13", shape=(2 * I, H))
         _need(Ws2, "Ws2", shape=(H, I))
     if out is None:
-        out = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+        out = _made(stream, x.device, torch.empty, (M, H), dtype=torch.bfloat16)
     _need(out, "out", shape=(M, H))
     if residual is not None:
         _need(residual, "residual", shape=(M, H))
@@ -354,7 +354,7 @@ def moe_decode_latent(x, Wrl, W13, W2, Wup, Ws13, Ws2, topk, out=None, topk_idx=
         _need(Ws13, "Ws13", shape=(2 * I, H))
         _need(Ws2, "Ws2", shape=(H, I))
     if out is None:
-        out = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+        out = _made(stream, x.device, torch.empty, (M, H), dtype=torch.bfloat16)
     _need(out, "out", shape=(M, H))
     if residual is not None:
         _need(residual, "residual", shape=(M, H))
@@ -389,7 +389,7 @@ def dec_add(a, b, out=None, stream=None):
     _need(a, "a")
     _need(b, "b", shape=a.shape)
     if out is None:
-        out = torch.empty_like(a)
+        out = _made(stream, a.device, torch.empty_like, a)
     _need(out, "out", shape=a.shape)
     _on_one_gpu(a=a, b=b, out=out)
     _check(lib().dec_add(_ptr(a), _ptr(b), _ptr(out), a.numel(), _stream(stream)), "dec_add")

@@ -17,7 +17,7 @@ from __future__ import annotations
 import ctypes
 import operator
 
-from . import REGIME_NAMES, _check, lib
+from . import REGIME_NAMES, _check, _made, lib
 
 _I32, _I64, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 
@@ -98,6 +98,12 @@ class _Handle:
         self.device, self._index = device, device.index
         self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
         self._empty, self._current = torch.empty, torch._C._cuda_getCurrentRawStream
+
+    def _new(self, shape, stream):
+        """A bf16 tensor for a call on ``stream``."""
+        if stream is None:
+            return self._empty(shape, dtype=self._bf16, device=self.device)
+        return _made(stream, self.device, self._empty, shape, dtype=self._bf16)
 
     def _stream(self, stream):
         return self._current(self._index) if stream is None else stream.cuda_stream
@@ -249,7 +255,7 @@ def kv_append(qkv, kv, rope, wq=None, wk=None, eps=1e-6, q=None, positions=None,
         _list("positions", kv, positions, kv._i32, T)
         pos = positions.data_ptr()
     if q is None:
-        q = kv._empty((T, hq * dim), dtype=bf, device=kv.device)
+        q = kv._new((T, hq * dim), stream)
         ldq = hq * dim
     else:
         rows, cols, ldq = _rows("q", kv, q, bf)
@@ -276,7 +282,7 @@ def kv_attention(q, kv, out=None, lse=None, scale=None, window=0, stream=None):
         raise ValueError("q: expected [T, Hq*%d] with Hq a multiple of %d, got shape %s"
                          % (dim, kv.heads, tuple(q.shape)))
     if out is None:
-        out = kv._empty((T, width), dtype=bf, device=kv.device)
+        out = kv._new((T, width), stream)
         ldo = width
     else:
         rows, cols, ldo = _rows("out", kv, out, bf)

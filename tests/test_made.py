@@ -109,3 +109,57 @@ def test_the_norm_and_the_projections_make_theirs_there(monkeypatch, call):
         w4.dec_quant_w4(x, stream=s.side)
     assert launched == [7] and s.now is s.main
     assert len(made) == {"norm_mx": 3, "linear": 1}.get(call, 2)
+
+
+def _operand(shape, dtype, strides=None):
+    t = _fake(shape, dtype, strides)
+    t.dim = lambda: len(shape)
+    t.numel = lambda: int(torch.Size(shape).numel())
+    return t
+
+
+@pytest.mark.parametrize("call", ["linear", "splitk", "moe", "latent", "add", "append", "attention"])
+def test_the_other_calls_make_theirs_there(monkeypatch, call):
+    from moe_decode_gemm_gb300 import paged
+
+    s = Streams(monkeypatch)
+    bf, f32, made, launched = torch.bfloat16, torch.float32, [], []
+
+    def empty(shape, dtype=None, device=None):
+        assert s.now is s.side
+        t = _operand(shape if isinstance(shape, (tuple, torch.Size)) else shape.shape, dtype or bf)
+        t.record_stream = made.append
+        return t
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: launched.append(name) or 0
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "empty_like", empty)
+    monkeypatch.setattr(dg, "_need", lambda t, *a, **k: t)
+    for module in (dg, paged):
+        monkeypatch.setattr(module, "lib", lambda: Lib())
+    x, W = _operand((4, 64), bf), _operand((16, 64), bf)
+    if call == "linear":
+        dg.dec_linear(x, W, stream=s.side)
+    elif call == "splitk":
+        dg.dec_linear_splitk(x, W, 1, stream=s.side)
+    elif call == "moe":
+        dg.moe_decode(x, _operand((8, 64), bf), _operand((8, 32, 64), bf, (2048, 64, 1)),
+                      _operand((8, 64, 16), bf, (1024, 16, 1)), None, None, 2, stream=s.side)
+    elif call == "latent":
+        dg.moe_decode_latent(x, _operand((40, 64), bf), _operand((8, 32, 32), bf, (1024, 32, 1)),
+                             _operand((8, 32, 16), bf, (512, 16, 1)), _operand((64, 32), bf), None, None, 2,
+                             stream=s.side)
+    elif call == "add":
+        dg.dec_add(x, x, stream=s.side)
+    else:
+        kv = paged._Handle()
+        kv.device, kv._index, kv._bf16, kv._f32, kv._empty = CUDA, 0, bf, f32, empty
+        kv.dim, kv.heads, kv._ref = 16, 1, None
+        if call == "append":
+            dg.kv_append(x, kv, _operand((9, 16), f32), stream=s.side)
+        else:
+            dg.kv_attention(x, kv, stream=s.side)
+    assert len(launched) == 1 and made == [s.main] and s.now is s.main
