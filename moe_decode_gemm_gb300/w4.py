@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _check, _made, lib
-from .paged import _Handle
+from .paged import _Handle, _int32
 
 _handles = {}
 
@@ -67,6 +67,9 @@ def _explain(what, t, dtype, shape, align):
         raise ValueError("%s: expected shape [%s], got %s"
                          % (what, ", ".join("any" if n is None else str(n) for n in shape),
                             tuple(t.shape)))
+    for n in t.shape:
+        if n >> 31:
+            raise ValueError("%s: %d does not fit 32 bits" % (what, n))
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("%s: needs unit column stride" % what)
     if t.dim() == 2 and t.shape[0] > 1:
@@ -133,7 +136,7 @@ class W4:
     def __init__(self, q, s, n, k):
         import torch
 
-        n, k = int(n), int(k)
+        n, k = _int32("n", int(n)), _int32("k", int(k))
         if n < 1 or k < 8 or k % 8:
             raise ValueError("W4: expected n >= 1 and k a multiple of 8, got %d, %d" % (n, k))
         nt, kc = -(-n // 128), -(-k // 128)
@@ -205,7 +208,7 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         bf = b._bf16
         if T < 2:
             ldx = H  # a single row's stride says nothing
-        ok = (x.dtype is bf and one == 1 and ldx % 8 == 0 and ldx >= H and w.dtype is bf
+        ok = (x.dtype is bf and one == 1 and ldx % 8 == 0 and ldx >= H and not (T | H) >> 31 and w.dtype is bf
               and w.get_device() == index and w.shape == (H,) and w.is_contiguous())
     except (AttributeError, TypeError, ValueError):
         ok = False
@@ -309,7 +312,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
         bf = b._bf16
         if mx:
             M, k = x.shape
-            ok = x._index == index and k == K
+            ok = x._index == index and k == K and not M >> 31
         else:
             try:
                 M, k = x.shape
@@ -317,7 +320,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
                 if M < 2:
                     ld = K  # a single row's stride says nothing
                 ok = (k == K and x.dtype is bf and x.get_device() == index and one == 1 and ld % 8 == 0
-                      and ld >= K)
+                      and ld >= K and not M >> 31)
             except (AttributeError, ValueError):
                 ok = False
     if ok and y is not None:
@@ -331,6 +334,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
         if mx:
             if x.shape[1] != K:
                 raise ValueError("x: expected shape [any, %d], got %s" % (K, tuple(x.shape)))
+            _int32("x", x.shape[0])
             xt, dt, al = x.q, torch.float8_e4m3fn, 16
         else:
             _explain("x", x, bf, (None, K), 8)
@@ -379,7 +383,7 @@ def dec_quant_w4(W, out=None, stream=None):
         index = W.get_device()
         b = _handles.get(index) or _bound(index) if index >= 0 else None
         ld = _is_matrix(W, b._bf16, index, N, K)
-        ok = ld and ld % 8 == 0 and N >= 1 and K >= 8 and K % 8 == 0
+        ok = ld and ld % 8 == 0 and N >= 1 and K >= 8 and K % 8 == 0 and not (N | K) >> 31
     except (AttributeError, ValueError):
         ok = False
     if not ok:
