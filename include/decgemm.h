@@ -504,7 +504,7 @@ int kv_compact(const dec_kv_pool* pool, void* stream);
  *
  * The sum of squares is that of the rounded h, in fp32; y is fp32 rounded once.
  * h may be x or res, and y may be x or res, with the same row stride (y not h).
- * Otherwise outputs overlap nothing. Errors: DEC_EINVAL, DEC_EUNSUPPORTED (H),
+ * Otherwise outputs overlap nothing (outputs that begin where an operand does are refused). Errors: DEC_EINVAL, DEC_EUNSUPPORTED (H),
  * DEC_ECUDA.
  *
  * dec_rmsnorm_mx -- the same y in 8 bits: q [rows, H] e4m3 (rows ldq apart, a
@@ -543,7 +543,8 @@ int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K
  *
  *   x    : [M, K] bf16, rows ldx elements apart (at least K, a multiple of 8);
  *          1 <= M <= 64, K a multiple of 8
- *   res, y : [M, N] bf16; y may be res
+ *   res, y : [M, N] bf16; y may be res. Otherwise y and work overlap nothing (refused where
+ *          they begin where another operand does)
  *   work : dec_linear_w4_work(M, K) bytes of device memory, 16-byte aligned, that the
  *          call may write until its kernels end; NULL where that is 0 (M <= 16). The
  *          library's own workspace is not used: calls with work spaces of their own

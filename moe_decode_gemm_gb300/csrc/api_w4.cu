@@ -27,6 +27,16 @@ static int norm(NormCall c, void* stream) {
   if (c.y && (c.ldy < c.H || c.ldy % 8 || c.y == c.h)) return DEC_EINVAL;
   if (c.q && (!c.sc || c.ldq < c.H || c.ldq % 16 || c.ldsc < c.H / 32)) return DEC_EINVAL;
   if (c.H > kNormMaxWidth) return DEC_EUNSUPPORTED;
+  // In place row by row only: other rows would be written before they are read.
+  auto in_place = [&](const void* out, long long ld, const void* in, long long ldin) {
+    return out && out == in && c.rows > 1 && ld != ldin;
+  };
+  if (in_place(c.h, c.ldh, c.x, c.ldx) || in_place(c.h, c.ldh, c.res, c.ldres) ||
+      in_place(c.y, c.ldy, c.x, c.ldx) || in_place(c.y, c.ldy, c.res, c.ldres))
+    return DEC_EINVAL;
+  if (c.h == c.w || c.y == c.w) return DEC_EINVAL;
+  for (const void* p : {c.x, c.res, c.w, static_cast<const void*>(c.h)})
+    if (c.q && (c.q == p || c.sc == p || c.q == c.sc)) return DEC_EINVAL;
   Ctx cx;
   if (int rc = kv_context(stream, 0, 0, &cx, nullptr, nullptr)) return rc;
   return result(launch_norm(cx, c));
@@ -40,6 +50,9 @@ static int linear(const W4Call& c, void* stream) {
   if (c.M > 64 || !w4_fits(c.N, c.K)) return DEC_EUNSUPPORTED;
   const bool work = !c.xs && w4_work_bytes(c.M, c.K) > 0;
   if (work && (!c.work || !al(c.work, 16))) return DEC_EINVAL;
+  // Outputs are written while other CTAs still read tokens, the work space before that.
+  if (c.y == c.x || c.y == c.xs || (work && (c.work == c.x || c.work == c.y || c.work == c.res)))
+    return DEC_EINVAL;
   Ctx cx;
   if (int rc = kv_context(stream, 0, 0, &cx, nullptr, nullptr)) return rc;
   return result(launch_w4_linear(cx, c), work ? 2 : 1);
