@@ -8,12 +8,13 @@ What a decode layer does around its attention and its experts:
   dec_quant_w4     bf16 weights as W4, once, when a model is loaded
 
 W4 and MX8 hold blocks of 32 numbers with a shared power of two (the OCP
-microscaling formats MXFP4 and MXFP8). They check their tensors once and keep
-them alive.
+microscaling formats MXFP4 and MXFP8). They check their tensors once, keep them
+alive and do not change them for others; a tensor that was given other memory
+(``t.data = ...``) is looked over anew by the next call.
 """
 from __future__ import annotations
 
-import ctypes
+import operator
 
 from . import _check, _made, lib
 from .paged import _Handle, _int32
@@ -115,10 +116,21 @@ class MX8:
         _explain("s", s, e8, (T, H // 32), 1)
         if q.device != s.device:
             raise ValueError("s: on %s, the other operands on %s" % (s.device, q.device))
-        self.q, self.s = q, s
-        self.shape, self._index = q.shape, q.get_device()
-        self._args = (q.data_ptr(), q.stride(0) if T > 1 else H, s.data_ptr(),
-                      s.stride(0) if T > 1 else H // 32)
+        self._set(q, s, q.shape, q.get_device(), q.stride(0) if T > 1 else H, s.stride(0) if T > 1 else H // 32)
+
+    def _set(self, q, s, shape, index, ldq, lds):
+        self._q, self._s, self._shape, self._index = q, s, shape, index
+        self._args = (q.data_ptr(), ldq, s.data_ptr(), lds)
+        return self
+
+    q, s, shape = (property(operator.attrgetter(name)) for name in ("_q", "_s", "_shape"))
+
+    def _at(self):
+        """What the C ABI is given of it."""
+        a = self._args
+        if self._q.data_ptr() != a[0] or self._s.data_ptr() != a[2]:
+            self.__init__(self._q, self._s)
+        return self._args
 
 
 class W4:
@@ -149,10 +161,19 @@ class W4:
         self._set(q, s, n, k)
 
     def _set(self, q, s, n, k):
-        self.q, self.s, self.n, self.k = q, s, n, k
+        self._q, self._s, self._n, self._k = q, s, n, k
         self._index = q.get_device()
         self._args = (q.data_ptr(), s.data_ptr())
         return self
+
+    q, s, n, k = (property(operator.attrgetter(name)) for name in ("_q", "_s", "_n", "_k"))
+
+    def _at(self):
+        """What the C ABI is given of it."""
+        a = self._args
+        if self._q.data_ptr() != a[0] or self._s.data_ptr() != a[1]:
+            self.__init__(self._q, self._s, self._n, self._k)
+        return self._args
 
     @staticmethod
     def empty(n, k, device="cuda"):
@@ -231,7 +252,8 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         if mx:
             if type(out) is not MX8:
                 raise TypeError("out: expected an MX8, got %s" % type(out).__name__)
-            if out._index != index or out.shape != shape:
+            at = out._at()
+            if out._index != index or out._shape != shape:
                 raise ValueError("out: expected shape %s on %s, got %s on %s"
                                  % ((T, H), x.device, tuple(out.shape), out.q.device))
         else:
@@ -251,11 +273,10 @@ def _norm(what, mx, x, w, residual, h, out, eps, stream):
         if out is None:
             q = _new(b, (T, H), b._f8, stream)
             s = _new(b, (T, H // 32), b._e8, stream)
-            out = MX8.__new__(MX8)
-            out.q, out.s, out.shape, out._index = q, s, x.shape, index
-            out._args = (q.data_ptr(), H, s.data_ptr(), H // 32)
+            out = MX8.__new__(MX8)._set(q, s, x.shape, index, H, H // 32)
+            at = out._args
         fn = lib().dec_rmsnorm_mx
-        args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, *out._args, T, H)
+        args = (x.data_ptr(), ldx, rp, ldr, w.data_ptr(), eps, hp, ldh, *at, T, H)
     else:
         if out is None:
             out = _rows_of(b, x, ldx, stream)
@@ -304,14 +325,16 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
     """
     if not isinstance(W, W4):
         raise TypeError("W: expected a W4, got %s" % type(W).__name__)
-    index, N, K = W._index, W.n, W.k
+    wat = W._at()
+    index, N, K = W._index, W._n, W._k
     mx = type(x) is MX8
     ok = index >= 0
     if ok:
         b = _handles.get(index) or _bound(index)
         bf = b._bf16
         if mx:
-            M, k = x.shape
+            xat = x._at()
+            M, k = x._shape
             ok = x._index == index and k == K and not M >> 31
         else:
             try:
@@ -353,7 +376,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
         L = lib()
         rp = None if residual is None else residual.data_ptr()
         if mx:
-            fn, args = L.dec_linear_w4_mx, (*x._args, *W._args, rp, y.data_ptr(), M, N, K)
+            fn, args = L.dec_linear_w4_mx, (*xat, *wat, rp, y.data_ptr(), M, N, K)
         else:
             wp = None
             if M > 16:
@@ -361,7 +384,7 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
                 if n:
                     work = _new(b, n, b._u8, stream, seen=False)
                     wp = work.data_ptr()
-            fn, args = L.dec_linear_w4, (x.data_ptr(), ld, *W._args, rp, y.data_ptr(), M, N, K, wp)
+            fn, args = L.dec_linear_w4, (x.data_ptr(), ld, *wat, rp, y.data_ptr(), M, N, K, wp)
         if b._getdev() == index:
             rc = fn(*args, b._current(index) if stream is None else stream.cuda_stream)
         else:
@@ -400,7 +423,7 @@ def dec_quant_w4(W, out=None, stream=None):
                                   _new(b, (nt, kc, 32, 4, 4), b._u8, stream), N, K)
     elif type(out) is not W4:
         raise TypeError("out: expected a W4, got %s" % type(out).__name__)
-    elif (out.n, out.k) != (N, K):
+    elif out._at() and (out.n, out.k) != (N, K):
         raise ValueError("out: expected a W4 of %d x %d, got %d x %d" % (N, K, out.n, out.k))
     elif out._index != index:
         raise ValueError("out: on %s, the other operands on %s" % (out.q.device, W.device))
