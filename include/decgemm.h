@@ -502,7 +502,8 @@ int kv_compact(const dec_kv_pool* pool, void* stream);
  *          least H and a multiple of 8); h is written with res only
  *   w    : [H] bf16;  H a multiple of 8, at most 65536;  eps >= 0
  *
- * The sum of squares is that of the rounded h, in fp32; y is fp32 rounded once.
+ * The sum of squares is that of the rounded h, in fp32 (past its range the root is 0,
+ * and y of finite h too); y is fp32 rounded once.
  * h may be x or res, and y may be x or res, with the same row stride (y not h).
  * Otherwise outputs overlap nothing (outputs that begin where an operand does are refused). Errors: DEC_EINVAL, DEC_EUNSUPPORTED (H),
  * DEC_ECUDA.

@@ -97,7 +97,8 @@ __device__ __forceinline__ float most_of(float a, float b, float c) {
   return y;
 }
 
-// The products of eight pairs of bf16 (each exact) with f, to fp32.
+// The products of eight pairs of bf16 with f, to fp32. (Those of the pairs are exact as
+// long as fp32 holds them; norm_e4m3 sees to the others.)
 __device__ __forceinline__ void times_root(const uint4& h, const uint4& w, Two f, float2 (&y)[4]) {
   const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -109,19 +110,24 @@ __device__ __forceinline__ void times_root(const uint4& h, const uint4& w, Two f
 
 // The same product, where it is not exact to the neighbour with an odd last bit, so that
 // a rounding of it to fewer bits sees on which side of a border the product lies. (A rest
-// of 2^-40 is the root's own error: the product is y.)
-__device__ __forceinline__ float to_odd(float y, float x, float g, Two f) {
-  const float p = x * g, r = fmaf(p, f.hi, -y) + p * f.lo;
+// of 2^-40 is the root's own error: the product is y.) The root's power of two, f's, is
+// 2^k and taken apart: it goes to the smaller of x and g where it is 1 or more, else to
+// the larger, so that x g f alone says whether fp32 holds what comes before it.
+__device__ __forceinline__ float to_odd(float x, float g, Two f, int k) {
+  const bool swap = (fabsf(x) < fabsf(g)) == (k < 0);
+  const float p = (swap ? g : x) * pow2_f(k) * (swap ? x : g);
+  const float y = fmaf(p, f.hi, p * f.lo), r = fmaf(p, f.hi, -y) + p * f.lo;
   uint32_t b = __float_as_uint(y);
   if (!(b & 1) && fabsf(r) > fabsf(y) * 0x1p-40f) b += (r > 0.f) == (y > 0.f) ? 1u : ~0u;
   return __uint_as_float(b);
 }
 __device__ __forceinline__ void to_odd(const uint4& h, const uint4& w, Two f, float2 (&y)[4]) {
   const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, ww[4] = {w.x, w.y, w.z, w.w};
+  const int k = min(max((int)(__float_as_uint(f.hi) >> 23) - 127, -126), 126);
+  const Two g = {f.hi * pow2_f(-k), f.lo * pow2_f(-k)};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    y[j] = make_float2(to_odd(y[j].x, bf16lo(hw[j]), bf16lo(ww[j]), f),
-                       to_odd(y[j].y, bf16hi(hw[j]), bf16hi(ww[j]), f));
+    y[j] = make_float2(to_odd(bf16lo(hw[j]), bf16lo(ww[j]), g, k), to_odd(bf16hi(hw[j]), bf16hi(ww[j]), g, k));
 }
 
 // The largest magnitude (its bits) of the 32 values that four lanes hold.
@@ -151,22 +157,24 @@ __device__ __forceinline__ uint2 to_e4m3(const float2 (&y)[4], float s) {
 // Eight values of a group of 32 (four lanes) in 8 bits, and the group's scale byte.
 // fp32 products are off by half a step: where 2^-22 more and 2^-22 less are the same
 // e4m3, so is the product. Otherwise (one warp in 700), where the largest is just what
-// a scale can hold, or where products are below 2^-100 and might not be as near as that,
-// the warp rounds them anew from their odd neighbours.
+// a scale can hold or not finite, or where products of pairs might be below fp32's
+// normal numbers (the largest y below 2^-90, of which the least e4m3 is 2^-19, or a root
+// above 2^12; below that a product that fp32 takes for 0 is 0 in 8 bits too), the warp
+// rounds them anew from their odd neighbours.
 __device__ __forceinline__ uint2 norm_e4m3(const uint4& h, const uint4& w, Two f, int* byte) {
   float2 y[4];
   times_root(h, w, f, y);
   uint32_t m = group_most(y);
   uint2 q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);  // NaN, as the scale
   *byte = 255;
-  bool near = false;
+  bool near = true;
   if (!not_finite(__uint_as_float(m))) {
     const int e = group_exponent(m);
     const float s = pow2_f(-e);
     q = to_e4m3(y, s * (1.f + 0x1p-22f));
     const uint2 less = to_e4m3(y, s * (1.f - 0x1p-22f));
     *byte = e + 127;
-    near = q.x != less.x || q.y != less.y || (m & 0x7FFFFFu) == 0x600000u || m - 1u < 27u << 23;
+    near = q.x != less.x || q.y != less.y || (m & 0x7FFFFFu) == 0x600000u || m - 1u < 37u << 23 || f.hi > 0x1p12f;
   }
   if (__any_sync(0xffffffffu, near)) {
     to_odd(h, w, f, y);
