@@ -547,7 +547,8 @@ int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K
  *   res, y : [M, N] bf16; y may be res. Otherwise y and work overlap nothing (refused where
  *          they begin where another operand does)
  *   work : dec_linear_w4_work(M, K) bytes of device memory, 16-byte aligned, that the
- *          call may write until its kernels end; NULL where that is 0 (M <= 16). The
+ *          call may write until its kernels end; NULL where that is 0 (M <= 16, and
+ *          what is refused). The
  *          library's own workspace is not used: calls with work spaces of their own
  *          may run at once.
  *

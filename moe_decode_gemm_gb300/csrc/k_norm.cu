@@ -292,7 +292,7 @@ __global__ void __maxnreg__(WARP ? 80 : VPT > 4 ? 64 : 48) norm_kernel(const Nor
 
 template <int VPT, bool WARP>
 static cudaError_t run_norm(const Ctx& cx, const NormArgs& a, int threads) {
-  const unsigned grid = WARP ? (unsigned)((a.rows + kNormWarps - 1) / kNormWarps) : (unsigned)a.rows;
+  const unsigned grid = WARP ? (unsigned)((a.rows - 1) / kNormWarps + 1) : (unsigned)a.rows;
   return a.q ? launch_k(norm_kernel<VPT, true, WARP>, dim3(grid), dim3(threads), 0, cx.stream, cx.pdl, a)
              : launch_k(norm_kernel<VPT, false, WARP>, dim3(grid), dim3(threads), 0, cx.stream, cx.pdl, a);
 }

@@ -731,7 +731,7 @@ static cudaError_t run_w4(const Ctx& cx, const W4Call& c) {
 constexpr int kW4Convert = 16;
 
 size_t w4_work_bytes(int M, int K) {
-  if (M <= kW4Convert) return 0;
+  if (M <= kW4Convert || K > kW4MaxK) return 0;
   const int mt = M <= 32 ? 32 : 64, pairs = ((K + kW4Tile - 1) / kW4Tile + kPair - 1) / kPair;
   return (size_t)pairs * (kPair * 2 * mt * 128 + 1024);
 }

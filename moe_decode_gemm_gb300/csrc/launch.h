@@ -260,8 +260,9 @@ bool make_tmap_bytes(CUtensorMap* map, const void* x, uint64_t rows, uint64_t co
                      uint32_t box_rows);
 
 // Whether the rows of the units of N x K weights, and places along K, fit 32 bits.
+constexpr int kW4MaxK = 1 << 29;
 inline bool w4_fits(int N, int K) {
-  return K <= (1 << 29) && ((int64_t)N + 127) / 128 * (((int64_t)K + 127) / 128) <= (INT32_MAX / 128);
+  return K <= kW4MaxK && ((int64_t)N + 127) / 128 * (((int64_t)K + 127) / 128) <= (INT32_MAX / 128);
 }
 
 struct W4Call {

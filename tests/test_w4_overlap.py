@@ -48,3 +48,9 @@ def test_through_the_binding(L):
     W = dg.dec_quant_w4(torch.zeros((64, 64), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(dg.DecError):
         dg.dec_linear_w4(x, W, y=x)
+
+
+@pytest.mark.parametrize("M,K", [(64, 2 ** 31 - 8), (17, 2 ** 29 + 8), (64, 2 ** 31 - 1)])
+def test_no_work_space_for_what_is_refused(L, M, K):
+    assert L.dec_linear_w4_work(M, K) == 0
+    assert L.dec_linear_w4_work(M, 2 ** 29) > 2 * M * 2 ** 29
