@@ -553,8 +553,10 @@ int dec_quant_w4(const void* W, int64_t ldw, void* q, void* scales, int N, int K
  *          may run at once.
  *
  * The tensor cores take 4-bit weights with 8-bit tokens. A bf16 token value enters
- * as the sum of two e4m3 numbers, each with a scale for 32 k: exact down to 2^-15
- * of the largest magnitude of its 32, off by at most 2^-22 of that magnitude below.
+ * as the sum of two e4m3 numbers, each with a scale for 32 k. With 2^e the least power of
+ * two that brings the largest magnitude of the 32 to 448 or less (e at least -123), values
+ * of at least 2^(e-6) are exact, those below off by at most 2^(e-14): 2^-13.8 and 2^-21.8
+ * of the largest magnitude, where it is just above 224 * 2^e.
  * Products are exact, sums fp32, in an order that does not change from run to
  * run; y is rounded once. A token with a value that is not finite gives NaN in
  * all its outputs. W is read while the previous kernel of the stream may still run, as

@@ -14,8 +14,9 @@
 // bf16 tokens enter as two e4m3 numbers, hi + lo, with a scale each per 32 k:
 // a bf16 has 8 significant bits, an e4m3 has 4. With u = x / 2^e, e the least
 // exponent that brings the group's largest to 448 or less, hi = e4m3(u) and
-// lo = e4m3(16 (u - hi)): the sum is x exactly down to 2^-15 of the group's
-// largest value and off by at most 2^-22 of it below. The MMA treats them as
+// lo = e4m3(16 (u - hi)), of which the least step is 2^-13 in u: the sum is u exactly
+// from 2^-6 on, and off by at most 2^-14 below; the group's largest is above 224, so
+// 2^-13.8 and 2^-21.8 of it. The MMA treats them as
 // twice as many tokens; fp32 sums of the two halves are added at the end.
 //
 // A unit of work is 128 weight rows x 128 k (8 KB of weights and 512 B of scales,

@@ -318,8 +318,8 @@ def dec_linear_w4(x, W, y=None, residual=None, stream=None):
     x: [M, K] bf16 (rows may be further apart than K, a multiple of 8 elements)
     or MX8, M <= 64. W: W4. y, residual: [M, N] bf16 contiguous; y may be residual,
     not x. fp32 sums, one rounding. bf16 tokens are taken as two 8-bit numbers
-    each: exact for values down to 2^-15 of the largest of their 32 (aligned) k,
-    off by at most 2^-22 of the largest below. A token with a value that is not
+    each: exact for values down to 2^-13.8 of the largest of their 32 (aligned) k,
+    off by at most 2^-21.8 of the largest below. A token with a value that is not
     finite gives NaN in all its outputs. More than 16 bf16 tokens take a work space
     from torch's allocator for the call.
     """
