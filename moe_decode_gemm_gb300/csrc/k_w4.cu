@@ -713,7 +713,7 @@ static cudaError_t run_w4(const Ctx& cx, const W4Call& c) {
   xmap = wmap;
   if (MODE == W4_MX && !make_tmap_bytes(&xmap, c.x, (uint64_t)c.M, (uint64_t)c.K, (uint64_t)c.ldx, (uint32_t)MT))
     return cudaErrorInvalidValue;
-  if (MODE == W4_READY) {
+  if constexpr (MODE == W4_READY) {
     const int items = pairs * c.M, per = kReadyThreads / 32;
     if (cudaError_t e = launch_k(w4_tokens_kernel<MT>, dim3((unsigned)((items + per - 1) / per)), dim3(kReadyThreads),
                                  0, cx.stream, cx.pdl, static_cast<const uint16_t*>(c.x), c.ldx,
