@@ -840,9 +840,8 @@ cudaError_t launch_w4_quant(const Ctx& cx, const void* W, long long ldw, void* q
   const int tiles = (N + kW4Tile - 1) / kW4Tile, KC = (K + kW4Tile - 1) / kW4Tile;
   // No early start of what follows (a projection reads weights before it waits for
   // the kernel before it): this kernel never lets its dependents launch.
-  w4_quant_kernel<<<(unsigned)((long long)tiles * KC), kQuantThreads, 0, cx.stream>>>(
-      static_cast<const uint16_t*>(W), ldw, static_cast<uint8_t*>(q), static_cast<uint8_t*>(s), N, K, KC);
-  return cudaGetLastError();
+  return launch_k(w4_quant_kernel, dim3((unsigned)((long long)tiles * KC)), dim3(kQuantThreads), 0, cx.stream, false,
+                  static_cast<const uint16_t*>(W), ldw, static_cast<uint8_t*>(q), static_cast<uint8_t*>(s), N, K, KC);
 }
 
 }  // namespace dg
