@@ -16,9 +16,9 @@
 // are rounded from what is exact.
 //
 // GB300, us (in brackets the bytes at the measured copy rate): 8000 x 7168 with
-// residual 67.4 (67.7), in 8 bits 66.6 (59.5: instructions); 64 x 7168 2.3 and 3.0
-// (latency); 3001 x 2048 5.7 (3.6) and 7.8 (2.8: one wave, load, sum, output one after
-// another). In 8 bits with every product in two numbers 73, 3.5 and 8.9.
+// residual 67.2 (67.7), in 8 bits 66.3 (59.5: instructions, issue slots 76 % busy); 64 x
+// 7168 2.5 and 2.9 (latency); 3001 x 2048 in 8 bits 7.7 (2.8: one wave, load, sum, output
+// one after another). In 8 bits with every product in two numbers 73, 3.5 and 8.9.
 #include "launch.h"
 #include "launch_util.cuh"
 #include "mx_common.cuh"

@@ -30,8 +30,8 @@
 // accumulators.
 //
 // GB300, us on the GPU (in brackets the weights' bytes at the measured copy rate):
-// 7168 x 7168 with 1 / 16 / 64 tokens 7.7 / 8.4 / 12.8 (4.0), 16384 x 7168 12.1 / 13.4 /
-// 19.3 (9.2), 64 tokens in 8 bits 9.4 and 15.3. About 3.5 us are start and end (first
+// 7168 x 7168 with 1 / 16 / 64 tokens 7.6 / 8.3 / 12.9 (4.0), 16384 x 7168 11.8 / 13.4 /
+// 19.5 (9.2), 64 tokens in 8 bits 9.4 and 15.2. About 3.5 us are start and end (first
 // copies, conversion, exchange, output); 64 bf16 tokens with one tile are bound by
 // the 64 bytes a clock that an SM takes in, 34 KB of tokens for 17 KB of weights.
 #include <atomic>
