@@ -92,3 +92,22 @@ def test_an_output_is_not_written_anew_while_it_is_read(calls, name):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, want))
     assert all(torch.equal(a, b) for a, b in zip(more, want)) and len(again) == 4 * len(want)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_captured_on_a_stream_beside_the_capturing_one(calls, name):
+    """The call's tensors are of the graph's own memory, and each replay writes them."""
+    call = calls[name]
+    want = [t.clone() for t in _flat(call(None))]
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for t in _flat(got):
+            t.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(_flat(got), want))
